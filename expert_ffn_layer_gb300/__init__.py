@@ -11,6 +11,10 @@ Function names follow the C ABI:
     moe_fused_moe (routing given, stacked [E, 2I, H] gate/up weights),
     moe_quantize_fp8_rows, moe_expert_ffn_fp8, moe_layer_forward_fp8 (FP8 E4M3
     expert weights, one scale per row; see Fp8Experts / quantize_fp8_experts),
+    moe_quantize_mxfp4_rows, moe_dequantize_mxfp4_rows, moe_expert_ffn_mxfp4,
+    moe_layer_forward_mxfp4 (MXFP4 expert weights; see Mxfp4Experts /
+    quantize_mxfp4_experts / pack_mxfp4), moe_layer_forward_few (at most 32
+    tokens, the whole layer in one kernel),
     moe_workspace_bytes, moe_ws_init, moe_ws_read_error, moe_check_dims
 
 Tensors are torch tensors on the current CUDA device: bf16 activations and
@@ -36,7 +40,8 @@ EXPORTS = ("moe_status_string", "moe_check_dims", "moe_workspace_bytes", "moe_ws
            "moe_route", "moe_permute", "moe_expert_ffn", "moe_expert_gate_up", "moe_expert_down", "moe_combine",
            "moe_layer_forward", "moe_fused_moe", "moe_expert_ffn_noalloc", "moe_selftest_wait_timeout",
            "moe_selftest_silu", "moe_quantize_fp8_rows", "moe_expert_ffn_fp8", "moe_layer_forward_fp8",
-           "moe_expert_ffn_w8a8", "moe_layer_forward_w8a8")
+           "moe_expert_ffn_w8a8", "moe_layer_forward_w8a8", "moe_quantize_mxfp4_rows", "moe_dequantize_mxfp4_rows",
+           "moe_expert_ffn_mxfp4", "moe_layer_forward_mxfp4", "moe_layer_forward_few")
 
 
 class MoeError(RuntimeError):
@@ -58,6 +63,10 @@ class MoeFp8Experts(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("gate", "up", "down", "gate_scale", "up_scale", "down_scale",
                                                 "s_gate", "s_up", "s_down", "s_gate_scale", "s_up_scale",
                                                 "s_down_scale")]
+
+
+class MoeMxfp4Experts(ctypes.Structure):
+    _fields_ = list(MoeFp8Experts._fields_)
 
 
 _lib = None
@@ -98,6 +107,11 @@ def load() -> ctypes.CDLL:
         "moe_layer_forward_fp8": (st, [D, P, P, P, ctypes.POINTER(MoeFp8Experts), P, P, C, P]),
         "moe_expert_ffn_w8a8": (st, [D, P, P, P, ctypes.POINTER(MoeFp8Experts), P, P, P, C, P]),
         "moe_layer_forward_w8a8": (st, [D, P, P, P, ctypes.POINTER(MoeFp8Experts), P, P, C, P]),
+        "moe_quantize_mxfp4_rows": (st, [P, ctypes.c_int64, ctypes.c_int, P, P, P]),
+        "moe_dequantize_mxfp4_rows": (st, [P, P, ctypes.c_int64, ctypes.c_int, P, P]),
+        "moe_expert_ffn_mxfp4": (st, [D, P, P, P, ctypes.POINTER(MoeMxfp4Experts), P, P, P, C, P]),
+        "moe_layer_forward_mxfp4": (st, [D, P, P, P, ctypes.POINTER(MoeMxfp4Experts), P, P, C, P]),
+        "moe_layer_forward_few": (st, [D, P, P, P, P, P, P, P, P, P, P, P, C, P]),
         "moe_selftest_wait_timeout": (st, [P, C, ctypes.c_ulonglong, P]),
         "moe_selftest_silu": (st, [P, P, P, ctypes.c_int64, P]),
     }
@@ -391,6 +405,123 @@ def moe_layer_forward_w8a8(d: MoeDims, hidden, router_w, expert_bias, w: Fp8Expe
     _check(w.t["gate"][0], torch.uint8, (d.E, d.I, d.H), "gate codes")
     _call("moe_layer_forward_w8a8", ctypes.byref(d), _ptr(hidden), _ptr(router_w), _ptr(expert_bias),
           ctypes.byref(w.struct), _ptr(out), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def moe_quantize_mxfp4_rows(src, codes, scales, stream=None) -> None:
+    """Packed codes [.., C / 2] uint8 and scale bytes [.., C / 32] uint8 of a bf16
+    matrix [.., C] (any leading dims are rows; C a multiple of 128)."""
+    C = src.shape[-1]
+    _check(src, torch.bfloat16, src.shape, "src")
+    _check(codes, torch.uint8, (*src.shape[:-1], C // 2), "codes")
+    _check(scales, torch.uint8, (*src.shape[:-1], C // 32), "scales")
+    _call("moe_quantize_mxfp4_rows", _ptr(src), src.numel() // C if C else 0, C, _ptr(codes), _ptr(scales),
+          _stream(stream))
+
+
+def moe_dequantize_mxfp4_rows(codes, scales, dst, stream=None) -> None:
+    """The bf16 values [.., C] that packed codes and scale bytes stand for."""
+    C = dst.shape[-1]
+    _check(dst, torch.bfloat16, dst.shape, "dst")
+    _check(codes, torch.uint8, (*dst.shape[:-1], C // 2), "codes")
+    _check(scales, torch.uint8, (*dst.shape[:-1], C // 32), "scales")
+    _call("moe_dequantize_mxfp4_rows", _ptr(codes), _ptr(scales), dst.numel() // C if C else 0, C, _ptr(dst),
+          _stream(stream))
+
+
+def pack_mxfp4(codes):
+    """Packed codes of plain ones: uint8 [.., C / 2] with value 2 i in the low and
+    2 i + 1 in the high four bits of byte i, as MXFP4 checkpoints hold them
+    (transposes each 64-byte piece's 4 x 4 words; its own inverse)."""
+    if codes.dtype != torch.uint8 or codes.shape[-1] % 64:
+        raise ValueError("codes: expected uint8 with a last dimension that is a multiple of 64")
+    return codes.reshape(*codes.shape[:-1], -1, 4, 4, 4).transpose(-3, -2).reshape(codes.shape).contiguous()
+
+
+class Mxfp4Experts:
+    """Device tensors of MXFP4 expert weights (packed codes, scale bytes) and the C
+    struct that points at them."""
+
+    NAMES = ("gate", "up", "down", "s_gate", "s_up", "s_down")
+
+    def __init__(self, **tensors):
+        self.t = tensors  # name -> (codes uint8, scales uint8) or None
+        st = MoeMxfp4Experts()
+        for n in self.NAMES:
+            pair = tensors.get(n)
+            setattr(st, n, _ptr(pair[0]) if pair is not None else None)
+            setattr(st, n + "_scale", _ptr(pair[1]) if pair is not None else None)
+        self.struct = st
+
+    def check(self, d: MoeDims) -> None:
+        shapes = {"gate": (d.E, d.I, d.H), "up": (d.E, d.I, d.H), "down": (d.E, d.H, d.I)}
+        if d.has_shared:
+            shapes.update(s_gate=(d.I_shared, d.H), s_up=(d.I_shared, d.H), s_down=(d.H, d.I_shared))
+        for n, (*lead, K) in shapes.items():
+            if self.t.get(n) is None:
+                raise ValueError(f"{n}: missing")
+            _check(self.t[n][0], torch.uint8, (*lead, K // 2), n + " codes")
+            _check(self.t[n][1], torch.uint8, (*lead, K // 32), n + " scales")
+
+
+def quantize_mxfp4_experts(w_gate, w_up, w_down, ws_gate=None, ws_up=None, ws_down=None,
+                           stream=None) -> Mxfp4Experts:
+    """Quantise bf16 expert weights (and the shared expert's, if given) with
+    moe_quantize_mxfp4_rows on the device."""
+    out = {}
+    for n, w in zip(Mxfp4Experts.NAMES, (w_gate, w_up, w_down, ws_gate, ws_up, ws_down)):
+        if w is None:
+            continue
+        codes = torch.empty((*w.shape[:-1], w.shape[-1] // 2), dtype=torch.uint8, device=w.device)
+        scales = torch.empty((*w.shape[:-1], w.shape[-1] // 32), dtype=torch.uint8, device=w.device)
+        moe_quantize_mxfp4_rows(w, codes, scales, stream)
+        out[n] = (codes, scales)
+    return Mxfp4Experts(**out)
+
+
+def moe_expert_ffn_mxfp4(d: MoeDims, hidden, perm, offsets, w: Mxfp4Experts, y_sorted, y_shared, ws,
+                         stream=None) -> None:
+    """The expert FFN with MXFP4 weights; one kernel for at most 32 tokens."""
+    S = d.T * d.top_k
+    _check(hidden, torch.bfloat16, (d.T, d.H), "hidden")
+    _check(perm, torch.int32, (S,), "perm")
+    _check(offsets, torch.int32, (d.E + 1,), "offsets")
+    w.check(d)
+    _check(y_sorted, torch.bfloat16, (S, d.H), "y_sorted")
+    if d.has_shared:
+        _check(y_shared, torch.bfloat16, (d.T, d.H), "y_shared")
+    _call("moe_expert_ffn_mxfp4", ctypes.byref(d), _ptr(hidden), _ptr(perm), _ptr(offsets), ctypes.byref(w.struct),
+          _ptr(y_sorted), _ptr(y_shared), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def moe_layer_forward_mxfp4(d: MoeDims, hidden, router_w, expert_bias, w: Mxfp4Experts, out, ws,
+                            stream=None) -> None:
+    """The layer with MXFP4 expert weights; one kernel for at most 32 tokens."""
+    _check(hidden, torch.bfloat16, (d.T, d.H), "hidden")
+    _check(router_w, torch.float32, (d.E, d.H), "router_w")
+    _check(expert_bias, torch.float32, (d.E,), "expert_bias")
+    w.check(d)
+    _check(out, torch.bfloat16, (d.T, d.H), "out")
+    _call("moe_layer_forward_mxfp4", ctypes.byref(d), _ptr(hidden), _ptr(router_w), _ptr(expert_bias),
+          ctypes.byref(w.struct), _ptr(out), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def moe_layer_forward_few(d: MoeDims, hidden, router_w, expert_bias, w_gate, w_up, w_down, ws_gate, ws_up, ws_down,
+                          out, ws, stream=None) -> None:
+    """moe_layer_forward for at most 32 tokens, as one kernel."""
+    _check(hidden, torch.bfloat16, (d.T, d.H), "hidden")
+    _check(router_w, torch.float32, (d.E, d.H), "router_w")
+    _check(expert_bias, torch.float32, (d.E,), "expert_bias")
+    _check(w_gate, torch.bfloat16, (d.E, d.I, d.H), "w_gate")
+    _check(w_up, torch.bfloat16, (d.E, d.I, d.H), "w_up")
+    _check(w_down, torch.bfloat16, (d.E, d.H, d.I), "w_down")
+    _check(out, torch.bfloat16, (d.T, d.H), "out")
+    if d.has_shared:
+        _check(ws_gate, torch.bfloat16, (d.I_shared, d.H), "ws_gate")
+        _check(ws_up, torch.bfloat16, (d.I_shared, d.H), "ws_up")
+        _check(ws_down, torch.bfloat16, (d.H, d.I_shared), "ws_down")
+    _call("moe_layer_forward_few", ctypes.byref(d), _ptr(hidden), _ptr(router_w), _ptr(expert_bias), _ptr(w_gate),
+          _ptr(w_up), _ptr(w_down), _ptr(ws_gate), _ptr(ws_up), _ptr(ws_down), _ptr(out), _ptr(ws), ws.numel(),
+          _stream(stream))
 
 
 def moe_selftest_wait_timeout(ws: torch.Tensor, limit_ns: int, stream=None) -> None:

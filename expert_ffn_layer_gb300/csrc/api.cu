@@ -3,6 +3,7 @@
 // in the kernels of router.cu, permute.cu, expert_gemm.cu and combine.cu.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -37,6 +38,21 @@ cudaError_t launch_ex(const void *func, dim3 grid, dim3 block, size_t smem, cuda
   }
   cfg.attrs = attrs;
   cfg.numAttrs = (unsigned)n;
+  return cudaLaunchKernelExC(&cfg, func, args);
+}
+
+cudaError_t launch_coop(const void *func, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, void **args) {
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeCooperative;
+  attr.val.cooperative = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelExC(&cfg, func, args);
 }
 
@@ -168,6 +184,32 @@ int router_ksplit(const moe_dims &d, int nsm) {
   return ks;
 }
 
+// The one-kernel layer's pieces, for batches of at most kFewMaxT tokens (they
+// share the workspace with the layout below: no call uses both).
+struct FewWs {
+  size_t logits, x16, x_unscale, act, act_s, amax, y, done, total;
+};
+FewWs few_ws(const moe_dims &d) {
+  FewWs L;
+  size_t off = kWsHeaderBytes;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align256(off + bytes);
+    return o;
+  };
+  const size_t T = (size_t)d.T, S = T * d.top_k, Is = d.has_shared ? (size_t)d.I_shared : 0;
+  L.logits = take(T * (size_t)d.E * 4);
+  L.x16 = take(T * (size_t)d.H * 2);
+  L.x_unscale = take(T * 4);
+  L.act = take(S * (size_t)d.I * 4);
+  L.act_s = take(T * Is * 4);
+  L.amax = take((S + T) * 4);
+  L.y = take((S + T) * (size_t)d.H * 4);
+  L.done = take((size_t)(d.H / 32) * 4);
+  L.total = off;
+  return L;
+}
+
 WsLayout ws_layout(const moe_dims &d) {
   WsLayout L;
   size_t off = 0;
@@ -204,6 +246,7 @@ WsLayout ws_layout(const moe_dims &d) {
   L.asc = take(S * 4);
   L.asc_s = take(T * 4);
   L.total = off;
+  if (d.T <= kFewMaxT) L.total = std::max(L.total, few_ws(d).total);
   return L;
 }
 
@@ -471,6 +514,68 @@ bool fp8_ok(const moe_dims &d, const moe_fp8_experts *q) {
                        !ptr_ok(q->s_up_scale) || !ptr_ok(q->s_down_scale)))
     return false;
   return true;
+}
+
+bool mxfp4_ok(const moe_dims &d, const moe_mxfp4_experts *q) {
+  if (q == nullptr || !ptr_ok(q->gate) || !ptr_ok(q->up) || !ptr_ok(q->down) || !ptr_ok(q->gate_scale) ||
+      !ptr_ok(q->up_scale) || !ptr_ok(q->down_scale))
+    return false;
+  if (d.has_shared && (!ptr_ok(q->s_gate) || !ptr_ok(q->s_up) || !ptr_ok(q->s_down) || !ptr_ok(q->s_gate_scale) ||
+                       !ptr_ok(q->s_up_scale) || !ptr_ok(q->s_down_scale)))
+    return false;
+  return true;
+}
+
+// What the one-kernel layer needs whatever its weights and routing.
+FewParams few_params(const moe_dims &d, const moe_bf16 *hidden, void *ws) {
+  const FewWs L = few_ws(d);
+  FewParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.hidden = reinterpret_cast<const __nv_bfloat16 *>(hidden);
+  p.x = hidden;
+  p.x16 = at<uint16_t>(ws, L.x16);
+  p.x_unscale = at<float>(ws, L.x_unscale);
+  p.logits = at<float>(ws, L.logits);
+  p.act = at<float>(ws, L.act);
+  p.act_s = at<float>(ws, L.act_s);
+  p.amax = at<unsigned>(ws, L.amax);
+  p.y = at<float>(ws, L.y);
+  p.done = at<unsigned>(ws, L.done);
+  p.err = p.sync = at<unsigned>(ws, 0);
+  p.T = d.T;
+  p.H = d.H;
+  p.E = d.E;
+  p.I = d.I;
+  p.Is = d.has_shared ? d.I_shared : 0;
+  p.top_k = d.top_k;
+  p.S = d.T * d.top_k;
+  p.has_shared = d.has_shared;
+  p.score_mode = d.score_mode;
+  p.route_scale = d.route_scale;
+  p.renorm_eps = d.renorm_eps;
+  return p;
+}
+
+void few_route(FewParams &p, const float *router_w, const float *bias, moe_bf16 *out) {
+  p.router_w = router_w;
+  p.bias = p.score_mode == MOE_SCORE_SIGMOID_BIAS ? bias : nullptr;
+  p.out = reinterpret_cast<__nv_bfloat16 *>(out);
+}
+
+void few_mxfp4(FewParams &p, const moe_mxfp4_experts &w) {
+  p.x = p.x16;
+  p.gate = w.gate;
+  p.up = w.up;
+  p.down = w.down;
+  p.s_gate = w.s_gate;
+  p.s_up = w.s_up;
+  p.s_down = w.s_down;
+  p.gate_scale = w.gate_scale;
+  p.up_scale = w.up_scale;
+  p.down_scale = w.down_scale;
+  p.s_gate_scale = w.s_gate_scale;
+  p.s_up_scale = w.s_up_scale;
+  p.s_down_scale = w.s_down_scale;
 }
 
 // Steps a3-a9 from a given routing, with the gate and up projections of every
@@ -763,6 +868,93 @@ MOE_API moe_status moe_layer_forward_w8a8(const moe_dims *d, const moe_bf16 *hid
                              sc, s, true, 0, w, true, true)) != MOE_OK)
     return st;
   return do_combine(*d, y, z, inv, wt, out, s, true);
+}
+
+MOE_API moe_status moe_quantize_mxfp4_rows(const moe_bf16 *src, int64_t rows, int cols, uint8_t *codes,
+                                           uint8_t *scales, void *stream) {
+  if (rows < 0 || cols <= 0 || cols % 128 != 0 || rows > INT64_MAX / cols) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!ptr_ok(src) || !ptr_ok(codes) || !ptr_ok(scales)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_quantize_mxfp4(reinterpret_cast<const __nv_bfloat16 *>(src), codes, scales,
+                                           (long long)rows * cols, (cudaStream_t)stream));
+}
+
+MOE_API moe_status moe_dequantize_mxfp4_rows(const uint8_t *codes, const uint8_t *scales, int64_t rows, int cols,
+                                             moe_bf16 *dst, void *stream) {
+  if (rows < 0 || cols <= 0 || cols % 128 != 0 || rows > INT64_MAX / cols) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!ptr_ok(dst) || !ptr_ok(codes) || !ptr_ok(scales)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_dequantize_mxfp4(codes, scales, reinterpret_cast<__nv_bfloat16 *>(dst),
+                                             (long long)rows * cols, (cudaStream_t)stream));
+}
+
+// MXFP4 rows are whole 64-byte pieces of 128 codes.
+bool mxfp4_shape_ok(const moe_dims &d) {
+  return d.H % 128 == 0 && d.I % 128 == 0 && (!d.has_shared || d.I_shared % 128 == 0);
+}
+
+MOE_API moe_status moe_expert_ffn_mxfp4(const moe_dims *d, const moe_bf16 *hidden, const int32_t *perm,
+                                        const int32_t *offsets, const moe_mxfp4_experts *w, moe_bf16 *y_sorted,
+                                        moe_bf16 *y_shared, void *ws, size_t ws_bytes, void *stream) {
+  moe_status st = moe_check_dims(d);
+  if (st != MOE_OK) return st;
+  if (!mxfp4_shape_ok(*d)) return MOE_ERR_UNSUPPORTED;
+  if (d->T == 0) return MOE_OK;
+  if (!ptr_ok(hidden) || !ptr_ok(perm) || !ptr_ok(offsets) || !ptr_ok(y_sorted) || !mxfp4_ok(*d, w))
+    return MOE_ERR_INVALID_ARG;
+  if (d->has_shared && !ptr_ok(y_shared)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
+  if (d->T > kFewMaxT) return MOE_ERR_UNSUPPORTED;
+  FewParams p = few_params(*d, hidden, ws);
+  few_mxfp4(p, *w);
+  p.perm = perm;
+  p.offsets = offsets;
+  p.y = nullptr;
+  p.y_sorted = reinterpret_cast<__nv_bfloat16 *>(y_sorted);
+  p.y_shared = reinterpret_cast<__nv_bfloat16 *>(y_shared);
+  return cuda_status(launch_few(p, true, num_sms(), (cudaStream_t)stream));
+}
+
+MOE_API moe_status moe_layer_forward_mxfp4(const moe_dims *d, const moe_bf16 *hidden, const float *router_w,
+                                           const float *expert_bias, const moe_mxfp4_experts *w, moe_bf16 *out,
+                                           void *ws, size_t ws_bytes, void *stream) {
+  moe_status st = moe_check_dims(d);
+  if (st != MOE_OK) return st;
+  if (!mxfp4_shape_ok(*d)) return MOE_ERR_UNSUPPORTED;
+  if (d->T == 0) return MOE_OK;
+  if (!ptr_ok(hidden) || !ptr_ok(router_w) || !ptr_ok(out) || !mxfp4_ok(*d, w)) return MOE_ERR_INVALID_ARG;
+  if (expert_bias != nullptr && !aligned16(expert_bias)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
+  if (d->T > kFewMaxT) return MOE_ERR_UNSUPPORTED;
+  FewParams p = few_params(*d, hidden, ws);
+  few_mxfp4(p, *w);
+  few_route(p, router_w, expert_bias, out);
+  return cuda_status(launch_few(p, true, num_sms(), (cudaStream_t)stream));
+}
+
+MOE_API moe_status moe_layer_forward_few(const moe_dims *d, const moe_bf16 *hidden, const float *router_w,
+                                         const float *expert_bias, const moe_bf16 *w_gate, const moe_bf16 *w_up,
+                                         const moe_bf16 *w_down, const moe_bf16 *ws_gate, const moe_bf16 *ws_up,
+                                         const moe_bf16 *ws_down, moe_bf16 *out, void *ws, size_t ws_bytes,
+                                         void *stream) {
+  moe_status st = moe_check_dims(d);
+  if (st != MOE_OK) return st;
+  if (d->T > kFewMaxT) return MOE_ERR_UNSUPPORTED;
+  if (d->T == 0) return MOE_OK;
+  if (!ptr_ok(hidden) || !ptr_ok(router_w) || !ptr_ok(w_gate) || !ptr_ok(w_up) || !ptr_ok(w_down) || !ptr_ok(out))
+    return MOE_ERR_INVALID_ARG;
+  if (expert_bias != nullptr && !aligned16(expert_bias)) return MOE_ERR_INVALID_ARG;
+  if (d->has_shared && (!ptr_ok(ws_gate) || !ptr_ok(ws_up) || !ptr_ok(ws_down))) return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
+  FewParams p = few_params(*d, hidden, ws);
+  p.gate = reinterpret_cast<const uint8_t *>(w_gate);
+  p.up = reinterpret_cast<const uint8_t *>(w_up);
+  p.down = reinterpret_cast<const uint8_t *>(w_down);
+  p.s_gate = reinterpret_cast<const uint8_t *>(ws_gate);
+  p.s_up = reinterpret_cast<const uint8_t *>(ws_up);
+  p.s_down = reinterpret_cast<const uint8_t *>(ws_down);
+  few_route(p, router_w, expert_bias, out);
+  return cuda_status(launch_few(p, false, num_sms(), (cudaStream_t)stream));
 }
 
 MOE_API moe_status moe_layer_forward(const moe_dims *d, const moe_bf16 *hidden, const float *router_w,

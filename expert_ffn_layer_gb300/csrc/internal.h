@@ -98,6 +98,7 @@ struct GemmParams {
 // word offsets into the workspace header (4 KiB, zero when the workspace is fresh;
 // every launch leaves them zero again)
 constexpr int kSyncClaim = 64, kSyncExit = 65, kSyncPermute = 66,
+              kSyncFew = 67,     // the one-kernel layer's two grid-wide waits and its exit counter
               kSyncDone = 128,   // kSyncDone .. + 257: gate/up tiles finished, per segment
               kSyncQuant = 512;  // kSyncQuant .. + 257: W8A8 quantisation tiles finished, per segment
 constexpr int kWsHeaderBytes = 4096;
@@ -121,6 +122,40 @@ cudaError_t launch_combine(const CombineParams &p, cudaStream_t stream, bool pdl
 cudaError_t launch_quantize_rows(const __nv_bfloat16 *src, uint8_t *q, float *scale, long long rows, int cols,
                                  cudaStream_t stream);
 
+// ----------------------------------------------------------------- MXFP4
+// packed codes [rows][cols / 2] and scale bytes [rows][cols / 32] of n = rows * cols
+// bf16 values (cols a multiple of 128, so n is too), and back
+cudaError_t launch_quantize_mxfp4(const __nv_bfloat16 *src, uint8_t *codes, uint8_t *scales, long long n,
+                                  cudaStream_t stream);
+cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, __nv_bfloat16 *dst, long long n,
+                                    cudaStream_t stream);
+
+// ------------------------------------------------- the layer for few tokens
+constexpr int kFewMaxT = 32;  // a token per bit of an expert's mask; four 8-token operand tiles
+struct FewParams {
+  const __nv_bfloat16 *hidden;  // [T][H]
+  const uint16_t *x;            // the products' token operand: hidden, or x16 with MXFP4 weights
+  uint16_t *x16;                // MXFP4: hidden as fp16 times a power of two per token (workspace)
+  float *x_unscale;             // MXFP4: [T] the reciprocals of those powers
+  const float *router_w;        // [E][H], or nullptr: the routing is given by perm and offsets
+  const float *bias;
+  const int32_t *perm, *offsets;
+  // weights: bf16 matrices, or packed MXFP4 codes and their scale bytes
+  const uint8_t *gate, *up, *down, *s_gate, *s_up, *s_down;
+  const uint8_t *gate_scale, *up_scale, *down_scale, *s_gate_scale, *s_up_scale, *s_down_scale;
+  float *logits;       // [T][E]
+  float *act, *act_s;  // [S][I], [T][Is] fp32 activations
+  unsigned *amax;      // [S + T] MXFP4: each activation row's largest magnitude (fp32 bits)
+  float *y;            // [S + T][H] fp32 outputs of every position, then of the shared expert; nullptr: write y_sorted
+  unsigned *done;      // finished segments per block of rows of y
+  __nv_bfloat16 *out;                  // [T][H]
+  __nv_bfloat16 *y_sorted, *y_shared;  // [S][H], [T][H]
+  unsigned *err, *sync;
+  int T, H, E, I, Is, top_k, S, has_shared, score_mode;
+  float route_scale, renorm_eps;
+};
+cudaError_t launch_few(const FewParams &p, bool mxfp4, int num_ctas, cudaStream_t stream);
+
 // self-test: a bounded wait on a barrier nothing completes (records MOE_DEVERR_TIMEOUT)
 cudaError_t launch_wait_timeout(unsigned *err, unsigned long long limit_ns, cudaStream_t stream);
 // self-test: out[i] = the expert epilogue's SiLU(g[i]) * u[i], n >= 1
@@ -140,5 +175,7 @@ cudaError_t set_smem_attr_once(const void *func, int bytes, unsigned long long &
 // shared launch helper: PDL attribute on, optional cluster dims
 cudaError_t launch_ex(const void *func, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool pdl,
                       int cluster_x, void **args);
+// cooperative launch: every CTA of the grid is resident, or the launch fails
+cudaError_t launch_coop(const void *func, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, void **args);
 
 }  // namespace moe

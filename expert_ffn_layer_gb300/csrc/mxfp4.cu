@@ -1,0 +1,101 @@
+// MXFP4 expert weights: rows of bf16 to packed E2M1 codes and scale bytes, and back.
+//
+// The Ascend deployment article (section 8.2) runs the routed experts with MXFP4
+// weights and fixes no further detail.  Here: the OCP Microscaling format, blocks
+// of 32 along a row, scale 2^(floor(log2 max|block|) - 2) (at least 2^-127), codes
+// nearest-even of value / scale with magnitudes past 6 saturated.  Both directions
+// are exact but for that one rounding: a scale is a power of two.
+//
+// Both kernels stream: 2 bytes read and 17/32 written a value, or the reverse, and
+// nothing is read twice.
+#include "internal.h"
+#include "mxfp4.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+constexpr int kMxThreads = 256;
+}  // namespace
+
+// One lane per 8 values: four lanes share a block's maximum, sixteen lanes a
+// 64-byte piece.  The maximum is taken on the magnitudes' bit patterns, which
+// order finite values by size and put infinities and NaN above them all.
+__global__ void __launch_bounds__(kMxThreads) quantize_mxfp4_kernel(const __nv_bfloat16 *__restrict__ src,
+                                                                    uint8_t *__restrict__ codes,
+                                                                    uint8_t *__restrict__ scales, long long n8) {
+  pdl_wait();
+  pdl_launch_dependents();
+  for (long long i = (long long)blockIdx.x * kMxThreads + threadIdx.x; i < n8; i += (long long)gridDim.x * kMxThreads) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(src) + i);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = max(top, max(u[j] & 0x7FFFu, (u[j] >> 16) & 0x7FFFu));
+    // n8 is a multiple of 16, so the lanes of a block are all here
+    const unsigned group = 0xFu << (threadIdx.x & 28u);
+    top = max(top, __shfl_xor_sync(group, top, 1));
+    top = max(top, __shfl_xor_sync(group, top, 2));
+    const uint32_t ex = top >> 7;  // biased exponent of the largest magnitude
+    const uint32_t e = ex == 255u ? 255u : ex > 2u ? ex - 2u : 0u;
+    const float inv = __uint_as_float((254u - min(e, 253u)) << 23);  // 2^(127 - e)
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = __uint_as_float(u[j] << 16) * inv;
+      f[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u) * inv;
+    }
+    const int l = (int)(i & 15), q = l >> 2, t = l & 3;
+    reinterpret_cast<uint32_t *>(codes)[(i & ~15ll) + 4 * t + q] = f32x8_to_e2m1(f);
+    if (t == 0) scales[i >> 2] = (uint8_t)e;
+  }
+}
+
+__global__ void __launch_bounds__(kMxThreads) dequantize_mxfp4_kernel(const uint8_t *__restrict__ codes,
+                                                                      const uint8_t *__restrict__ scales,
+                                                                      __nv_bfloat16 *__restrict__ dst, long long n8) {
+  pdl_wait();
+  pdl_launch_dependents();
+  for (long long i = (long long)blockIdx.x * kMxThreads + threadIdx.x; i < n8; i += (long long)gridDim.x * kMxThreads) {
+    const int l = (int)(i & 15), q = l >> 2, t = l & 3;
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(codes) + (i & ~15ll) + 4 * t + q);
+    const float s = e8m0_value(__ldg(scales + (i >> 2)));
+    uint32_t h[4], o[4];
+    e2m1x8_to_f16(w, h);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
+      o[j] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    __stcs(reinterpret_cast<uint4 *>(dst) + i, make_uint4(o[0], o[1], o[2], o[3]));
+  }
+}
+
+namespace {
+unsigned stream_blocks(long long n8) {
+  int dev = 0, nsm = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+  const long long blocks = (n8 + kMxThreads - 1) / kMxThreads, cap = (long long)(nsm > 0 ? nsm : 1) * 8;
+  return (unsigned)(blocks < cap ? blocks : cap);
+}
+}  // namespace
+
+cudaError_t launch_quantize_mxfp4(const __nv_bfloat16 *src, uint8_t *codes, uint8_t *scales, long long n,
+                                  cudaStream_t stream) {
+  long long n8 = n / 8;
+  void *args[] = {(void *)&src, (void *)&codes, (void *)&scales, (void *)&n8};
+  return launch_ex((const void *)quantize_mxfp4_kernel, dim3(stream_blocks(n8)), dim3(kMxThreads), 0, stream, true, 1,
+                   args);
+}
+
+cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, __nv_bfloat16 *dst, long long n,
+                                    cudaStream_t stream) {
+  long long n8 = n / 8;
+  void *args[] = {(void *)&codes, (void *)&scales, (void *)&dst, (void *)&n8};
+  return launch_ex((const void *)dequantize_mxfp4_kernel, dim3(stream_blocks(n8)), dim3(kMxThreads), 0, stream, true,
+                   1, args);
+}
+
+}  // namespace moe

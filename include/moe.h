@@ -304,6 +304,75 @@ moe_status moe_layer_forward_w8a8(const moe_dims *d, const moe_bf16 *hidden, con
                                   const float *expert_bias, const moe_fp8_experts *w, moe_bf16 *out, void *ws,
                                   size_t ws_bytes, void *stream);
 
+/* ----------------------------------------------------------------- MXFP4
+ * MXFP4 expert weights (the Ascend deployment article, section 8.2, runs the
+ * routed experts with them and fixes no further detail): OCP Microscaling,
+ * blocks of 32 values along a row sharing one power-of-two scale, elements E2M1
+ * (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives).  Weight-only: activations stay
+ * unquantised.  17/32 of a byte per weight, against two for bf16.
+ *   scale byte e stands for 2^(e - 127), e = floor(log2 max|block|) - 2 + 127, at
+ *     least 0; 255 (a block with an infinity or NaN) makes every output that
+ *     reads it non-finite, and the block's codes are then unspecified
+ *   code = nearest E2M1 value of w / 2^(e - 127), ties to the even code,
+ *     magnitudes past 6 saturated to 6; sign in the top bit
+ * Packed rows: a row of K codes (K a multiple of 128) is K / 128 pieces of 64
+ * bytes.  32-bit word 4 t + q of a piece (t, q in 0..3) holds the codes of the
+ * piece's values 32 q + 8 t .. + 7, the first in the lowest four bits: the plain
+ * order, in which that word is 4 q + t, with its 4 x 4 words transposed.  Codes of
+ * an existing MXFP4 checkpoint are brought into it by that transposition alone.
+ * The scales of a row are K / 32 bytes in order. */
+typedef struct {
+  const uint8_t *gate, *up;                   /* [E, I, H / 2] packed codes */
+  const uint8_t *down;                        /* [E, H, I / 2] */
+  const uint8_t *gate_scale, *up_scale;       /* [E, I, H / 32] scale bytes */
+  const uint8_t *down_scale;                  /* [E, H, I / 32] */
+  const uint8_t *s_gate, *s_up;               /* shared expert [I_shared, H / 2] (unused when !has_shared) */
+  const uint8_t *s_down;                      /* [H, I_shared / 2] */
+  const uint8_t *s_gate_scale, *s_up_scale;   /* [I_shared, H / 32] */
+  const uint8_t *s_down_scale;                /* [H, I_shared / 32] */
+} moe_mxfp4_experts;
+
+/* Quantise a bf16 matrix [rows, cols] (cols a multiple of 128): packed codes
+ * [rows, cols / 2] and scale bytes [rows, cols / 32]; and the bf16 values that
+ * codes and scales stand for (exact, but for results past bf16's range, which
+ * round as bf16 does).  Pointers 16-byte aligned.  Async on `stream`. */
+moe_status moe_quantize_mxfp4_rows(const moe_bf16 *src, int64_t rows, int cols, uint8_t *codes, uint8_t *scales,
+                                   void *stream);
+moe_status moe_dequantize_mxfp4_rows(const uint8_t *codes, const uint8_t *scales, int64_t rows, int cols,
+                                     moe_bf16 *dst, void *stream);
+
+/* moe_expert_ffn and moe_layer_forward with MXFP4 expert weights (all pointers
+ * in *w 16-byte aligned); arguments, layouts and errors as for those.  H, I and
+ * I_shared multiples of 128 (else MOE_ERR_UNSUPPORTED).
+ *   Batches of at most 32 tokens run as one kernel (for the layer: router,
+ *   selection, experts and combine).  It multiplies the code values, exact in
+ *   fp16, by the token values as fp16 times a power of two of each row's largest
+ *   magnitude -- exact for bf16 values down to 2^-28 of it; the fp32 activation is
+ *   rounded to fp16's 11 bits -- sums in fp32 and applies each block's scale to
+ *   its own fp32 sum.  A scale byte of 0 counts as a zero there.  The layer's
+ *   output is rounded once.
+ *   Such a call needs the whole device: it is a cooperative launch, whose blocks
+ *   (one per SM) are resident together. */
+moe_status moe_expert_ffn_mxfp4(const moe_dims *d, const moe_bf16 *hidden, const int32_t *perm,
+                                const int32_t *offsets, const moe_mxfp4_experts *w, moe_bf16 *y_sorted,
+                                moe_bf16 *y_shared, void *ws, size_t ws_bytes, void *stream);
+moe_status moe_layer_forward_mxfp4(const moe_dims *d, const moe_bf16 *hidden, const float *router_w,
+                                   const float *expert_bias, const moe_mxfp4_experts *w, moe_bf16 *out, void *ws,
+                                   size_t ws_bytes, void *stream);
+
+/* The whole layer (a1-a9) for few tokens, T <= 32 (else MOE_ERR_UNSUPPORTED), in
+ * one kernel: arguments as for moe_layer_forward, whose chain of kernels it
+ * replaces where their launches and hand-overs cost more than the work between
+ * them.  Its logits are fp32 sums of fp32 products of the bf16 hidden state and
+ * the fp32 router weight; activations and expert outputs stay fp32 (the down
+ * product takes the activation as two bf16 values, 16 bits of it) and `out` is
+ * rounded once, so its results differ from moe_layer_forward's in the last bits.
+ * Results do not depend on timing.  A cooperative launch, as above. */
+moe_status moe_layer_forward_few(const moe_dims *d, const moe_bf16 *hidden, const float *router_w,
+                                 const float *expert_bias, const moe_bf16 *w_gate, const moe_bf16 *w_up,
+                                 const moe_bf16 *w_down, const moe_bf16 *ws_gate, const moe_bf16 *ws_up,
+                                 const moe_bf16 *ws_down, moe_bf16 *out, void *ws, size_t ws_bytes, void *stream);
+
 /* The whole layer (a1-a9) chained on `stream` with programmatic dependent
  * launch; every intermediate lives in `ws`.  Arguments as above; out [T, H] bf16. */
 moe_status moe_layer_forward(const moe_dims *d, const moe_bf16 *hidden, const float *router_w,
