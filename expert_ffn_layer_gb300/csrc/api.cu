@@ -363,7 +363,8 @@ moe_status do_expert_phases(const moe_dims &d, int phases, const moe_bf16 *hidde
                             const moe_bf16 *w_down, const moe_bf16 *ws_gate, const moe_bf16 *ws_up,
                             const moe_bf16 *ws_down, moe_bf16 *y_sorted, moe_bf16 *y_shared,
                             const ExpertScratch &sc, cudaStream_t stream, bool pdl, uint64_t gu_stride = 0,
-                            const moe_fp8_experts *q = nullptr, bool early = false, bool w8a8 = false) {
+                            const moe_fp8_experts *q = nullptr, bool early = false, bool w8a8 = false,
+                            const moe_mxfp4_experts *q4 = nullptr) {
   // tiles of one launch at the narrowest chunking (16 tokens), for the 32-bit
   // claim counter and tile numbers
   {
@@ -425,6 +426,25 @@ moe_status do_expert_phases(const moe_dims &d, int phases, const moe_bf16 *hidde
     for (int b = 0; b < 4; ++b) ok = ok && map_u8_2d_sw(&g.map_act[b], g.aq, d.I, g.S, 16u << b);
     if (d.has_shared)
       for (int b = 0; b < 4; ++b) ok = ok && map_u8_2d_sw(&g.map_acts[b], g.aq_s, g.Is, d.T, 16u << b);
+    if (!ok) return MOE_ERR_CUDA;
+    return cuda_status(launch_expert_ffn(g, bn, num_sms(), stream, pdl));
+  }
+  if (q4 != nullptr) {  // MXFP4: maps of the packed codes, and the scale bytes
+    g.mode = 3;
+    g.qs_g = q4->gate_scale;
+    g.qs_u = q4->up_scale;
+    g.qs_d = q4->down_scale;
+    g.qs_sg = q4->s_gate_scale;
+    g.qs_su = q4->s_up_scale;
+    g.qs_sd = q4->s_down_scale;
+    ok = map_u8_3d(&g.map_wg, q4->gate, d.H / 2, d.I, d.E, 128) &&
+         map_u8_3d(&g.map_wu, q4->up, d.H / 2, d.I, d.E, 128) && map_u8_3d(&g.map_wd, q4->down, d.I / 2, d.H, d.E, 128);
+    if (d.has_shared)
+      ok = ok && map_u8_2d(&g.map_sg, q4->s_gate, d.H / 2, g.Is, 128) &&
+           map_u8_2d(&g.map_su, q4->s_up, d.H / 2, g.Is, 128) && map_u8_2d(&g.map_sd, q4->s_down, g.Is / 2, d.H, 128);
+    for (int b = 0; b < 4; ++b) ok = ok && map_bf16_2d(&g.map_act[b], g.act, d.I, g.S, 16u << b);
+    if (d.has_shared)
+      for (int b = 0; b < 4; ++b) ok = ok && map_bf16_2d(&g.map_acts[b], g.act_s, g.Is, d.T, 16u << b);
     if (!ok) return MOE_ERR_CUDA;
     return cuda_status(launch_expert_ffn(g, bn, num_sms(), stream, pdl));
   }
@@ -904,7 +924,10 @@ MOE_API moe_status moe_expert_ffn_mxfp4(const moe_dims *d, const moe_bf16 *hidde
     return MOE_ERR_INVALID_ARG;
   if (d->has_shared && !ptr_ok(y_shared)) return MOE_ERR_INVALID_ARG;
   if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
-  if (d->T > kFewMaxT) return MOE_ERR_UNSUPPORTED;
+  if (d->T > kFewMaxT)
+    return do_expert_phases(*d, 3, hidden, perm, offsets, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
+                            y_sorted, y_shared, scratch_in(*d, ws), (cudaStream_t)stream, true, 0, nullptr, false,
+                            false, w);
   FewParams p = few_params(*d, hidden, ws);
   few_mxfp4(p, *w);
   p.perm = perm;
@@ -925,7 +948,21 @@ MOE_API moe_status moe_layer_forward_mxfp4(const moe_dims *d, const moe_bf16 *hi
   if (!ptr_ok(hidden) || !ptr_ok(router_w) || !ptr_ok(out) || !mxfp4_ok(*d, w)) return MOE_ERR_INVALID_ARG;
   if (expert_bias != nullptr && !aligned16(expert_bias)) return MOE_ERR_INVALID_ARG;
   if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
-  if (d->T > kFewMaxT) return MOE_ERR_UNSUPPORTED;
+  if (d->T > kFewMaxT) {
+    const WsLayout L = ws_layout(*d);
+    cudaStream_t s = (cudaStream_t)stream;
+    int32_t *idx = at<int32_t>(ws, L.topk_idx);
+    float *wt = at<float>(ws, L.topk_w);
+    int32_t *perm = at<int32_t>(ws, L.perm), *inv = at<int32_t>(ws, L.inv);
+    int32_t *offs = at<int32_t>(ws, L.offsets);
+    moe_bf16 *y = at<moe_bf16>(ws, L.y_sorted), *z = at<moe_bf16>(ws, L.y_shared);
+    if ((st = do_route(*d, hidden, router_w, expert_bias, nullptr, idx, wt, ws, s, true)) != MOE_OK) return st;
+    if ((st = do_permute(*d, idx, at<int32_t>(ws, L.counts), offs, perm, inv, ws, s, true)) != MOE_OK) return st;
+    if ((st = do_expert_phases(*d, 3, hidden, perm, offs, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, y, z,
+                               scratch_in(*d, ws), s, true, 0, nullptr, true, false, w)) != MOE_OK)
+      return st;
+    return do_combine(*d, y, z, inv, wt, out, s, true);
+  }
   FewParams p = few_params(*d, hidden, ws);
   few_mxfp4(p, *w);
   few_route(p, router_w, expert_bias, out);

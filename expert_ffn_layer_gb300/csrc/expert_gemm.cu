@@ -62,6 +62,7 @@
 
 #include "fp8.cuh"
 #include "internal.h"
+#include "mxfp4.cuh"
 #include "ptx.cuh"
 #include "silu.cuh"
 
@@ -97,26 +98,30 @@ constexpr unsigned long long kDrainNs = 20000000ull;
 // Kernel modes: bf16 weights; FP8 weights expanded to bf16 in shared memory by
 // converter warps (weight-only); W8A8 -- FP8 weights and FP8 activations fed
 // straight to kind::f8f6f4 MMAs (K steps of 128 codes: 128-byte rows again).
-constexpr int kModeBF16 = 0, kModeQ8 = 1, kModeF8 = 2;
+// MXFP4 weights (kModeQ4) go the way of the weight-only FP8 ones: a code slot
+// holds 128 codes of each row, two K steps, and the converters multiply each code's
+// value by its block's power of two (exact in bf16).
+constexpr int kModeBF16 = 0, kModeQ8 = 1, kModeF8 = 2, kModeQ4 = 3;
+constexpr bool converts(int mode) { return mode == kModeQ8 || mode == kModeQ4; }
 
 // Ring depths: weight slots of 32 KB and token slots of BN x 128 bytes; with
 // FP8 weights, code slots of 16 KB (the bytes in flight from HBM) and three
 // bf16 weight slots between the converters and the MMAs.
 template <int BN, int MODE>
 struct Rings {
-  static constexpr bool Q8 = MODE == kModeQ8;
-  static constexpr int kW = Q8 ? 3 : BN >= 256 ? 3 : BN >= 240 ? 4 : BN >= 128 ? 5 : 6;
-  static constexpr int kQ = Q8 ? (BN >= 128 ? 4 : 6) : 0;
+  static constexpr bool CV = converts(MODE);
+  static constexpr int kW = CV ? 3 : BN >= 256 ? 3 : BN >= 240 ? 4 : BN >= 128 ? 5 : 6;
+  static constexpr int kQ = CV ? (BN >= 128 ? 4 : 6) : 0;
   static constexpr int kT = BN >= 64 ? 3 : 4;
 };
 
 template <int BN, int MODE>
 struct Layout {
-  static constexpr bool Q8 = MODE == kModeQ8;
+  static constexpr bool CV = converts(MODE);
   static constexpr int kW = Rings<BN, MODE>::kW;
   static constexpr int kQ = Rings<BN, MODE>::kQ;
   static constexpr int kT = Rings<BN, MODE>::kT;
-  static constexpr int kEpiW = Q8 ? kEpiWarps - kCvtWarps : kEpiWarps;  // epilogue warps
+  static constexpr int kEpiW = CV ? kEpiWarps - kCvtWarps : kEpiWarps;  // epilogue warps
   static constexpr int kTokBytes = BN * 128;
   static constexpr int kQOff = kW * kABytes;
   static constexpr int kTOff = kQOff + kQ * kQBytes;
@@ -147,7 +152,7 @@ struct Layout {
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert(kTmemUsed <= 512, "TMEM budget");
   static_assert(kW <= 16 && kT <= 16 && kQ <= 16, "issue masks");
-  static_assert(!Q8 || BN <= 128, "FP8 weights run the narrow tiles");
+  static_assert(!CV || BN <= 128, "converted weights run the narrow tiles");
   static_assert(MODE != kModeF8 || BN <= 240, "the W8A8 epilogue has no staged (256-token) form");
 };
 
@@ -530,6 +535,20 @@ __device__ __forceinline__ uint4 e4m3x8_to_bf16(uint32_t w0, uint32_t w1) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// Eight E2M1 codes times their block's scale, as bf16 (exact but for results past
+// bf16's range: four significant bits at most).
+__device__ __forceinline__ uint4 e2m1x8_to_bf16(uint32_t w, float s) {
+  uint32_t h[4], o[4];
+  e2m1x8_to_f16(w, h);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
+    o[j] = *reinterpret_cast<const uint32_t *>(&b);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // W8A8 quantisation tile: the activation rows of one chunk (or one block of 256
 // of their columns, see quant_blocks) to E4M3 codes, once
 // (each down row block then loads the codes by TMA instead of quantising the
@@ -579,7 +598,7 @@ __device__ __forceinline__ void quantize_chunk_rows(const GemmParams &p, const T
 template <int BN, int MODE>
 __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __grid_constant__ GemmParams p) {
   using L = Layout<BN, MODE>;
-  constexpr bool Q8 = MODE == kModeQ8, F8 = MODE == kModeF8;
+  constexpr bool Q8 = MODE == kModeQ8, F8 = MODE == kModeF8, Q4 = MODE == kModeQ4, CV = converts(MODE);
   constexpr int KE = F8 ? 128 : 64;  // K elements per step: one 128-byte row of a weight or token box
   constexpr int KSH = F8 ? 7 : 6;
   constexpr int KW = L::kW, KT = L::kT, KQ = L::kQ, EW = L::kEpiW;
@@ -615,12 +634,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < KW; ++s) {
-      mbar_init(wfull_bar(s), Q8 ? kCvtWarps / 2 : 1);  // the weight loader's expect_tx arrival, or one converter group
+      mbar_init(wfull_bar(s), CV ? kCvtWarps / 2 : 1);  // the weight loader's expect_tx arrival, or one converter group
       mbar_init(wempty_bar(s), 2);                  // both MMA issuers' commits
     }
     for (int s = 0; s < KQ; ++s) {
       mbar_init(qfull_bar(s), 1);           // the loader's expect_tx arrival
-      mbar_init(qempty_bar(s), kCvtWarps / 2);  // one converter group done reading
+      mbar_init(qempty_bar(s), Q4 ? kCvtWarps : kCvtWarps / 2);  // its converter groups done reading
     }
     for (int s = 0; s < KT; ++s) {
       mbar_init(tfull_bar(s), kTokThreads);  // one arrival per loader thread (cp.async, or the TMA expect_tx)
@@ -634,7 +653,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
     mbar_init(drain_bar2, 1);
     for (int r = 0; r < kRing; ++r) {
       mbar_init(id_full(r), 1);
-      mbar_init(id_empty(r), 2 + 4 + EW + (Q8 ? kCvtWarps : 0));  // MMA issuers, token loaders, epilogue, converters
+      mbar_init(id_empty(r), 2 + 4 + EW + (CV ? kCvtWarps : 0));  // MMA issuers, token loaders, epilogue, converters
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -669,15 +688,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
     // of its tiles depends on the routing, and the early block alone would
     // stream them from a few SMs.  Each CTA takes a strided share of the
     // 64 x 128 boxes of ws_gate, ws_up and ws_down.
-    const int kx_gu = p.H / KE, n_gu = kx_gu * ((p.Is + 127) / 128);
-    const int kx_d = p.Is / KE, n_d = kx_d * ((p.H + 127) / 128);
+    constexpr int KB = Q4 ? 64 : KE, KV = Q4 ? 128 : KE;  // a box's columns as the maps count them, and K values
+    const int kx_gu = p.H / KV, n_gu = kx_gu * ((p.Is + 127) / 128);
+    const int kx_d = p.Is / KV, n_d = kx_d * ((p.H + 127) / 128);
     for (int b = blockIdx.x; b < 2 * n_gu + n_d; b += gridDim.x) {
       if (b < 2 * n_gu) {
         const int bb = b < n_gu ? b : b - n_gu;
-        tma_prefetch_l2_2d(b < n_gu ? &p.map_sg : &p.map_su, (bb % kx_gu) * KE, (bb / kx_gu) * 128);
+        tma_prefetch_l2_2d(b < n_gu ? &p.map_sg : &p.map_su, (bb % kx_gu) * KB, (bb / kx_gu) * 128);
       } else {
         const int bb = b - 2 * n_gu;
-        tma_prefetch_l2_2d(&p.map_sd, (bb % kx_d) * KE, (bb / kx_d) * 128);
+        tma_prefetch_l2_2d(&p.map_sd, (bb % kx_d) * KB, (bb / kx_d) * 128);
       }
     }
   }
@@ -693,7 +713,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
     // issues the weight TMA loads (FP8 weights to the code slots, bf16 weights
     // straight to the weight slots); the whole warp builds the claim-order
     // tables when the first tile past the early block is claimed.
-    constexpr int NS = Q8 ? KQ : KW;
+    constexpr int NS = CV ? KQ : KW;
     // Weights stream with the evict-first L2 policy.  256-token tiles (experts
     // averaging more than 256 tokens) split an expert into several chunks whose
     // tiles read the same weight rows at about the same time: there every chunk
@@ -739,15 +759,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
           const int last_row0 = seg0 + (chunk_count<BN>(cnt) - 1) * chunk_base<BN>(cnt);
           if (tl.row0 < last_row0) pol_w = pol_keep;
         }
-        for (int kb = 0; kb < tl.nk; ++kb) {
-          const uint32_t fb = Q8 ? qfull_bar(ws) : wfull_bar(ws);
-          ok = mbar_wait(Q8 ? qempty_bar(ws) : wempty_bar(ws), wph ^ 1u, err, abort_flag);
+        const int nload = Q4 ? tl.nk >> 1 : tl.nk;  // MXFP4: a load brings the codes of two K steps
+        for (int kb = 0; kb < nload; ++kb) {
+          const uint32_t fb = CV ? qfull_bar(ws) : wfull_bar(ws);
+          ok = mbar_wait(CV ? qempty_bar(ws) : wempty_bar(ws), wph ^ 1u, err, abort_flag);
           if (!ok) break;
-          const int k0 = kb * KE;
-          mbar_arrive_expect_tx(fb, (uint32_t)(Q8 ? kQBytes : kABytes));
+          const int k0 = kb * KE;  // MXFP4: 64 bytes of packed codes
+          mbar_arrive_expect_tx(fb, (uint32_t)(CV ? kQBytes : kABytes));
           issued |= 1u << ws;
           issued_par = (issued_par & ~(1u << ws)) | (wph << ws);
-          const uint32_t a0 = Q8 ? q_smem(ws) : w_smem(ws), a1 = a0 + (Q8 ? kQBytes / 2 : kABytes / 2);
+          const uint32_t a0 = CV ? q_smem(ws) : w_smem(ws), a1 = a0 + (CV ? kQBytes / 2 : kABytes / 2);
           if (tl.phase == 0) {
             if (tl.shared) {
               tma_load_2d_hint(a0, &p.map_sg, fb, k0, i0, pol_w);
@@ -775,7 +796,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
     }
     if (!ok && lane == 0)
       for (int s2 = 0; s2 < NS; ++s2)
-        if ((issued >> s2) & 1u) mbar_wait_drain(Q8 ? qfull_bar(s2) : wfull_bar(s2), (issued_par >> s2) & 1u);
+        if ((issued >> s2) & 1u) mbar_wait_drain(CV ? qfull_bar(s2) : wfull_bar(s2), (issued_par >> s2) & 1u);
   } else if (warp < kTokWarp0 + 4) {
     // ================= token rows (gate/up) or activation rows (down)
     const int tid = threadIdx.x - 32 * kTokWarp0;  // 0..127
@@ -1199,6 +1220,81 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
         if (warp == kEpiWarp0 && lane == 0) atomicAdd(done1 + tl.seg, 1u);
       }
     }
+  } else if constexpr (Q4) {
+    // ================= MXFP4 weights (warps 14..21): codes and scales -> bf16
+    // weight slots.  Two groups of four warps as with FP8 weights below; here a
+    // code slot holds two K steps, so group 0 takes the first and group 1 the
+    // second of every slot (nk is even) and both free it.  In a pass lane l
+    // converts, in row 8 it + r, the codes of the step's two blocks in the row's
+    // 16-byte piece l & 3 -- eight values of each block, 16 bytes of bf16.  The
+    // eight lanes of a store phase take rows r and r + 4, whose swizzles differ in
+    // the upper half of the row, so their 16-byte pieces cover all banks.
+    // A step's scale bytes are loaded a step ahead, before the wait for its codes.
+    const int cw = warp - (kEpiWarp0 + EW);
+    const int grp = cw >> 2, wg = cw & 3;
+    const int box = wg >> 1, c = lane & 3, rlane = (lane >> 3) + (lane & 4);
+    int ws = 0, qs = 0;
+    uint32_t wph = 0, qph = 0;
+    for (int i = 0; ok; ++i) {
+      const int rs = i % kRing;
+      ok = __all_sync(0xffffffffu, mbar_wait(id_full(rs), (uint32_t)(i / kRing) & 1u, err, abort_flag));
+      if (!ok) break;
+      const int t = ring[rs];
+      const Tile tl = tiles[rs];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(id_empty(rs));
+      if (t < 0) break;
+      const int rows = tl.phase == 0 ? (tl.shared ? p.Is : p.I) : p.H, nsc = tl.nk * 2;  // scale bytes of a row
+      const uint8_t *mat = tl.phase == 0 ? (tl.shared ? (box ? p.qs_su : p.qs_sg) : (box ? p.qs_u : p.qs_g))
+                                         : (tl.shared ? p.qs_sd : p.qs_d);
+      const int row_b = tl.rb * (tl.phase == 0 ? 128 : 256) + (tl.phase == 0 ? 0 : box * 128) + 64 * (wg & 1) + rlane;
+      if (!tl.shared) mat += (size_t)tl.seg * rows * nsc;
+      uint32_t sc[8];
+      auto load_scales = [&](int kb) {
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+          const int row = row_b + 8 * it;
+          sc[it] = row < rows ? __ldg(reinterpret_cast<const uint16_t *>(mat + (size_t)row * nsc + 2 * kb)) : 0u;
+        }
+      };
+      if (grp < tl.nk) load_scales(grp);
+      for (int kb = 0; kb < tl.nk; ++kb) {
+        if ((kb & 1) == grp) {
+          ok = __all_sync(0xffffffffu, mbar_wait(qfull_bar(qs), qph, err, abort_flag) &&
+                                           mbar_wait(wempty_bar(ws), wph ^ 1u, err, abort_flag));
+          if (!ok) break;
+          const uint8_t *src = smem + L::kQOff + qs * kQBytes + box * (kQBytes / 2) + c * 16 + grp * 8;
+          uint8_t *dst = smem + ws * kABytes + box * (kABytes / 2);
+          uint2 v[8];
+#pragma unroll
+          for (int it = 0; it < 8; ++it)
+            v[it] = *reinterpret_cast<const uint2 *>(src + (64 * (wg & 1) + 8 * it + rlane) * 64);
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            const int rr = 64 * (wg & 1) + 8 * it + rlane;
+            uint8_t *row = dst + rr * 128;
+            *reinterpret_cast<uint4 *>(row + ((c ^ (rr & 7)) << 4)) = e2m1x8_to_bf16(v[it].x, e8m0_value(sc[it] & 255u));
+            *reinterpret_cast<uint4 *>(row + (((4 + c) ^ (rr & 7)) << 4)) =
+                e2m1x8_to_bf16(v[it].y, e8m0_value(sc[it] >> 8));
+          }
+          fence_proxy_async_smem();  // generic-proxy writes read by the tensor core
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(wfull_bar(ws));
+            mbar_arrive(qempty_bar(qs));
+          }
+          if (kb + 2 < tl.nk) load_scales(kb + 2);
+        }
+        if (++ws == KW) {
+          ws = 0;
+          wph ^= 1u;
+        }
+        if ((kb & 1) && ++qs == KQ) {
+          qs = 0;
+          qph ^= 1u;
+        }
+      }
+    }
   } else if constexpr (Q8) {
     // ================= FP8 weights (warps 14..21): codes -> bf16 weight slots
     // (the values of the codes; the epilogue applies each row's scale).
@@ -1319,6 +1415,13 @@ cudaError_t launch_expert_ffn(const GemmParams &p, int bn, int num_ctas, cudaStr
       case 64: return launch_one<64, kModeQ8>(p, num_ctas, stream, pdl);
       case 128: return launch_one<128, kModeQ8>(p, num_ctas, stream, pdl);
       default: return cudaErrorInvalidValue;
+    }
+  }
+  if (p.mode == kModeQ4) {
+    switch (bn < 128 ? bn : 128) {
+      case 64: return launch_one<64, kModeQ4>(p, num_ctas, stream, pdl);
+      case 128: return launch_one<128, kModeQ4>(p, num_ctas, stream, pdl);
+      default: return cudaErrorInvalidValue;  // 32 tokens and fewer run the one-kernel form
     }
   }
   if (p.mode == kModeF8) {  // W8A8: up to 240-token tiles (the epilogue has no staged form)

@@ -73,6 +73,9 @@ struct GemmParams {
   int mode;
   const float *sc_g, *sc_u, *sc_d;     // [E][I], [E][I], [E][H]
   const float *sc_sg, *sc_su, *sc_sd;  // [Is], [Is], [H]
+  // MXFP4 (mode 3): maps as mode 1's, of the packed codes (K / 2 bytes a row), and
+  // the scale bytes [E][I][H / 32], [E][I][H / 32], [E][H][I / 32], shared alike
+  const uint8_t *qs_g, *qs_u, *qs_d, *qs_sg, *qs_su, *qs_sd;
   // W8A8 (mode 2): the hidden state quantised per token (codes [T][H], scales
   // [T]), and the gate/up epilogue's per-32-column maxima of the bf16
   // activations ([S][I/32] routed, [T][Is/32] shared) that set the down tiles'

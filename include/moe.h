@@ -351,7 +351,10 @@ moe_status moe_dequantize_mxfp4_rows(const uint8_t *codes, const uint8_t *scales
  *   rounded to fp16's 11 bits -- sums in fp32 and applies each block's scale to
  *   its own fp32 sum.  A scale byte of 0 counts as a zero there.  The layer's
  *   output is rounded once.
- *   Such a call needs the whole device: it is a cooperative launch, whose blocks
+ *   Larger batches run the chain of kernels of moe_layer_forward; its expert kernel
+ *   expands the weights to bf16 in shared memory (exact) and keeps the activations
+ *   between the products in bf16, as the bf16 kernel does.
+ *   A call of at most 32 tokens needs the whole device: it is a cooperative launch, whose blocks
  *   (one per SM) are resident together. */
 moe_status moe_expert_ffn_mxfp4(const moe_dims *d, const moe_bf16 *hidden, const int32_t *perm,
                                 const int32_t *offsets, const moe_mxfp4_experts *w, moe_bf16 *y_sorted,

@@ -185,6 +185,38 @@ def test_expert_ffn_mxfp4_few(w, T):
     ffn_case(w, W.layer_inputs(w), topk)
 
 
+@pytest.mark.parametrize("w", [TINY, WIDE, ODD, NOSH, MID], ids=lambda w: w.name)
+@pytest.mark.parametrize("T", [33, 64, 65, 128, 129, 300])
+def test_expert_ffn_mxfp4_many(w, T):
+    """Batches past 32 tokens: the expert kernel with converter warps."""
+    w = w.with_(T=T)
+    rng = np.random.default_rng(T)
+    topk = np.stack([rng.permutation(w.E)[:w.top_k] for _ in range(T)]).astype(np.int32)
+    ffn_case(w, W.layer_inputs(w), topk)
+
+
+@pytest.mark.parametrize("T", [700, 1040])
+def test_expert_ffn_mxfp4_skewed(T):
+    """One expert holding every token (several chunks), idle experts."""
+    w = MID.with_(T=T, top_k=2)
+    topk = np.zeros((T, 2), dtype=np.int32)
+    topk[:, 0] = 3
+    topk[:, 1] = np.where(np.arange(T) < 512, 6, 1)
+    ffn_case(w, W.layer_inputs(w), topk)
+
+
+@pytest.mark.parametrize("w", [TINY, MID, NOSH], ids=lambda w: w.name)
+@pytest.mark.parametrize("T", [33, 200])
+def test_layer_mxfp4_many(w, T):
+    w = w.with_(T=T)
+    inp = W.layer_inputs(w)
+    dl = DeviceLayer(w, inp)
+    got = host_f64(layer(dl, experts_of(dl)))
+    assert moe.moe_ws_read_error(dl.ws) == 0
+    # the chain's router: 1e-5 of the logits' norm, from the split of the router weight
+    check_layer(w, dequantised(inp), got, BF16_HALF, f"{w.name} T={T}", y_eps=BF16_HALF)
+
+
 def test_expert_ffn_mxfp4_repeated_expert():
     """A routing that names the same expert twice for a token, and one expert for all."""
     w = ODD.with_(T=9)
