@@ -187,7 +187,7 @@ int router_ksplit(const moe_dims &d, int nsm) {
 // The one-kernel layer's pieces, for batches of at most kFewMaxT tokens (they
 // share the workspace with the layout below: no call uses both).
 struct FewWs {
-  size_t logits, x16, x_unscale, act, act_s, amax, y, done, total;
+  size_t logits, x16, x_unscale, act, act16, act_exp, y, total;
 };
 FewWs few_ws(const moe_dims &d) {
   FewWs L;
@@ -201,11 +201,11 @@ FewWs few_ws(const moe_dims &d) {
   L.logits = take(T * (size_t)d.E * 4);
   L.x16 = take(T * (size_t)d.H * 2);
   L.x_unscale = take(T * 4);
-  L.act = take(S * (size_t)d.I * 4);
-  L.act_s = take(T * Is * 4);
-  L.amax = take((S + T) * 4);
+  const size_t n_act = S * (size_t)d.I + T * Is;
+  L.act = take(n_act * 4);
+  L.act16 = take(n_act * 2);
+  L.act_exp = take(n_act / 32);
   L.y = take((S + T) * (size_t)d.H * 4);
-  L.done = take((size_t)(d.H / 32) * 4);
   L.total = off;
   return L;
 }
@@ -557,10 +557,9 @@ FewParams few_params(const moe_dims &d, const moe_bf16 *hidden, void *ws) {
   p.x_unscale = at<float>(ws, L.x_unscale);
   p.logits = at<float>(ws, L.logits);
   p.act = at<float>(ws, L.act);
-  p.act_s = at<float>(ws, L.act_s);
-  p.amax = at<unsigned>(ws, L.amax);
+  p.act16 = at<uint16_t>(ws, L.act16);
+  p.act_exp = at<uint8_t>(ws, L.act_exp);
   p.y = at<float>(ws, L.y);
-  p.done = at<unsigned>(ws, L.done);
   p.err = p.sync = at<unsigned>(ws, 0);
   p.T = d.T;
   p.H = d.H;

@@ -30,11 +30,12 @@
 // Two grid-wide waits order the phases (logits -> selection, activations -> down).
 // They are bounded like every wait here: a CTA that gives up sets
 // MOE_DEVERR_TIMEOUT and the kernel winds down.
+#include <climits>
+
 #include "internal.h"
 #include "mxfp4.cuh"
 #include "ptx.cuh"
 #include "silu.cuh"
-#include "topk.cuh"
 
 namespace moe {
 
@@ -53,28 +54,28 @@ struct Fmt {  // weights: 0 bf16, 1 MXFP4
   static constexpr int kStage = kStageW + (WT ? 128 : 0);  // with the 32 rows' four scale bytes
 };
 
-template <int NT>
-struct FewLayout {
-  static constexpr int kNst = 4;
-  static constexpr int kRedBufs = NT <= 2 ? 2 : 1;  // double-buffered where it fits
-  static constexpr int kRedFloats = kFewWarps * 2 * NT * 128;
-};
+constexpr int kNst = 4;         // steps of a warp's ring
+constexpr int kRedCol = 20;     // floats from one column of a partial 16 x 8 tile to the next (16 rows: no bank conflicts)
+constexpr int kRedTile = 8 * kRedCol;
+constexpr int kRedFloats = kFewWarps * 2 * kRedTile;  // one of two buffers
 
 // Tables every CTA builds for itself from the routing.
 struct FewTables {
-  // active segments in expert order (the shared expert is not in the list): an
-  // expert's positions, in pieces of at most 8 NT -- a given routing may name an
-  // expert more than once for a token
+  // segments: the active experts in order, each in pieces of at most 8 positions
+  // (the columns of a product).  An expert of more re-reads its weights, by then in
+  // L2; with at most 32 tokens few have more.
   int seg_e[kMaxSegs];
-  int seg_row0[kMaxSegs + 1];  // first position of each
+  int seg_row0[kMaxSegs];  // first position of each
+  int seg_n[kMaxSegs];     // positions of each
   int tok[kMaxPos];   // token of each routed position
   int pos[kFewMaxT * 16];      // position of slot t * k + j
   float w[kFewMaxT * 16];      // combine weight of each slot
   int idx[kFewMaxT * 16];
   unsigned mask[256];          // tokens of each expert
   int base[256];               // first position of each expert
-  int nact, nsh;               // active routed segments; 1 with a shared expert
-  int last, abort_flag;
+  int scan[8];                 // build_segments' warp totals
+  int nact, nsh;               // routed segments; the shared expert's pieces of 8 tokens
+  int abort_flag;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
@@ -128,6 +129,14 @@ __device__ __forceinline__ float fp16_unscale(uint32_t top) {
   return __uint_as_float((ex - 14u) << 23);
 }
 
+// Scale byte i of a word as a power of two, 2^(byte - 127) (0 counts as zero, 255 is infinite).
+__device__ __forceinline__ float scale_of(uint32_t w, int i) {
+  return __uint_as_float((i < 3 ? w << (23 - 8 * i) : w >> 1) & 0x7F800000u);
+}
+__device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&h);
@@ -168,9 +177,9 @@ struct Plan {
   int ks, rg_shift;   // K slices, log2 of the row groups
   int unit_rows;      // rows (pairs of rows for gate/up) of a unit
   int rows_r, rows_s; // rows of a routed / the shared expert
-  int rb_r, rb_s;     // units of each
+  int rb_r, rb_s;     // units of a segment of each
   int steps_r, steps_s;
-  int units;
+  int n_sh, units;    // units of the shared expert (they come first), and all
 };
 
 // KS by the shortest makespan: rounds of units over the CTAs, each as long as its
@@ -180,7 +189,7 @@ template <bool DOWN>
 __device__ Plan make_plan(const FewTables &tb, int rows_r, int rows_s, int steps_r, int steps_s) {
   Plan best = {};
   int best_cost = 0x7fffffff;
-  for (int sh = 0; sh <= 4; ++sh) {  // RG = 2^sh
+  for (int sh = DOWN ? 0 : 1; sh <= 4; ++sh) {  // RG = 2^sh; gate/up units are whole blocks of 32 activations
     Plan q;
     q.rg_shift = sh;
     q.ks = kFewWarps >> sh;
@@ -190,8 +199,9 @@ __device__ Plan make_plan(const FewTables &tb, int rows_r, int rows_s, int steps
     q.steps_r = steps_r;
     q.steps_s = steps_s;
     q.rb_r = (rows_r + q.unit_rows - 1) / q.unit_rows;
-    q.rb_s = tb.nsh ? (rows_s + q.unit_rows - 1) / q.unit_rows : 0;
-    q.units = q.rb_s + tb.nact * q.rb_r;
+    q.rb_s = (rows_s + q.unit_rows - 1) / q.unit_rows;
+    q.n_sh = tb.nsh * q.rb_s;
+    q.units = q.n_sh + tb.nact * q.rb_r;
     const int rounds = (q.units + gridDim.x - 1) / gridDim.x;
     const int cost = rounds * (((max(steps_r, tb.nsh ? steps_s : 0) + q.ks - 1) / q.ks) * 1400 + 300);
     if (cost < best_cost) {
@@ -203,31 +213,36 @@ __device__ Plan make_plan(const FewTables &tb, int rows_r, int rows_s, int steps
 }
 
 struct Unit {
-  int seg;   // index in the active list, -1 the shared expert
-  int e;     // expert (0 for the shared one)
+  bool sh;           // of the shared expert
+  int e;             // expert (0 for the shared one)
   int rb, row0, ntok;
-  int s0, n; // this warp's first step and its number of steps
+  int s0, n;         // this warp's first step and its number of steps
 };
 
 __device__ __forceinline__ Unit decode_unit(const FewParams &p, const FewTables &tb, const Plan &q, int u, int warp,
                                             int warp_rows) {
   Unit t;
+  if (u >= q.units) {
+    t.n = 0;
+    t.ntok = 0;
+    return t;
+  }
   int steps, rows;
-  if (u < q.rb_s) {
-    t.seg = -1;
+  t.sh = u < q.n_sh;
+  if (t.sh) {  // pieces innermost: the units that read the same weights run together
+    t.rb = u / tb.nsh;
+    const int piece = u - t.rb * tb.nsh;
     t.e = 0;
-    t.rb = u;
-    t.row0 = p.S;
-    t.ntok = p.T;
+    t.row0 = p.S + 8 * piece;
+    t.ntok = min(8, p.T - 8 * piece);
     steps = q.steps_s;
     rows = q.rows_s;
   } else {
-    const int v = u - q.rb_s;
-    t.seg = v / q.rb_r;
-    t.rb = v - t.seg * q.rb_r;
-    t.e = tb.seg_e[t.seg];
-    t.row0 = tb.seg_row0[t.seg];
-    t.ntok = tb.seg_row0[t.seg + 1] - t.row0;
+    const int v = u - q.n_sh, seg = v / q.rb_r;
+    t.rb = v - seg * q.rb_r;
+    t.e = tb.seg_e[seg];
+    t.row0 = tb.seg_row0[seg];
+    t.ntok = tb.seg_n[seg];
     steps = q.steps_r;
     rows = q.rows_r;
   }
@@ -238,16 +253,25 @@ __device__ __forceinline__ Unit decode_unit(const FewParams &p, const FewTables 
   return t;
 }
 
+// The token operand of one step in registers: this lane's 8 values of each group
+// of 32, for column g; MXFP4 down also the groups' exponents for columns 2 t, 2 t + 1.
+template <int WT, bool DOWN>
+struct TokenStep {
+  static constexpr int kN = (DOWN && !WT) ? 2 * Fmt<WT>::kGroups : Fmt<WT>::kGroups;
+  uint4 v[kN];
+  uint32_t ex[2];
+};
+
 // One phase over this CTA's units.  DOWN: the products with w_down, else gate/up.
-template <int WT, int NT, bool DOWN>
+template <int WT, bool DOWN>
 __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, float *red, unsigned *wait_for, bool &ok) {
-  constexpr int NST = FewLayout<NT>::kNst, G = Fmt<WT>::kGroups, STAGE = Fmt<WT>::kStage;
+  constexpr int G = Fmt<WT>::kGroups, STAGE = Fmt<WT>::kStage;
   constexpr int kRows = DOWN ? 32 : 16;  // rows a warp's unit advances by
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const int K_r = DOWN ? p.I : p.H, K_s = DOWN ? p.Is : p.H;
   const Plan q = make_plan<DOWN>(tb, DOWN ? p.H : p.I, DOWN ? p.H : p.Is, K_r / Fmt<WT>::kStep, K_s / Fmt<WT>::kStep);
   const int rg = warp / q.ks;
-  const uint32_t my_ring = smem_u32(ring) + warp * NST * STAGE;
+  const uint32_t my_ring = smem_u32(ring) + warp * kNst * STAGE;
 
   // ---- the weight stream: position (unit, step) of the next step to copy
   int fu = blockIdx.x, fs = 0, fn = 0, fslot = 0;
@@ -257,19 +281,18 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
     while (fu < q.units) {
       const Unit t = decode_unit(p, tb, q, fu, warp, kRows);
       if (t.n > 0) {
-        const bool sh = t.seg < 0;
-        const int K = sh ? K_s : K_r;
+        const int K = t.sh ? K_s : K_r;
         const size_t rowb = WT ? (size_t)K / 2 : (size_t)K * 2;
         const size_t row = (size_t)t.e * (DOWN ? p.H : p.I) + t.rb * q.unit_rows + rg * kRows;
-        const uint8_t *m0 = DOWN ? (sh ? p.s_down : p.down) : (sh ? p.s_gate : p.gate);
-        const uint8_t *m1 = DOWN ? m0 + 16 * rowb : (sh ? p.s_up : p.up);
+        const uint8_t *m0 = DOWN ? (t.sh ? p.s_down : p.down) : (t.sh ? p.s_gate : p.gate);
+        const uint8_t *m1 = DOWN ? m0 + 16 * rowb : (t.sh ? p.s_up : p.up);
         f0 = m0 + (row + g) * rowb + t.s0 * kStepBytes + t4 * 16;
         f1 = m1 + (row + g) * rowb + t.s0 * kStepBytes + t4 * 16;
         f8 = 8 * rowb;
         if constexpr (WT) {
           const size_t sb = (size_t)K / 32;
-          const uint8_t *c0 = DOWN ? (sh ? p.s_down_scale : p.down_scale) : (sh ? p.s_gate_scale : p.gate_scale);
-          const uint8_t *c1 = DOWN ? c0 + 16 * sb : (sh ? p.s_up_scale : p.up_scale);
+          const uint8_t *c0 = DOWN ? (t.sh ? p.s_down_scale : p.down_scale) : (t.sh ? p.s_gate_scale : p.gate_scale);
+          const uint8_t *c1 = DOWN ? c0 + 16 * sb : (t.sh ? p.s_up_scale : p.up_scale);
           fsc = (lane < 16 ? c0 : c1) + (row + (lane & 15)) * sb + t.s0 * 4;
         }
         fs = 0;
@@ -299,9 +322,9 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
       }
     }
     cp_async_commit();
-    fslot = fslot + 1 == NST ? 0 : fslot + 1;
+    fslot = fslot + 1 == kNst ? 0 : fslot + 1;
   };
-  for (int i = 0; i < NST - 1; ++i) fill();
+  for (int i = 0; i < kNst - 1; ++i) fill();
 
   if (wait_for != nullptr && !grid_wait(p, wait_for, tb)) {
     ok = false;
@@ -309,211 +332,206 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
     return;
   }
 
-  // ---- the token operand of one step: this lane's 8 values of each group of 32, for column n
-  constexpr int NB = DOWN ? 2 * G : G;
-  auto load_b = [&](uint4 (&b)[NB], const Unit &t, int s, int n) {
-    if (n >= t.ntok) {
+  using Step = TokenStep<WT, DOWN>;
+  auto load_b = [&](Step &b, const Unit &t, int s) {
+    const int st = t.s0 + s, k0 = st * Fmt<WT>::kStep + t4 * 8;
+    if (g < t.ntok) {
+      if constexpr (DOWN) {
+        const size_t at = t.sh ? (size_t)p.S * p.I + (size_t)(t.row0 - p.S + g) * p.Is : (size_t)(t.row0 + g) * p.I;
+        if constexpr (WT) {
+          const uint4 *src = reinterpret_cast<const uint4 *>(p.act16 + at + k0);
 #pragma unroll
-      for (int i = 0; i < NB; ++i) b[i] = make_uint4(0u, 0u, 0u, 0u);
-      return;
-    }
-    const int k0 = (t.s0 + s) * Fmt<WT>::kStep + t4 * 8;
-    if constexpr (DOWN) {
-      const float *row = t.seg < 0 ? p.act_s + (size_t)n * p.Is : p.act + (size_t)(t.row0 + n) * p.I;
-      const uint4 *src = reinterpret_cast<const uint4 *>(row + k0);
+          for (int i = 0; i < G; ++i) b.v[i] = src[4 * i];
+        } else {
+          const uint4 *src = reinterpret_cast<const uint4 *>(p.act + at + k0);
+          b.v[0] = src[0];
+          b.v[1] = src[1];
+        }
+      } else {
+        const int tk = t.sh ? t.row0 - p.S + g : tb.tok[t.row0 + g];
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.x + (size_t)tk * p.H + k0);
 #pragma unroll
-      for (int i = 0; i < G; ++i) {
-        b[2 * i] = src[8 * i];
-        b[2 * i + 1] = src[8 * i + 1];
+        for (int i = 0; i < G; ++i) b.v[i] = src[4 * i];
       }
     } else {
-      const int tk = t.seg < 0 ? n : tb.tok[t.row0 + n];
-      const uint4 *src = reinterpret_cast<const uint4 *>(p.x + (size_t)tk * p.H + k0);
 #pragma unroll
-      for (int i = 0; i < G; ++i) b[i] = src[4 * i];
+      for (int i = 0; i < Step::kN; ++i) b.v[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if constexpr (DOWN && WT) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = min(2 * t4 + c, t.ntok - 1);
+        const size_t at = t.sh ? (size_t)p.S * p.I + (size_t)(t.row0 - p.S + col) * p.Is : (size_t)(t.row0 + col) * p.I;
+        b.ex[c] = *reinterpret_cast<const uint32_t *>(p.act_exp + at / 32 + 4 * st);
+      }
     }
   };
 
   int slot = 0, buf = 0;
+  Unit nxt = decode_unit(p, tb, q, blockIdx.x, warp, kRows);
+  Step bn;
+  if (nxt.n > 0) load_b(bn, nxt, 0);
   for (int u = blockIdx.x; u < q.units; u += gridDim.x) {
-    const Unit t = decode_unit(p, tb, q, u, warp, kRows);
-    const int nts = (t.ntok + 7) >> 3;
-    float acc[2][NT][4];
+    const Unit t = nxt;
+    nxt = decode_unit(p, tb, q, u + gridDim.x, warp, kRows);
+    float acc[2][4];
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[a][n][i] = 0.0f;
-    float bscale[NT];  // MXFP4 down: the activation row's power of two
-    if constexpr (WT && DOWN) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        bscale[n] = n * 8 + g < t.ntok ? fp16_scale(__ldcg(p.amax + t.row0 + n * 8 + g)) : 0.0f;
-    }
+      for (int i = 0; i < 4; ++i) acc[a][i] = 0.0f;
+    if (t.n == 0 && nxt.n > 0) load_b(bn, nxt, 0);
     for (int s = 0; s < t.n; ++s) {
-      cp_async_wait<NST - 2>();
+      const Step b = bn;
+      // the next step's token values, a step ahead of their use
+      if (s + 1 < t.n) load_b(bn, t, s + 1);
+      else if (nxt.n > 0) load_b(bn, nxt, 0);
+      cp_async_wait<kNst - 2>();
       __syncwarp();
       fill();  // into the slot read in the previous step
       const uint32_t st = my_ring + slot * STAGE;
-      slot = slot + 1 == NST ? 0 : slot + 1;
+      slot = slot + 1 == kNst ? 0 : slot + 1;
       const uint32_t wa = st + g * kStepBytes + t4 * 16;
       uint4 v[4];  // tile 0 rows g, g + 8; tile 1 rows g, g + 8
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = lds128(wa + i * 8 * kStepBytes);
-      uint32_t sc[4];
       if constexpr (WT) {
+        uint32_t sc[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[i] = lds32(st + kStageW + (i * 8 + g) * 4);
-      }
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (n < nts) {
-          uint4 b[NB];
-          load_b(b, t, s, n * 8 + g);
+        for (int gr = 0; gr < G; ++gr) {
+          float sx[2] = {1.0f, 1.0f};
+          if constexpr (DOWN) {
+            sx[0] = scale_of(b.ex[0], gr);
+            sx[1] = scale_of(b.ex[1], gr);
+          }
+          const uint4 bv = b.v[gr];
 #pragma unroll
-          for (int gr = 0; gr < G; ++gr) {
-            uint32_t bh[4], bl[4];
+          for (int a = 0; a < 2; ++a) {
+            uint32_t h0[4], h8[4];
+            e2m1x8_to_f16(word_of(v[2 * a], gr), h0);
+            e2m1x8_to_f16(word_of(v[2 * a + 1], gr), h8);
+            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma16<true>(part, h0[0], h8[0], h0[1], h8[1], bv.x, bv.y);
+            mma16<true>(part, h0[2], h8[2], h0[3], h8[3], bv.z, bv.w);
+            const float s0 = scale_of(sc[2 * a], gr), s8 = scale_of(sc[2 * a + 1], gr);
             if constexpr (DOWN) {
-              const uint4 x0 = b[2 * gr], x1 = b[2 * gr + 1];
-              const uint32_t xu[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float fa = __uint_as_float(xu[2 * i]), fb = __uint_as_float(xu[2 * i + 1]);
-                if constexpr (WT) {
-                  bh[i] = pack_f16(fa * bscale[n], fb * bscale[n]);
-                } else {
-                  // the fp32 activation as the sum of two bf16 values (16 of its 24 bits)
-                  bh[i] = pack_bf16(fa, fb);
-                  bl[i] = pack_bf16(fa - __uint_as_float(bh[i] << 16), fb - __uint_as_float(bh[i] & 0xFFFF0000u));
-                }
-              }
+              acc[a][0] = fmaf(s0 * sx[0], part[0], acc[a][0]);
+              acc[a][1] = fmaf(s0 * sx[1], part[1], acc[a][1]);
+              acc[a][2] = fmaf(s8 * sx[0], part[2], acc[a][2]);
+              acc[a][3] = fmaf(s8 * sx[1], part[3], acc[a][3]);
             } else {
-              bh[0] = b[gr].x, bh[1] = b[gr].y, bh[2] = b[gr].z, bh[3] = b[gr].w;
+              acc[a][0] = fmaf(s0, part[0], acc[a][0]);
+              acc[a][1] = fmaf(s0, part[1], acc[a][1]);
+              acc[a][2] = fmaf(s8, part[2], acc[a][2]);
+              acc[a][3] = fmaf(s8, part[3], acc[a][3]);
             }
+          }
+        }
+      } else {
+        uint32_t bh[4] = {b.v[0].x, b.v[0].y, b.v[0].z, b.v[0].w}, bl[4];
+        if constexpr (DOWN) {  // the fp32 activation as the sum of two bf16 values (16 of its 24 bits)
+          const uint4 x1 = b.v[1];
+          const uint32_t xu[8] = {bh[0], bh[1], bh[2], bh[3], x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
-              if constexpr (WT) {
-                const uint4 &r0 = v[2 * a], &r8 = v[2 * a + 1];
-                uint32_t h0[4], h8[4];
-                e2m1x8_to_f16(gr == 0 ? r0.x : gr == 1 ? r0.y : gr == 2 ? r0.z : r0.w, h0);
-                e2m1x8_to_f16(gr == 0 ? r8.x : gr == 1 ? r8.y : gr == 2 ? r8.z : r8.w, h8);
-                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma16<true>(part, h0[0], h8[0], h0[1], h8[1], bh[0], bh[1]);
-                mma16<true>(part, h0[2], h8[2], h0[3], h8[3], bh[2], bh[3]);
-                const float s0 = __uint_as_float((gr < 3 ? sc[2 * a] << (23 - 8 * gr) : sc[2 * a] >> 1) & 0x7F800000u);
-                const float s8 =
-                    __uint_as_float((gr < 3 ? sc[2 * a + 1] << (23 - 8 * gr) : sc[2 * a + 1] >> 1) & 0x7F800000u);
-                acc[a][n][0] = fmaf(s0, part[0], acc[a][n][0]);
-                acc[a][n][1] = fmaf(s0, part[1], acc[a][n][1]);
-                acc[a][n][2] = fmaf(s8, part[2], acc[a][n][2]);
-                acc[a][n][3] = fmaf(s8, part[3], acc[a][n][3]);
-              } else {
-                const uint4 &r0 = v[2 * a], &r8 = v[2 * a + 1];
-                mma16<false>(acc[a][n], r0.x, r8.x, r0.y, r8.y, bh[0], bh[1]);
-                mma16<false>(acc[a][n], r0.z, r8.z, r0.w, r8.w, bh[2], bh[3]);
-                if constexpr (DOWN) {
-                  mma16<false>(acc[a][n], r0.x, r8.x, r0.y, r8.y, bl[0], bl[1]);
-                  mma16<false>(acc[a][n], r0.z, r8.z, r0.w, r8.w, bl[2], bl[3]);
-                }
-              }
-            }
+          for (int i = 0; i < 4; ++i) {
+            const float fa = __uint_as_float(xu[2 * i]), fb = __uint_as_float(xu[2 * i + 1]);
+            bh[i] = pack_bf16(fa, fb);
+            bl[i] = pack_bf16(fa - __uint_as_float(bh[i] << 16), fb - __uint_as_float(bh[i] & 0xFFFF0000u));
+          }
+        }
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          const uint4 &r0 = v[2 * a], &r8 = v[2 * a + 1];
+          mma16<false>(acc[a], r0.x, r8.x, r0.y, r8.y, bh[0], bh[1]);
+          mma16<false>(acc[a], r0.z, r8.z, r0.w, r8.w, bh[2], bh[3]);
+          if constexpr (DOWN) {
+            mma16<false>(acc[a], r0.x, r8.x, r0.y, r8.y, bl[0], bl[1]);
+            mma16<false>(acc[a], r0.z, r8.z, r0.w, r8.w, bl[2], bl[3]);
           }
         }
       }
     }
 
-    // ---- the warps' partial products, then the sums in slice order
-    float *rd = red + buf * FewLayout<NT>::kRedFloats;
+    // ---- the warps' partial products, then the sums in slice order: a warp takes 32
+    // rows of one column, a lane each
+    float *rd = red + buf * kRedFloats;
+    buf ^= 1;
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (n < nts)
-          *reinterpret_cast<float4 *>(rd + ((warp * 2 + a) * NT + n) * 128 + lane * 4) =
-              make_float4(acc[a][n][0], acc[a][n][1], acc[a][n][2], acc[a][n][3]);
+    for (int a = 0; a < 2; ++a) {
+      float *d = rd + (warp * 2 + a) * kRedTile + 2 * t4 * kRedCol + g;
+      d[0] = acc[a][0];
+      d[kRedCol] = acc[a][1];
+      d[8] = acc[a][2];
+      d[kRedCol + 8] = acc[a][3];
+    }
     __syncthreads();
-    const int rgs = 1 << q.rg_shift;
-    const bool sh = t.seg < 0;
-    if constexpr (!DOWN) {
-      const int rows = sh ? q.rows_s : q.rows_r;
-      for (int o = threadIdx.x; o < (rgs * nts) << 7; o += kFewThreads) {
-        const int e = o & 127, nr = o >> 7, n = nr % nts, r = nr / nts;
-        const int c = e & 3, ln = e >> 2;
-        const int col = n * 8 + 2 * (ln & 3) + (c & 1), row = t.rb * q.unit_rows + r * 16 + (ln >> 2) + 8 * (c >> 1);
-        float a = 0.0f;
-        if (col < t.ntok && row < rows) {
-          float gs = 0.0f, us = 0.0f;
-          const float *src = rd + (r * q.ks * 2 * NT + n) * 128 + e;
-          for (int k = 0; k < q.ks; ++k, src += 2 * NT * 128) {
-            gs += src[0];
-            us += src[NT * 128];
-          }
+    const int groups = (DOWN ? 1 << q.rg_shift : (1 << q.rg_shift) >> 1) * t.ntok;  // (32 rows, column) pairs
+    for (int o = warp; o < groups; o += kFewWarps) {
+      const int blk = o / t.ntok, col = o - blk * t.ntok;
+      const int row = t.rb * q.unit_rows + blk * 32 + lane;
+      if constexpr (!DOWN) {
+        // rows of the two row groups 2 blk, 2 blk + 1
+        const float *src = rd + (2 * blk + (lane >> 4)) * q.ks * 2 * kRedTile + col * kRedCol + (lane & 15);
+        float gs = 0.0f, us = 0.0f;
+        for (int k = 0; k < q.ks; ++k, src += 2 * kRedTile) {
+          gs += src[0];
+          us += src[kRedTile];
+        }
+        const bool live = row < (t.sh ? q.rows_s : q.rows_r);  // whole blocks of 32 rows: I is a multiple of 64
+        if (live) {
+          const size_t at =
+              (t.sh ? (size_t)p.S * p.I + (size_t)(t.row0 - p.S + col) * p.Is : (size_t)(t.row0 + col) * p.I) + row;
           if constexpr (WT) {
-            const float un = __ldcg(p.x_unscale + (sh ? col : tb.tok[t.row0 + col]));
-            gs *= un;
-            us *= un;
+            const float un = __ldcg(p.x_unscale + (t.sh ? t.row0 - p.S + col : tb.tok[t.row0 + col]));
+            const float a = silu_mul(gs * un, us * un);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(a) & 0x7FFFFFFFu);
+            const __half h = __float2half_rn(a * fp16_scale(top));
+            p.act16[at] = __half_as_ushort(h);
+            if (lane == 0) p.act_exp[at / 32] = (uint8_t)(__float_as_uint(fp16_unscale(top)) >> 23);
+          } else {
+            p.act[at] = silu_mul(gs, us);
           }
-          a = silu_mul(gs, us);
-          (sh ? p.act_s + (size_t)col * p.Is : p.act + (size_t)(t.row0 + col) * p.I)[row] = a;
         }
-        if constexpr (WT) {  // the largest magnitude of each activation row: its four lanes' rows first
-          uint32_t m = __float_as_uint(a) & 0x7FFFFFFFu;
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
-          if ((lane & 18) == 0 && col < t.ntok) atomicMax(p.amax + t.row0 + col, m);
-        }
-      }
-    } else {
-      for (int o = threadIdx.x; o < (2 * rgs * nts) << 7; o += kFewThreads) {
-        const int e = o & 127, nr = o >> 7, n = nr % nts, ra = nr / nts, r = ra >> 1, a = ra & 1;
-        const int c = e & 3, ln = e >> 2;
-        const int col = n * 8 + 2 * (ln & 3) + (c & 1);
-        const int row = t.rb * q.unit_rows + r * 32 + a * 16 + (ln >> 2) + 8 * (c >> 1);
-        if (col < t.ntok && row < p.H) {
-          float y = 0.0f;
-          const float *src = rd + ((r * q.ks * 2 + a) * NT + n) * 128 + e;
-          for (int k = 0; k < q.ks; ++k, src += 2 * NT * 128) y += *src;
-          if constexpr (WT) y *= fp16_unscale(__ldcg(p.amax + t.row0 + col));
+      } else {
+        const float *src = rd + (blk * q.ks * 2 + (lane >> 4)) * kRedTile + col * kRedCol + (lane & 15);
+        float y = 0.0f;
+        for (int k = 0; k < q.ks; ++k, src += 2 * kRedTile) y += *src;
+        if (row < p.H) {
           if (p.y != nullptr) p.y[(size_t)(t.row0 + col) * p.H + row] = y;
-          else if (sh) p.y_shared[(size_t)col * p.H + row] = __float2bfloat16_rn(y);
+          else if (t.sh) p.y_shared[(size_t)(t.row0 - p.S + col) * p.H + row] = __float2bfloat16_rn(y);
           else p.y_sorted[(size_t)(t.row0 + col) * p.H + row] = __float2bfloat16_rn(y);
         }
       }
-      if (p.y != nullptr) {
-        // the last segment to finish a block of rows combines it, in slot order
-        __syncthreads();
-        if (threadIdx.x == 0) {
-          __threadfence();
-          tb.last = atomicAdd(p.done + t.rb, 1u) == (unsigned)(tb.nact + tb.nsh - 1);
-          __threadfence();
-        }
-        __syncthreads();
-        if (tb.last) {
-          const int w0 = t.rb * q.unit_rows, w1 = min(p.H, w0 + q.unit_rows), nw = (w1 - w0) >> 2;
-          for (int o = threadIdx.x; o < p.T * nw; o += kFewThreads) {
-            const int tk = o / nw, h = w0 + 4 * (o - tk * nw);
-            float4 s4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int j = 0; j < p.top_k; ++j) {
-              const float w = tb.w[tk * p.top_k + j];
-              const float4 y = __ldcg(
-                  reinterpret_cast<const float4 *>(p.y + (size_t)tb.pos[tk * p.top_k + j] * p.H + h));
-              s4 = make_float4(fmaf(w, y.x, s4.x), fmaf(w, y.y, s4.y), fmaf(w, y.z, s4.z), fmaf(w, y.w, s4.w));
-            }
-            if (tb.nsh) {
-              const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.y + (size_t)(p.S + tk) * p.H + h));
-              s4 = make_float4(s4.x + y.x, s4.y + y.y, s4.z + y.z, s4.w + y.w);
-            }
-            *reinterpret_cast<uint2 *>(p.out + (size_t)tk * p.H + h) =
-                make_uint2(pack_bf16(s4.x, s4.y), pack_bf16(s4.z, s4.w));
-          }
-        }
-      }
     }
-    if (FewLayout<NT>::kRedBufs == 1) __syncthreads();
-    else buf ^= 1;
   }
   cp_async_wait<0>();
+}
+
+// out[t] = sum_j w[t, j] y[pos(t, j)] + y_shared[t], in slot order, rounded once.
+// A warp takes 128 values of a token; warps are dealt out over the CTAs.
+__device__ void combine_rows(const FewParams &p, const FewTables &tb) {
+  const int lane = threadIdx.x & 31, h4 = p.H >> 2;
+  for (int o = (blockIdx.x + (int)gridDim.x * (threadIdx.x >> 5)) * 32 + lane; o < p.T * h4; o += gridDim.x * kFewThreads) {
+    const int tk = o / h4, h = 4 * (o - tk * h4);
+    float4 s4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), z = s4;
+    if (tb.nsh) z = __ldcg(reinterpret_cast<const float4 *>(p.y + (size_t)(p.S + tk) * p.H + h));
+    for (int j0 = 0; j0 < p.top_k; j0 += 8) {  // eight rows in flight
+      float4 y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < p.top_k)
+          y[j] = __ldcg(reinterpret_cast<const float4 *>(p.y + (size_t)tb.pos[tk * p.top_k + j0 + j] * p.H + h));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < p.top_k) {
+          const float w = tb.w[tk * p.top_k + j0 + j];
+          s4 = make_float4(fmaf(w, y[j].x, s4.x), fmaf(w, y[j].y, s4.y), fmaf(w, y[j].z, s4.z), fmaf(w, y[j].w, s4.w));
+        }
+    }
+    if (tb.nsh) s4 = make_float4(s4.x + z.x, s4.y + z.y, s4.z + z.z, s4.w + z.w);
+    *reinterpret_cast<uint2 *>(p.out + (size_t)tk * p.H + h) = make_uint2(pack_bf16(s4.x, s4.y), pack_bf16(s4.z, s4.w));
+  }
 }
 
 // ---- router logits of this CTA's experts, two at a time: each thread the same
@@ -602,51 +620,116 @@ __device__ void convert_token(const FewParams &p, int t, unsigned *top_smem) {
   __syncthreads();
 }
 
-// Selection and tables from the logits.
-__device__ void tables_from_logits(const FewParams &p, FewTables &tb, float *lg_smem) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = p.top_k;
-  for (int e = threadIdx.x; e < 256; e += kFewThreads) tb.mask[e] = 0u;
-  __syncthreads();
-  const TopkRule rule = {p.bias, p.E, k, p.score_mode, p.route_scale, p.renorm_eps};
-  float *lg = lg_smem + warp * 256;
-  for (int t = warp; t < p.T; t += kFewWarps) {
-    for (int e = lane; e < p.E; e += 32) lg[e] = __ldcg(p.logits + (size_t)t * p.E + e);
-    __syncwarp();
-    int e = 0;
-    float w = 0.0f;
-    warp_select_topk(rule, lg, lane, e, w);
-    if (lane < k) {
-      tb.idx[t * k + lane] = e;
-      tb.w[t * k + lane] = w;
-      atomicOr(&tb.mask[e], 1u << t);
-    }
-    __syncwarp();
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int rows = 0, act = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int e = e0 + lane, cnt = e < p.E ? __popc(tb.mask[e]) : 0;
-      int incl = cnt;
+// Segments and first positions from the experts' counts, one thread per expert
+// (threads 0..255; cnt is 0 past E).  Positions are counted on in expert order.
+__device__ __forceinline__ void build_segments(FewTables &tb, int cnt) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // positions in the low half, pieces of 8 in the high half of one scanned word
+  const int mine = cnt | (((cnt + 7) >> 3) << 16);
+  int incl = mine;
+  if (threadIdx.x < 256) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      const unsigned live = __ballot_sync(0xffffffffu, cnt > 0);
-      if (cnt > 0) {
-        const int a = act + __popc(live & ((1u << lane) - 1u));
-        tb.seg_e[a] = e;
-        tb.seg_row0[a] = tb.base[e] = rows + incl - cnt;
-      }
-      rows += __shfl_sync(0xffffffffu, incl, 31);
-      act += __popc(live);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
     }
-    if (lane == 0) {
-      tb.seg_row0[act] = rows;
-      tb.nact = act;
-    }
+    if (lane == 31) tb.scan[warp] = incl;
   }
+  __syncthreads();
+  if (threadIdx.x < 256) {
+    int before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) before += w < warp ? tb.scan[w] : 0;
+    const int row0 = before & 0xFFFF, a = before >> 16;
+    tb.base[threadIdx.x] = row0;
+    for (int i = 0; 8 * i < cnt; ++i) {
+      tb.seg_e[a + i] = threadIdx.x;
+      tb.seg_row0[a + i] = row0 + 8 * i;
+      tb.seg_n[a + i] = min(8, cnt - 8 * i);
+    }
+    if (threadIdx.x == 255) tb.nact = (before + mine) >> 16;
+  }
+}
+
+// An fp32 value as an integer of the same order.
+__device__ __forceinline__ int ordered(float f) {
+  const int b = __float_as_int(f);
+  return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+
+// Selection of one token by a warp, with the rule and results of the router.s top-k kernel: the
+// largest key each round by one integer reduction over the lanes, the lower of
+// equal experts by another.
+__device__ __forceinline__ void select_token(const FewParams &p, FewTables &tb, int t, const float (&bias)[8], int lane) {
+  const int E = p.E, k = p.top_k;
+  float v[8], sc[8];
+  int key[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = lane + 32 * j < E ? __ldcg(p.logits + (size_t)t * E + lane + 32 * j) : -INFINITY;
+  if (p.score_mode == MOE_SCORE_SIGMOID_BIAS) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sc[j] = 1.0f / (1.0f + expf(-v[j]));
+  } else {
+    float mx = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mx = fmaxf(mx, v[j]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      sc[j] = lane + 32 * j < E ? expf(v[j] - mx) : 0.0f;
+      sum += sc[j];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sc[j] = sc[j] / sum;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float kk = sc[j] + bias[j] + 0.0f;  // -0 as 0
+    key[j] = lane + 32 * j < E ? (kk == kk ? ordered(kk) : ordered(-INFINITY)) : INT_MIN;
+  }
+  int my_e = 0;
+  float my_s = 0.0f;
+#pragma unroll 1
+  for (int r = 0; r < k; ++r) {
+    int bk = INT_MIN, bj = 0;
+    float bs = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (key[j] > bk) {
+        bk = key[j];
+        bj = j;
+        bs = sc[j];
+      }
+    const int top = __reduce_max_sync(0xffffffffu, bk);
+    const int e = __reduce_min_sync(0xffffffffu, bk == top ? lane + 32 * bj : 0x7fffffff);
+    const float es = __shfl_sync(0xffffffffu, bs, e & 31);
+    if (lane == r) {
+      my_e = e;
+      my_s = es;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (e == lane + 32 * j) key[j] = INT_MIN;
+  }
+  float tot = lane < k ? my_s : 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+  if (lane < k) {
+    tb.idx[t * k + lane] = my_e;
+    tb.w[t * k + lane] = p.score_mode == MOE_SCORE_SIGMOID_BIAS ? my_s / tot * p.route_scale : my_s / fmaxf(tot, p.renorm_eps);
+    atomicOr(&tb.mask[my_e], 1u << t);
+  }
+}
+
+// Selection and tables from the logits (tb.mask is zero).
+__device__ void tables_from_logits(const FewParams &p, FewTables &tb, const float (&bias)[8]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = p.top_k;
+  for (int t = warp; t < p.T; t += kFewWarps) select_token(p, tb, t, bias, lane);
+  __syncthreads();
+  build_segments(tb, threadIdx.x < 256 ? __popc(tb.mask[threadIdx.x]) : 0);
   __syncthreads();
   for (int s = threadIdx.x; s < p.S; s += kFewThreads) {
     const int t = s / k, e = tb.idx[s];
@@ -659,38 +742,12 @@ __device__ void tables_from_logits(const FewParams &p, FewTables &tb, float *lg_
 
 // Tables from a given permutation.  Offsets that are not a partition of the slots
 // leave no routed work; slots out of range read token 0; both are recorded.
-__device__ void tables_from_perm(const FewParams &p, FewTables &tb, int cap) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) {
-    bool good = __ldg(p.offsets) == 0 && __ldg(p.offsets + p.E) == p.S;
-    for (int e = lane; e < p.E; e += 32) good = good && __ldg(p.offsets + e) <= __ldg(p.offsets + e + 1);
-    good = __all_sync(0xffffffffu, good);
-    int act = 0;
-    if (good) {
-      for (int e0 = 0; e0 < p.E; e0 += 32) {
-        const int e = e0 + lane;
-        const int lo = e < p.E ? __ldg(p.offsets + e) : 0, hi = e < p.E ? __ldg(p.offsets + e + 1) : 0;
-        const int pieces = (hi - lo + cap - 1) / cap;
-        int incl = pieces;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
-        }
-        for (int i = 0, a = act + incl - pieces; i < pieces; ++i, ++a) {
-          tb.seg_e[a] = e;
-          tb.seg_row0[a] = lo + i * cap;
-        }
-        act += __shfl_sync(0xffffffffu, incl, 31);
-      }
-    } else if (blockIdx.x == 0 && lane == 0) {
-      atomicOr(p.err, MOE_DEVERR_OFFSETS);
-    }
-    if (lane == 0) {
-      tb.seg_row0[act] = p.S;
-      tb.nact = act;
-    }
-  }
+__device__ void tables_from_perm(const FewParams &p, FewTables &tb) {
+  const int e = threadIdx.x;
+  const int lo = e <= p.E ? __ldg(p.offsets + e) : p.S, hi = e < p.E ? __ldg(p.offsets + e + 1) : lo;
+  const bool good = __syncthreads_and(hi >= lo && (e != 0 || lo == 0) && (e != p.E || lo == p.S));
+  if (!good && e == 0 && blockIdx.x == 0) atomicOr(p.err, MOE_DEVERR_OFFSETS);
+  build_segments(tb, good && e < 256 ? hi - lo : 0);
   for (int i = threadIdx.x; i < p.S; i += kFewThreads) {
     const int slot = __ldg(p.perm + i);
     int t = slot / p.top_k;
@@ -703,77 +760,91 @@ __device__ void tables_from_perm(const FewParams &p, FewTables &tb, int cap) {
   __syncthreads();
 }
 
-template <int WT, int NT>
+// The shared expert's weights into L2 while the routing is found: none of them
+// depends on it, and the memory is idle then.
+template <int WT>
+__device__ void prefetch_shared(const FewParams &p) {
+  constexpr unsigned kPiece = 8192;
+  const size_t n = (size_t)p.Is * p.H * (WT ? 1 : 4) / 2;  // bytes of one matrix, a multiple of 16
+  const uint8_t *m[3] = {p.s_gate, p.s_up, p.s_down};
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    for (size_t at = ((size_t)blockIdx.x * 32 + (threadIdx.x & 31)) * kPiece; at < n; at += (size_t)gridDim.x * 32 * kPiece)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(m[i] + at), "r"((unsigned)min((size_t)kPiece, n - at))
+                   : "memory");
+}
+
+template <int WT>
 struct FewSmem {
-  static constexpr int kRing = kFewWarps * FewLayout<NT>::kNst * Fmt<WT>::kStage;
-  static constexpr int kRed = FewLayout<NT>::kRedBufs * FewLayout<NT>::kRedFloats * 4;
-  static constexpr int kTables = (int)sizeof(FewTables);
-  static constexpr int kBytes = kRing + kRed + kTables;
+  static constexpr int kRing = kFewWarps * kNst * Fmt<WT>::kStage;
+  static constexpr int kRed = 2 * kRedFloats * 4;
+  static constexpr int kBytes = kRing + kRed + (int)sizeof(FewTables);
   static_assert(kBytes <= 232448, "shared memory budget");
-  static_assert(kRed >= kFewWarps * 256 * 4, "the logits' staging shares the reduction buffer");
 };
 
 }  // namespace
 
-template <int WT, int NT>
+template <int WT>
 __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_constant__ FewParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  using L = FewSmem<WT, NT>;
+  using L = FewSmem<WT>;
   uint8_t *ring = smem;
   float *red = reinterpret_cast<float *>(smem + L::kRing);
   FewTables &tb = *reinterpret_cast<FewTables *>(smem + L::kRing + L::kRed);
-  unsigned *bar0 = p.sync + kSyncFew, *bar1 = p.sync + kSyncFew + 1, *exits = p.sync + kSyncFew + 2;
+  unsigned *bar = p.sync + kSyncFew, *exits = bar + 3;
+  const bool route = p.router_w != nullptr;
   if (threadIdx.x == 0) {
     tb.abort_flag = 0;
-    tb.nsh = p.has_shared ? 1 : 0;
+    tb.nsh = p.has_shared ? (p.T + 7) >> 3 : 0;
   }
-  // counters and maxima of this call
-  if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i < p.S + p.T; i += kFewThreads) p.amax[i] = 0u;
-    for (int i = threadIdx.x; i < (p.H + 31) / 32; i += kFewThreads) p.done[i] = 0u;
+  if (threadIdx.x < 256) tb.mask[threadIdx.x] = 0u;
+  float bias[8];  // of this lane's experts, wanted after the first wait
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int e = (threadIdx.x & 31) + 32 * j;
+    bias[j] = p.bias != nullptr && e < p.E ? __ldg(p.bias + e) : 0.0f;
   }
   if (WT)
     for (int t = gridDim.x - 1 - blockIdx.x; t < p.T; t += gridDim.x) convert_token(p, t, reinterpret_cast<unsigned *>(red));
   __syncthreads();
-  if (p.router_w != nullptr) router_rows(p, red);
-  grid_arrive(bar0);
-  bool ok = grid_wait(p, bar0, tb);
+  if (route) router_rows(p, red);
+  if (route || WT) grid_arrive(bar);
+  if (p.has_shared && threadIdx.x < 32) prefetch_shared<WT>(p);
+  if (!route) tables_from_perm(p, tb);
+  bool ok = true;
+  if (route || WT) ok = grid_wait(p, bar, tb);
   if (ok) {
-    if (p.router_w != nullptr) tables_from_logits(p, tb, red);
-    else tables_from_perm(p, tb, 8 * NT);
-    run_phase<WT, NT, false>(p, tb, ring, red, nullptr, ok);
-    __syncthreads();
+    if (route) tables_from_logits(p, tb, bias);
+    run_phase<WT, false>(p, tb, ring, red, nullptr, ok);
   }
-  grid_arrive(bar1);  // also after a wait that ran out: the others need not wait for theirs to do so
-  if (ok) run_phase<WT, NT, true>(p, tb, ring, red, bar1, ok);
+  grid_arrive(bar + 1);  // also after a wait that ran out: the others need not wait for theirs to do so
+  if (ok) run_phase<WT, true>(p, tb, ring, red, bar + 1, ok);
+  if (route) {
+    grid_arrive(bar + 2);
+    if (ok && grid_wait(p, bar + 2, tb)) combine_rows(p, tb);
+  }
   __syncthreads();
   // the last CTA out zeroes the counters
   if (threadIdx.x == 0) {
     __threadfence();
     if (atomicAdd(exits, 1u) == gridDim.x - 1) {
-      volatile unsigned *s = p.sync + kSyncFew;
-      s[0] = s[1] = 0;
+      volatile unsigned *s = bar;
+      s[0] = s[1] = s[2] = 0;
       __threadfence();
-      s[2] = 0;
+      s[3] = 0;
     }
   }
 }
 
 namespace {
-template <int WT, int NT>
-cudaError_t launch_few_one(const FewParams &p, int num_ctas, cudaStream_t stream) {
-  using L = FewSmem<WT, NT>;
-  static thread_local unsigned long long attr_ctx = 0;
-  const cudaError_t e = set_smem_attr_once((const void *)few_kernel<WT, NT>, L::kBytes, attr_ctx);
-  if (e != cudaSuccess) return e;
-  void *args[] = {(void *)&p};
-  return launch_coop((const void *)few_kernel<WT, NT>, dim3(num_ctas), dim3(kFewThreads), L::kBytes, stream, args);
-}
 template <int WT>
 cudaError_t launch_few_wt(const FewParams &p, int num_ctas, cudaStream_t stream) {
-  if (p.T <= 8) return launch_few_one<WT, 1>(p, num_ctas, stream);
-  if (p.T <= 16) return launch_few_one<WT, 2>(p, num_ctas, stream);
-  return launch_few_one<WT, 4>(p, num_ctas, stream);
+  using L = FewSmem<WT>;
+  static thread_local unsigned long long attr_ctx = 0;
+  const cudaError_t e = set_smem_attr_once((const void *)few_kernel<WT>, L::kBytes, attr_ctx);
+  if (e != cudaSuccess) return e;
+  void *args[] = {(void *)&p};
+  return launch_coop((const void *)few_kernel<WT>, dim3(num_ctas), dim3(kFewThreads), L::kBytes, stream, args);
 }
 }  // namespace
 

@@ -101,7 +101,7 @@ struct GemmParams {
 // word offsets into the workspace header (4 KiB, zero when the workspace is fresh;
 // every launch leaves them zero again)
 constexpr int kSyncClaim = 64, kSyncExit = 65, kSyncPermute = 66,
-              kSyncFew = 67,     // the one-kernel layer's two grid-wide waits and its exit counter
+              kSyncFew = 67,     // the one-kernel layer's three grid-wide waits and its exit counter
               kSyncDone = 128,   // kSyncDone .. + 257: gate/up tiles finished, per segment
               kSyncQuant = 512;  // kSyncQuant .. + 257: W8A8 quantisation tiles finished, per segment
 constexpr int kWsHeaderBytes = 4096;
@@ -134,7 +134,7 @@ cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales,
                                     cudaStream_t stream);
 
 // ------------------------------------------------- the layer for few tokens
-constexpr int kFewMaxT = 32;  // a token per bit of an expert's mask; four 8-token operand tiles
+constexpr int kFewMaxT = 32;  // a token per bit of an expert's mask
 struct FewParams {
   const __nv_bfloat16 *hidden;  // [T][H]
   const uint16_t *x;            // the products' token operand: hidden, or x16 with MXFP4 weights
@@ -147,10 +147,13 @@ struct FewParams {
   const uint8_t *gate, *up, *down, *s_gate, *s_up, *s_down;
   const uint8_t *gate_scale, *up_scale, *down_scale, *s_gate_scale, *s_up_scale, *s_down_scale;
   float *logits;       // [T][E]
-  float *act, *act_s;  // [S][I], [T][Is] fp32 activations
-  unsigned *amax;      // [S + T] MXFP4: each activation row's largest magnitude (fp32 bits)
+  // activations, routed [S][I] then shared [T][Is]: fp32, or with MXFP4 weights fp16
+  // times a power of two per block of 32 and the blocks' exponent bytes (2^(e - 127)
+  // undoes it)
+  float *act;
+  uint16_t *act16;
+  uint8_t *act_exp;
   float *y;            // [S + T][H] fp32 outputs of every position, then of the shared expert; nullptr: write y_sorted
-  unsigned *done;      // finished segments per block of rows of y
   __nv_bfloat16 *out;                  // [T][H]
   __nv_bfloat16 *y_sorted, *y_shared;  // [S][H], [T][H]
   unsigned *err, *sync;

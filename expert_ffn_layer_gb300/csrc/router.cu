@@ -19,7 +19,6 @@
 //           shuffles, renormalises.
 #include "internal.h"
 #include "ptx.cuh"
-#include "topk.cuh"
 
 namespace moe {
 
@@ -33,6 +32,10 @@ constexpr int kXTileBytes = 128 * 128;  // 128 rows x 64 bf16
 // lowest kept bit.  Returns the rounded value as fp32 bits (low half zero).
 __device__ __forceinline__ uint32_t bf16_rne_bits(uint32_t u) {
   return (u + 0x7FFFu + ((u >> 16) & 1u)) & 0xFFFF0000u;
+}
+
+__device__ __forceinline__ bool better(float k1, int e1, float k2, int e2) {
+  return k1 > k2 || (k1 == k2 && e1 < e2);
 }
 
 }  // namespace
@@ -202,13 +205,83 @@ __global__ void __launch_bounds__(kRouterThreads, 1) router_gemm_kernel(const __
 // ------------------------------------------------------------------ topk
 // Scoring and top-k selection of token t by one warp from its logits lg[0..E).
 __device__ __forceinline__ void select_topk(const RouterParams &p, const float *lg, int t, int lane) {
-  const TopkRule rule = {p.bias, p.E, p.top_k, p.score_mode, p.route_scale, p.renorm_eps};
-  int e = 0;
-  float w = 0.0f;
-  warp_select_topk(rule, lg, lane, e, w);
-  if (lane < p.top_k) {
-    p.topk_idx[(size_t)t * p.top_k + lane] = e;
-    p.topk_w[(size_t)t * p.top_k + lane] = w;
+  const int E = p.E, k = p.top_k;
+  const int nj = (E + 31) >> 5;
+  float v[8], key[8], sc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = (j < nj && lane + 32 * j < E) ? lg[lane + 32 * j] : 0.0f;
+  if (p.score_mode == MOE_SCORE_SIGMOID_BIAS) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int e = lane + 32 * j;
+      const float s = 1.0f / (1.0f + expf(-v[j]));
+      const float kk = s + ((p.bias != nullptr && j < nj && e < E) ? p.bias[e] : 0.0f);
+      sc[j] = s;
+      key[j] = (kk == kk) ? kk : -INFINITY;
+    }
+  } else {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < nj && lane + 32 * j < E) mx = fmaxf(mx, v[j]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    float ex[8], sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      ex[j] = (j < nj && lane + 32 * j < E) ? expf(v[j] - mx) : 0.0f;
+      sum += ex[j];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      sc[j] = ex[j] / sum;
+      key[j] = (sc[j] == sc[j]) ? sc[j] : -INFINITY;
+    }
+  }
+  uint32_t taken = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (!(j < nj && lane + 32 * j < E)) taken |= 1u << j;
+  int my_e = 0;
+  float my_s = 0.0f;
+  for (int rnd = 0; rnd < k; ++rnd) {
+    float bk = -INFINITY, bs = 0.0f;
+    int be = 0x7fffffff;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int e = lane + 32 * j;
+      if (!((taken >> j) & 1u) && better(key[j], e, bk, be)) {
+        bk = key[j];
+        be = e;
+        bs = sc[j];
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float ok2 = __shfl_xor_sync(0xffffffffu, bk, o);
+      const int oe = __shfl_xor_sync(0xffffffffu, be, o);
+      const float os = __shfl_xor_sync(0xffffffffu, bs, o);
+      if (better(ok2, oe, bk, be)) {
+        bk = ok2;
+        be = oe;
+        bs = os;
+      }
+    }
+    if (be < E && (be & 31) == lane) taken |= 1u << (be >> 5);
+    if (lane == rnd) {
+      my_e = be < E ? be : 0;
+      my_s = bs;
+    }
+  }
+  float tot = lane < k ? my_s : 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+  if (lane < k) {
+    const float w = p.score_mode == MOE_SCORE_SIGMOID_BIAS ? my_s / tot * p.route_scale : my_s / fmaxf(tot, p.renorm_eps);
+    p.topk_idx[(size_t)t * k + lane] = my_e;
+    p.topk_w[(size_t)t * k + lane] = w;
   }
 }
 

@@ -213,10 +213,11 @@ def test_few_two_calls_at_once():
     ref = few(dl).clone()
     ws2 = moe.alloc_workspace(dl.d)
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
-    torch.cuda.synchronize()
-    outs = []
-    for _ in range(10):
-        outs += [few(dl, stream=s1, out=torch.zeros_like(ref)), few(dl, stream=s2, out=torch.zeros_like(ref), ws=ws2)]
+    outs = [torch.zeros_like(ref) for _ in range(80)]
+    torch.cuda.synchronize()  # the zeros are written on the default stream
+    for i in range(0, len(outs), 2):
+        few(dl, stream=s1, out=outs[i])
+        few(dl, stream=s2, out=outs[i + 1], ws=ws2)
     torch.cuda.synchronize()
     assert all(torch.equal(o, ref) for o in outs)
 
