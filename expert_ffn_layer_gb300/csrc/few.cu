@@ -44,6 +44,7 @@ namespace {
 constexpr int kFewWarps = 16, kFewThreads = kFewWarps * 32;
 constexpr int kStepBytes = 64;               // bytes of one row in a step
 constexpr int kStageW = 32 * kStepBytes;     // 32 rows: two 16-row operand tiles
+static_assert(kFewMaxT <= 2 * kFewWarps, "two tokens a warp in the selection");
 constexpr int kMaxPos = kFewMaxT * 16 + kFewMaxT;  // routed positions and shared rows
 constexpr int kMaxSegs = 256 + kFewMaxT * 16 / 8;
 
@@ -54,7 +55,7 @@ struct Fmt {  // weights: 0 bf16, 1 MXFP4
   static constexpr int kStage = kStageW + (WT ? 128 : 0);  // with the 32 rows' four scale bytes
 };
 
-constexpr int kNst = 4;         // steps of a warp's ring
+constexpr int kNst = 4;         // steps of a warp's ring (a power of two)
 constexpr int kRedCol = 20;     // floats from one column of a partial 16 x 8 tile to the next (16 rows: no bank conflicts)
 constexpr int kRedTile = 8 * kRedCol;
 constexpr int kRedFloats = kFewWarps * 2 * kRedTile;  // one of two buffers
@@ -105,15 +106,24 @@ template <bool HALF>
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                       uint32_t b1) {
   if constexpr (HALF)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// D = A B in fp16 operands, K = 16.
+__device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // The power of two that brings a largest magnitude (its fp32 bits) into
@@ -172,39 +182,39 @@ __device__ __forceinline__ bool grid_wait(const FewParams &p, unsigned *counter,
   return tb.abort_flag == 0;
 }
 
-// Units of one phase and how the warps share one.
+// How the warps share the units of one phase.  A unit is 32 rows of one segment
+// (32 pairs of rows for gate/up); a team of warps takes one: KS slices of K, and for
+// gate/up two warps a slice (16 gate and 16 up rows each).  The CTA's teams go their
+// own ways, each with its own units and its own barrier.
 struct Plan {
-  int ks, rg_shift;   // K slices, log2 of the row groups
-  int unit_rows;      // rows (pairs of rows for gate/up) of a unit
-  int rows_r, rows_s; // rows of a routed / the shared expert
-  int rb_r, rb_s;     // units of a segment of each
+  int ks, ks_shift;   // K slices and their log2
+  int tw_shift;       // log2 of a team's warps
+  int rows_r, rows_s; // rows of a routed / the shared expert, multiples of 32
   int steps_r, steps_s;
-  int n_sh, units;    // units of the shared expert (they come first), and all
+  int units;
 };
 
-// KS by the shortest makespan: rounds of units over the CTAs, each as long as its
+// KS by the shortest makespan: rounds of units over the teams, each as long as its
 // warps' steps (about 1400 cycles of the SM's share of the memory rate, 16 warps
 // together) and the exchange of partial products (about 300).
 template <bool DOWN>
 __device__ Plan make_plan(const FewTables &tb, int rows_r, int rows_s, int steps_r, int steps_s) {
   Plan best = {};
   int best_cost = 0x7fffffff;
-  for (int sh = DOWN ? 0 : 1; sh <= 4; ++sh) {  // RG = 2^sh; gate/up units are whole blocks of 32 activations
+  for (int sh = 0; sh <= (DOWN ? 4 : 3); ++sh) {
     Plan q;
-    q.rg_shift = sh;
-    q.ks = kFewWarps >> sh;
-    q.unit_rows = (DOWN ? 32 : 16) << sh;
+    q.ks = 1 << sh;
+    q.ks_shift = sh;
+    q.tw_shift = DOWN ? sh : sh + 1;
     q.rows_r = rows_r;
     q.rows_s = rows_s;
     q.steps_r = steps_r;
     q.steps_s = steps_s;
-    q.rb_r = (rows_r + q.unit_rows - 1) / q.unit_rows;
-    q.rb_s = (rows_s + q.unit_rows - 1) / q.unit_rows;
-    q.n_sh = tb.nsh * q.rb_s;
-    q.units = q.n_sh + tb.nact * q.rb_r;
-    const int rounds = (q.units + gridDim.x - 1) / gridDim.x;
-    const int cost = rounds * (((max(steps_r, tb.nsh ? steps_s : 0) + q.ks - 1) / q.ks) * 1400 + 300);
-    if (cost < best_cost) {
+    q.units = (tb.nsh * rows_s + tb.nact * rows_r) >> 5;
+    const int teams = gridDim.x * (kFewWarps >> q.tw_shift);
+    const int rounds = (q.units + teams - 1) / teams;
+    const int cost = rounds * (((max(steps_r, tb.nsh ? steps_s : 0) + q.ks - 1) >> sh) * 1400 + 300);
+    if (cost <= best_cost) {
       best_cost = cost;
       best = q;
     }
@@ -212,99 +222,100 @@ __device__ Plan make_plan(const FewTables &tb, int rows_r, int rows_s, int steps
   return best;
 }
 
+// One of a team's units, for one of its warps.
 struct Unit {
-  bool sh;           // of the shared expert
-  int e;             // expert (0 for the shared one)
-  int rb, row0, ntok;
-  int s0, n;         // this warp's first step and its number of steps
+  int w_row;           // the unit's first row of the stacked weight matrix
+  int sh, row0, ntok;  // of the shared expert; first position; number of positions (0: past the last unit)
+  int row;             // the unit's first row in its expert
+  int s0, n;           // this warp's first step and its number of steps
 };
 
-__device__ __forceinline__ Unit decode_unit(const FewParams &p, const FewTables &tb, const Plan &q, int u, int warp,
-                                            int warp_rows) {
-  Unit t;
-  if (u >= q.units) {
-    t.n = 0;
-    t.ntok = 0;
+// A team's units in order, decoded 32 at a time, one by each lane of a warp, and
+// read by shuffles -- which also tells the compiler that they are the warp's, not
+// the lane's.  Packed: positions (4 bits), first position (10), first row / 32 (10), shared (1).
+struct UnitList {
+  int base, w_row, word;
+
+  // unit i of the list is number team + i * teams of the phase
+  __device__ __forceinline__ void decode(const FewTables &tb, const Plan &q, int S, int T, int team, int teams, int first,
+                                         int lane) {
+    base = first;
+    const int u = team + (first + lane) * teams, rb_s = q.rows_s >> 5, rb_r = q.rows_r >> 5, n_sh = tb.nsh * rb_s;
+    word = 0;
+    w_row = 0;
+    if (u < n_sh) {
+      const int seg = u / rb_s, rb = u - seg * rb_s;
+      w_row = rb * 32;
+      word = min(8, T - 8 * seg) | (S + 8 * seg) << 4 | rb << 14 | 1 << 24;
+    } else if (u < q.units) {
+      const int v = u - n_sh, seg = v / rb_r, rb = v - seg * rb_r;
+      w_row = tb.seg_e[seg] * q.rows_r + rb * 32;
+      word = tb.seg_n[seg] | tb.seg_row0[seg] << 4 | rb << 14;
+    }
+  }
+  // unit i, 0 <= i - base < 32
+  __device__ __forceinline__ Unit get(int i, const int (&s0)[2], const int (&n)[2]) const {
+    Unit t;
+    const int x = __shfl_sync(0xffffffffu, word, i - base);
+    t.w_row = __shfl_sync(0xffffffffu, w_row, i - base);
+    t.ntok = x & 15;
+    t.row0 = x >> 4 & 1023;
+    t.row = (x >> 14 & 1023) << 5;
+    t.sh = x >> 24;
+    t.s0 = t.sh ? s0[1] : s0[0];
+    t.n = t.ntok == 0 ? 0 : t.sh ? n[1] : n[0];
     return t;
   }
-  int steps, rows;
-  t.sh = u < q.n_sh;
-  if (t.sh) {  // pieces innermost: the units that read the same weights run together
-    t.rb = u / tb.nsh;
-    const int piece = u - t.rb * tb.nsh;
-    t.e = 0;
-    t.row0 = p.S + 8 * piece;
-    t.ntok = min(8, p.T - 8 * piece);
-    steps = q.steps_s;
-    rows = q.rows_s;
-  } else {
-    const int v = u - q.n_sh, seg = v / q.rb_r;
-    t.rb = v - seg * q.rb_r;
-    t.e = tb.seg_e[seg];
-    t.row0 = tb.seg_row0[seg];
-    t.ntok = tb.seg_n[seg];
-    steps = q.steps_r;
-    rows = q.rows_r;
-  }
-  const int ks = warp & (q.ks - 1), rg = warp / q.ks;
-  t.s0 = steps * ks / q.ks;
-  t.n = steps * (ks + 1) / q.ks - t.s0;
-  if (t.rb * q.unit_rows + rg * warp_rows >= rows) t.n = 0;  // past the expert's last rows
-  return t;
-}
-
-// The token operand of one step in registers: this lane's 8 values of each group
-// of 32, for column g; MXFP4 down also the groups' exponents for columns 2 t, 2 t + 1.
-template <int WT, bool DOWN>
-struct TokenStep {
-  static constexpr int kN = (DOWN && !WT) ? 2 * Fmt<WT>::kGroups : Fmt<WT>::kGroups;
-  uint4 v[kN];
-  uint32_t ex[2];
 };
 
 // One phase over this CTA's units.  DOWN: the products with w_down, else gate/up.
 template <int WT, bool DOWN>
 __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, float *red, unsigned *wait_for, bool &ok) {
   constexpr int G = Fmt<WT>::kGroups, STAGE = Fmt<WT>::kStage;
-  constexpr int kRows = DOWN ? 32 : 16;  // rows a warp's unit advances by
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const int K_r = DOWN ? p.I : p.H, K_s = DOWN ? p.Is : p.H;
   const Plan q = make_plan<DOWN>(tb, DOWN ? p.H : p.I, DOWN ? p.H : p.Is, K_r / Fmt<WT>::kStep, K_s / Fmt<WT>::kStep);
-  const int rg = warp / q.ks;
+  const int tw = 1 << q.tw_shift, wi = warp & (tw - 1);  // the team's warps, this one's place
+  const int ks = wi & (q.ks - 1), off = DOWN ? 0 : (wi >> q.ks_shift) * 16;  // K slice; first row in the unit
+  const int tm = warp >> q.tw_shift, teams = gridDim.x * (kFewWarps >> q.tw_shift), team = tm * gridDim.x + blockIdx.x;
+  const int s0[2] = {q.steps_r * ks >> q.ks_shift, q.steps_s * ks >> q.ks_shift};
+  const int ns[2] = {(q.steps_r * (ks + 1) >> q.ks_shift) - s0[0], (q.steps_s * (ks + 1) >> q.ks_shift) - s0[1]};
+  const int mine = q.units > team ? (q.units - 1 - team) / teams + 1 : 0;
+  UnitList list, flist;  // of the products and of the weight stream ahead of them
+  list.decode(tb, q, p.S, p.T, team, teams, 0, lane);
+  flist = list;
   const uint32_t my_ring = smem_u32(ring) + warp * kNst * STAGE;
 
-  // ---- the weight stream: position (unit, step) of the next step to copy
-  int fu = blockIdx.x, fs = 0, fn = 0, fslot = 0;
+  // ---- the weight stream: the unit and step to copy next
+  int fi = 0, fs = 0, fn = 0, fslot = 0;
   const uint8_t *f0 = nullptr, *f1 = nullptr, *fsc = nullptr;
-  size_t f8 = 0;  // bytes from a row to the one eight below
-  auto f_unit = [&]() {  // settle on the next unit in which this warp has steps
-    while (fu < q.units) {
-      const Unit t = decode_unit(p, tb, q, fu, warp, kRows);
-      if (t.n > 0) {
-        const int K = t.sh ? K_s : K_r;
-        const size_t rowb = WT ? (size_t)K / 2 : (size_t)K * 2;
-        const size_t row = (size_t)t.e * (DOWN ? p.H : p.I) + t.rb * q.unit_rows + rg * kRows;
-        const uint8_t *m0 = DOWN ? (t.sh ? p.s_down : p.down) : (t.sh ? p.s_gate : p.gate);
-        const uint8_t *m1 = DOWN ? m0 + 16 * rowb : (t.sh ? p.s_up : p.up);
-        f0 = m0 + (row + g) * rowb + t.s0 * kStepBytes + t4 * 16;
-        f1 = m1 + (row + g) * rowb + t.s0 * kStepBytes + t4 * 16;
-        f8 = 8 * rowb;
-        if constexpr (WT) {
-          const size_t sb = (size_t)K / 32;
-          const uint8_t *c0 = DOWN ? (t.sh ? p.s_down_scale : p.down_scale) : (t.sh ? p.s_gate_scale : p.gate_scale);
-          const uint8_t *c1 = DOWN ? c0 + 16 * sb : (t.sh ? p.s_up_scale : p.up_scale);
-          fsc = (lane < 16 ? c0 : c1) + (row + (lane & 15)) * sb + t.s0 * 4;
-        }
-        fs = 0;
-        fn = t.n;
-        return;
-      }
-      fu += gridDim.x;
-    }
-  };
-  f_unit();
+  uint32_t f8 = 0;  // bytes from a row to the one eight below
   auto fill = [&]() {  // copy one step and commit it (an empty group past the end)
-    if (fu < q.units) {
+    if (fs == fn) {    // on to the next unit in which this warp has steps
+      fs = fn = 0;
+      while (fi < mine && fn == 0) {
+        if (fi - flist.base == 32) flist.decode(tb, q, p.S, p.T, team, teams, fi, lane);
+        const Unit f = flist.get(fi++, s0, ns);
+        fn = f.n;
+        if (fn > 0) {
+          const int K = f.sh ? K_s : K_r;
+          const uint32_t rowb = WT ? K / 2 : K * 2;
+          const uint8_t *m0 = DOWN ? (f.sh ? p.s_down : p.down) : (f.sh ? p.s_gate : p.gate);
+          const uint8_t *m1 = DOWN ? m0 + 16 * rowb : (f.sh ? p.s_up : p.up);
+          const size_t at = (size_t)(f.w_row + off + g) * rowb + f.s0 * kStepBytes + t4 * 16;
+          f0 = m0 + at;
+          f1 = m1 + at;
+          f8 = 8 * rowb;
+          if constexpr (WT) {
+            const uint32_t sb = K / 32;
+            const uint8_t *c0 = DOWN ? (f.sh ? p.s_down_scale : p.down_scale) : (f.sh ? p.s_gate_scale : p.gate_scale);
+            const uint8_t *c1 = DOWN ? c0 + 16 * sb : (f.sh ? p.s_up_scale : p.up_scale);
+            fsc = (lane < 16 ? c0 : c1) + (size_t)(f.w_row + off + (lane & 15)) * sb + f.s0 * 4;
+          }
+        }
+      }
+    }
+    if (fs < fn) {
       const uint32_t d = my_ring + fslot * STAGE + g * kStepBytes + t4 * 16;
       cp_async16(d, f0);
       cp_async16(d + 8 * kStepBytes, f0 + f8);
@@ -316,14 +327,12 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
         cp_async4(my_ring + fslot * STAGE + kStageW + lane * 4, fsc);
         fsc += 4;
       }
-      if (++fs == fn) {
-        fu += gridDim.x;
-        f_unit();
-      }
+      ++fs;
     }
     cp_async_commit();
-    fslot = fslot + 1 == kNst ? 0 : fslot + 1;
+    fslot = (fslot + 1) & (kNst - 1);
   };
+#pragma unroll 1
   for (int i = 0; i < kNst - 1; ++i) fill();
 
   if (wait_for != nullptr && !grid_wait(p, wait_for, tb)) {
@@ -332,64 +341,85 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
     return;
   }
 
-  using Step = TokenStep<WT, DOWN>;
-  auto load_b = [&](Step &b, const Unit &t, int s) {
-    const int st = t.s0 + s, k0 = st * Fmt<WT>::kStep + t4 * 8;
-    if (g < t.ntok) {
-      if constexpr (DOWN) {
-        const size_t at = t.sh ? (size_t)p.S * p.I + (size_t)(t.row0 - p.S + g) * p.Is : (size_t)(t.row0 + g) * p.I;
-        if constexpr (WT) {
-          const uint4 *src = reinterpret_cast<const uint4 *>(p.act16 + at + k0);
+  // ---- the token operand: this lane's 8 values of each group of 32, for column g
+  // (columns past the segment's repeat its last: their sums are not read), a step
+  // ahead of their use.  MXFP4: each register is loaded anew as soon as the step has
+  // used it; bf16, whose steps are a quarter as long: a second set of registers.
+  constexpr int kB = (DOWN && !WT) ? 2 * G : G;
+  uint4 bv[kB];
+  uint32_t ex[2] = {0u, 0u};            // MXFP4 down: the groups' exponents for columns 2 t, 2 t + 1
+  const uint4 *bp = nullptr;            // the next values to load
+  const uint32_t *xp[2] = {nullptr, nullptr};
+  auto point = [&](const Unit &u) {  // bp and xp at a unit's first step
+    const int col = min(g, u.ntok - 1);
+    const int k0 = u.s0 * Fmt<WT>::kStep + t4 * 8;
+    if constexpr (DOWN) {
+      // first value of position row0, and values from a position to the next
+      const size_t at = u.sh ? (size_t)p.S * p.I + (size_t)(u.row0 - p.S) * p.Is : (size_t)u.row0 * p.I;
+      const int ld = u.sh ? p.Is : p.I;
+      if constexpr (WT) {
+        bp = reinterpret_cast<const uint4 *>(p.act16 + at + (size_t)col * ld + k0);
 #pragma unroll
-          for (int i = 0; i < G; ++i) b.v[i] = src[4 * i];
-        } else {
-          const uint4 *src = reinterpret_cast<const uint4 *>(p.act + at + k0);
-          b.v[0] = src[0];
-          b.v[1] = src[1];
-        }
+        for (int c = 0; c < 2; ++c)
+          xp[c] = reinterpret_cast<const uint32_t *>(p.act_exp + (at + (size_t)min(2 * t4 + c, u.ntok - 1) * ld) / 32) + u.s0;
       } else {
-        const int tk = t.sh ? t.row0 - p.S + g : tb.tok[t.row0 + g];
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.x + (size_t)tk * p.H + k0);
-#pragma unroll
-        for (int i = 0; i < G; ++i) b.v[i] = src[4 * i];
+        bp = reinterpret_cast<const uint4 *>(p.act + at + (size_t)col * ld + k0);
       }
     } else {
-#pragma unroll
-      for (int i = 0; i < Step::kN; ++i) b.v[i] = make_uint4(0u, 0u, 0u, 0u);
+      const int tk = u.sh ? u.row0 - p.S + col : tb.tok[u.row0 + col];
+      bp = reinterpret_cast<const uint4 *>(p.x + (size_t)tk * p.H + k0);
     }
-    if constexpr (DOWN && WT) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int col = min(2 * t4 + c, t.ntok - 1);
-        const size_t at = t.sh ? (size_t)p.S * p.I + (size_t)(t.row0 - p.S + col) * p.Is : (size_t)(t.row0 + col) * p.I;
-        b.ex[c] = *reinterpret_cast<const uint32_t *>(p.act_exp + at / 32 + 4 * st);
-      }
+  };
+  auto load_b = [&](int i) {
+    if constexpr (DOWN && !WT) {
+      bv[2 * i] = bp[8 * i];
+      bv[2 * i + 1] = bp[8 * i + 1];
+    } else {
+      bv[i] = bp[4 * i];
     }
+  };
+  constexpr int kBStep = (DOWN && !WT) ? 8 * G : 4 * G;  // 16-byte pieces from a step to the next
+  auto first_b = [&](const Unit &u) {
+    point(u);
+#pragma unroll
+    for (int i = 0; i < G; ++i) load_b(i);
+    if constexpr (DOWN && WT) ex[0] = *xp[0], ex[1] = *xp[1];
   };
 
   int slot = 0, buf = 0;
-  Unit nxt = decode_unit(p, tb, q, blockIdx.x, warp, kRows);
-  Step bn;
-  if (nxt.n > 0) load_b(bn, nxt, 0);
-  for (int u = blockIdx.x; u < q.units; u += gridDim.x) {
+  Unit nxt = list.get(0, s0, ns);
+  if (nxt.n > 0) first_b(nxt);
+#pragma unroll 1
+  for (int ui = 0; ui < mine; ++ui) {
     const Unit t = nxt;
-    nxt = decode_unit(p, tb, q, u + gridDim.x, warp, kRows);
+    if (ui + 1 - list.base == 32) list.decode(tb, q, p.S, p.T, team, teams, ui + 1, lane);
+    nxt = list.get(ui + 1, s0, ns);
     float acc[2][4];
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[a][i] = 0.0f;
-    if (t.n == 0 && nxt.n > 0) load_b(bn, nxt, 0);
+    if (t.n == 0 && nxt.n > 0) first_b(nxt);
+#pragma unroll 1
     for (int s = 0; s < t.n; ++s) {
-      const Step b = bn;
-      // the next step's token values, a step ahead of their use
-      if (s + 1 < t.n) load_b(bn, t, s + 1);
-      else if (nxt.n > 0) load_b(bn, nxt, 0);
+      // where the registers' next values come from (after the last step: anywhere valid)
+      if (s + 1 < t.n) {
+        bp += kBStep;
+        if constexpr (DOWN && WT) ++xp[0], ++xp[1];
+      } else if (nxt.n > 0) {
+        point(nxt);
+      }
+      uint4 b0[kB];
+      if constexpr (!WT) {
+#pragma unroll
+        for (int i = 0; i < kB; ++i) b0[i] = bv[i];
+        load_b(0);
+      }
       cp_async_wait<kNst - 2>();
       __syncwarp();
       fill();  // into the slot read in the previous step
       const uint32_t st = my_ring + slot * STAGE;
-      slot = slot + 1 == kNst ? 0 : slot + 1;
+      slot = (slot + 1) & (kNst - 1);
       const uint32_t wa = st + g * kStepBytes + t4 * 16;
       uint4 v[4];  // tile 0 rows g, g + 8; tile 1 rows g, g + 8
 #pragma unroll
@@ -398,41 +428,41 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
         uint32_t sc[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[i] = lds32(st + kStageW + (i * 8 + g) * 4);
+        const uint32_t e0 = ex[0], e1 = ex[1];
+        if constexpr (DOWN) ex[0] = *xp[0], ex[1] = *xp[1];
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
-          float sx[2] = {1.0f, 1.0f};
-          if constexpr (DOWN) {
-            sx[0] = scale_of(b.ex[0], gr);
-            sx[1] = scale_of(b.ex[1], gr);
-          }
-          const uint4 bv = b.v[gr];
+          float part[2][4];
 #pragma unroll
           for (int a = 0; a < 2; ++a) {
             uint32_t h0[4], h8[4];
             e2m1x8_to_f16(word_of(v[2 * a], gr), h0);
             e2m1x8_to_f16(word_of(v[2 * a + 1], gr), h8);
-            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma16<true>(part, h0[0], h8[0], h0[1], h8[1], bv.x, bv.y);
-            mma16<true>(part, h0[2], h8[2], h0[3], h8[3], bv.z, bv.w);
+            mma16_first(part[a], h0[0], h8[0], h0[1], h8[1], bv[gr].x, bv[gr].y);
+            mma16<true>(part[a], h0[2], h8[2], h0[3], h8[3], bv[gr].z, bv[gr].w);
+          }
+          load_b(gr);
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
             const float s0 = scale_of(sc[2 * a], gr), s8 = scale_of(sc[2 * a + 1], gr);
             if constexpr (DOWN) {
-              acc[a][0] = fmaf(s0 * sx[0], part[0], acc[a][0]);
-              acc[a][1] = fmaf(s0 * sx[1], part[1], acc[a][1]);
-              acc[a][2] = fmaf(s8 * sx[0], part[2], acc[a][2]);
-              acc[a][3] = fmaf(s8 * sx[1], part[3], acc[a][3]);
+              const float x0 = scale_of(e0, gr), x1 = scale_of(e1, gr);
+              acc[a][0] = fmaf(s0 * x0, part[a][0], acc[a][0]);
+              acc[a][1] = fmaf(s0 * x1, part[a][1], acc[a][1]);
+              acc[a][2] = fmaf(s8 * x0, part[a][2], acc[a][2]);
+              acc[a][3] = fmaf(s8 * x1, part[a][3], acc[a][3]);
             } else {
-              acc[a][0] = fmaf(s0, part[0], acc[a][0]);
-              acc[a][1] = fmaf(s0, part[1], acc[a][1]);
-              acc[a][2] = fmaf(s8, part[2], acc[a][2]);
-              acc[a][3] = fmaf(s8, part[3], acc[a][3]);
+              acc[a][0] = fmaf(s0, part[a][0], acc[a][0]);
+              acc[a][1] = fmaf(s0, part[a][1], acc[a][1]);
+              acc[a][2] = fmaf(s8, part[a][2], acc[a][2]);
+              acc[a][3] = fmaf(s8, part[a][3], acc[a][3]);
             }
           }
         }
       } else {
-        uint32_t bh[4] = {b.v[0].x, b.v[0].y, b.v[0].z, b.v[0].w}, bl[4];
+        uint32_t bh[4] = {b0[0].x, b0[0].y, b0[0].z, b0[0].w}, bl[4];
         if constexpr (DOWN) {  // the fp32 activation as the sum of two bf16 values (16 of its 24 bits)
-          const uint4 x1 = b.v[1];
-          const uint32_t xu[8] = {bh[0], bh[1], bh[2], bh[3], x1.x, x1.y, x1.z, x1.w};
+          const uint32_t xu[8] = {bh[0], bh[1], bh[2], bh[3], b0[kB - 1].x, b0[kB - 1].y, b0[kB - 1].z, b0[kB - 1].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float fa = __uint_as_float(xu[2 * i]), fb = __uint_as_float(xu[2 * i + 1]);
@@ -453,55 +483,49 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
       }
     }
 
-    // ---- the warps' partial products, then the sums in slice order: a warp takes 32
-    // rows of one column, a lane each
-    float *rd = red + buf * kRedFloats;
+    // ---- the team's partial products, then the sums in slice order: a warp takes the
+    // unit's 32 rows of one column, a lane each.  Two buffers: the next unit's products
+    // are written while these are added, and the barrier before their sums orders both.
+    float *rd = red + buf * kRedFloats + (warp - wi) * 2 * kRedTile;
     buf ^= 1;
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-      float *d = rd + (warp * 2 + a) * kRedTile + 2 * t4 * kRedCol + g;
+      float *d = rd + (wi * 2 + a) * kRedTile + 2 * t4 * kRedCol + g;
       d[0] = acc[a][0];
       d[kRedCol] = acc[a][1];
       d[8] = acc[a][2];
       d[kRedCol + 8] = acc[a][3];
     }
-    __syncthreads();
-    const int groups = (DOWN ? 1 << q.rg_shift : (1 << q.rg_shift) >> 1) * t.ntok;  // (32 rows, column) pairs
-    for (int o = warp; o < groups; o += kFewWarps) {
-      const int blk = o / t.ntok, col = o - blk * t.ntok;
-      const int row = t.rb * q.unit_rows + blk * 32 + lane;
+    if (tw == 1) __syncwarp();
+    else named_bar_sync(1 + tm, 32 * tw);
+    const int row = t.row + lane;
+    for (int col = wi; col < t.ntok; col += tw) {
       if constexpr (!DOWN) {
-        // rows of the two row groups 2 blk, 2 blk + 1
-        const float *src = rd + (2 * blk + (lane >> 4)) * q.ks * 2 * kRedTile + col * kRedCol + (lane & 15);
+        // row group lane / 16 is its KS warps' gate and up tiles
+        const float *src = rd + ((lane >> 4) << q.ks_shift) * 2 * kRedTile + col * kRedCol + (lane & 15);
         float gs = 0.0f, us = 0.0f;
         for (int k = 0; k < q.ks; ++k, src += 2 * kRedTile) {
           gs += src[0];
           us += src[kRedTile];
         }
-        const bool live = row < (t.sh ? q.rows_s : q.rows_r);  // whole blocks of 32 rows: I is a multiple of 64
-        if (live) {
-          const size_t at =
-              (t.sh ? (size_t)p.S * p.I + (size_t)(t.row0 - p.S + col) * p.Is : (size_t)(t.row0 + col) * p.I) + row;
-          if constexpr (WT) {
-            const float un = __ldcg(p.x_unscale + (t.sh ? t.row0 - p.S + col : tb.tok[t.row0 + col]));
-            const float a = silu_mul(gs * un, us * un);
-            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(a) & 0x7FFFFFFFu);
-            const __half h = __float2half_rn(a * fp16_scale(top));
-            p.act16[at] = __half_as_ushort(h);
-            if (lane == 0) p.act_exp[at / 32] = (uint8_t)(__float_as_uint(fp16_unscale(top)) >> 23);
-          } else {
-            p.act[at] = silu_mul(gs, us);
-          }
+        const size_t at =
+            (t.sh ? (size_t)p.S * p.I + (size_t)(t.row0 - p.S + col) * p.Is : (size_t)(t.row0 + col) * p.I) + row;
+        if constexpr (WT) {
+          const float un = __ldcg(p.x_unscale + (t.sh ? t.row0 - p.S + col : tb.tok[t.row0 + col]));
+          const float a = silu_mul(gs * un, us * un);
+          const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(a) & 0x7FFFFFFFu);
+          p.act16[at] = __half_as_ushort(__float2half_rn(a * fp16_scale(top)));
+          if (lane == 0) p.act_exp[at / 32] = (uint8_t)(__float_as_uint(fp16_unscale(top)) >> 23);
+        } else {
+          p.act[at] = silu_mul(gs, us);
         }
       } else {
-        const float *src = rd + (blk * q.ks * 2 + (lane >> 4)) * kRedTile + col * kRedCol + (lane & 15);
+        const float *src = rd + (lane >> 4) * kRedTile + col * kRedCol + (lane & 15);
         float y = 0.0f;
         for (int k = 0; k < q.ks; ++k, src += 2 * kRedTile) y += *src;
-        if (row < p.H) {
-          if (p.y != nullptr) p.y[(size_t)(t.row0 + col) * p.H + row] = y;
-          else if (t.sh) p.y_shared[(size_t)(t.row0 - p.S + col) * p.H + row] = __float2bfloat16_rn(y);
-          else p.y_sorted[(size_t)(t.row0 + col) * p.H + row] = __float2bfloat16_rn(y);
-        }
+        if (p.y != nullptr) p.y[(size_t)(t.row0 + col) * p.H + row] = y;
+        else if (t.sh) p.y_shared[(size_t)(t.row0 - p.S + col) * p.H + row] = __float2bfloat16_rn(y);
+        else p.y_sorted[(size_t)(t.row0 + col) * p.H + row] = __float2bfloat16_rn(y);
       }
     }
   }
@@ -657,77 +681,99 @@ __device__ __forceinline__ int ordered(float f) {
   return b ^ ((b >> 31) & 0x7FFFFFFF);
 }
 
-// Selection of one token by a warp, with the rule and results of the router.s top-k kernel: the
-// largest key each round by one integer reduction over the lanes, the lower of
-// equal experts by another.
-__device__ __forceinline__ void select_token(const FewParams &p, FewTables &tb, int t, const float (&bias)[8], int lane) {
+// Selection of NT tokens (t, t + kFewWarps; past the last: none) by a warp, with the
+// rule and results of the router's top-k kernel: the largest key each round by one
+// integer reduction over the lanes, the lower of equal experts by another.  The
+// tokens' chains of reductions overlap.
+template <int NT>
+__device__ __forceinline__ void select_tokens(const FewParams &p, FewTables &tb, int t, const float (&bias)[8], int lane) {
   const int E = p.E, k = p.top_k;
-  float v[8], sc[8];
-  int key[8];
+  float sc[NT][8];
+  int key[NT][8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = lane + 32 * j < E ? __ldcg(p.logits + (size_t)t * E + lane + 32 * j) : -INFINITY;
-  if (p.score_mode == MOE_SCORE_SIGMOID_BIAS) {
+  for (int n = 0; n < NT; ++n) {
+    const int tk = min(t + n * kFewWarps, p.T - 1);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sc[j] = 1.0f / (1.0f + expf(-v[j]));
-  } else {
-    float mx = -INFINITY, sum = 0.0f;
+    for (int j = 0; j < 8; ++j)
+      sc[n][j] = lane + 32 * j < E ? __ldcg(p.logits + (size_t)tk * E + lane + 32 * j) : -INFINITY;
+  }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) mx = fmaxf(mx, v[j]);
+  for (int n = 0; n < NT; ++n) {
+    if (p.score_mode == MOE_SCORE_SIGMOID_BIAS) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      for (int j = 0; j < 8; ++j)
+        if (32 * j < E) sc[n][j] = 1.0f / (1.0f + expf(-sc[n][j]));
+    } else {
+      float mx = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mx = fmaxf(mx, sc[n][j]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (32 * j < E) {
+          sc[n][j] = lane + 32 * j < E ? expf(sc[n][j] - mx) : 0.0f;
+          sum += sc[n][j];
+        }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (32 * j < E) sc[n][j] = sc[n][j] / sum;
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      sc[j] = lane + 32 * j < E ? expf(v[j] - mx) : 0.0f;
-      sum += sc[j];
+      const float kk = sc[n][j] + bias[j] + 0.0f;  // -0 as 0
+      key[n][j] = lane + 32 * j < E ? (kk == kk ? ordered(kk) : ordered(-INFINITY)) : INT_MIN;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sc[j] = sc[j] / sum;
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float kk = sc[j] + bias[j] + 0.0f;  // -0 as 0
-    key[j] = lane + 32 * j < E ? (kk == kk ? ordered(kk) : ordered(-INFINITY)) : INT_MIN;
-  }
-  int my_e = 0;
-  float my_s = 0.0f;
+  int my_e[NT] = {};
+  float my_s[NT] = {};
 #pragma unroll 1
   for (int r = 0; r < k; ++r) {
-    int bk = INT_MIN, bj = 0;
-    float bs = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (key[j] > bk) {
-        bk = key[j];
-        bj = j;
-        bs = sc[j];
+    for (int n = 0; n < NT; ++n) {
+      int bk = INT_MIN, bj = 0;
+      float bs = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (key[n][j] > bk) {
+          bk = key[n][j];
+          bj = j;
+          bs = sc[n][j];
+        }
+      const int top = __reduce_max_sync(0xffffffffu, bk);
+      const int e = __reduce_min_sync(0xffffffffu, bk == top ? lane + 32 * bj : 0x7fffffff);
+      const float es = __shfl_sync(0xffffffffu, bs, e & 31);
+      if (lane == r) {
+        my_e[n] = e;
+        my_s[n] = es;
       }
-    const int top = __reduce_max_sync(0xffffffffu, bk);
-    const int e = __reduce_min_sync(0xffffffffu, bk == top ? lane + 32 * bj : 0x7fffffff);
-    const float es = __shfl_sync(0xffffffffu, bs, e & 31);
-    if (lane == r) {
-      my_e = e;
-      my_s = es;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (e == lane + 32 * j) key[n][j] = INT_MIN;
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (e == lane + 32 * j) key[j] = INT_MIN;
   }
-  float tot = lane < k ? my_s : 0.0f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-  if (lane < k) {
-    tb.idx[t * k + lane] = my_e;
-    tb.w[t * k + lane] = p.score_mode == MOE_SCORE_SIGMOID_BIAS ? my_s / tot * p.route_scale : my_s / fmaxf(tot, p.renorm_eps);
-    atomicOr(&tb.mask[my_e], 1u << t);
+  for (int n = 0; n < NT; ++n) {
+    const int tk = t + n * kFewWarps;
+    float tot = lane < k ? my_s[n] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+    if (lane < k && tk < p.T) {
+      tb.idx[tk * k + lane] = my_e[n];
+      tb.w[tk * k + lane] =
+          p.score_mode == MOE_SCORE_SIGMOID_BIAS ? my_s[n] / tot * p.route_scale : my_s[n] / fmaxf(tot, p.renorm_eps);
+      atomicOr(&tb.mask[my_e[n]], 1u << tk);
+    }
   }
 }
 
 // Selection and tables from the logits (tb.mask is zero).
 __device__ void tables_from_logits(const FewParams &p, FewTables &tb, const float (&bias)[8]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = p.top_k;
-  for (int t = warp; t < p.T; t += kFewWarps) select_token(p, tb, t, bias, lane);
+  if (p.T > kFewWarps) select_tokens<2>(p, tb, warp, bias, lane);
+  else if (warp < p.T) select_tokens<1>(p, tb, warp, bias, lane);
   __syncthreads();
   build_segments(tb, threadIdx.x < 256 ? __popc(tb.mask[threadIdx.x]) : 0);
   __syncthreads();
