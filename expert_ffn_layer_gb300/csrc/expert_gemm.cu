@@ -111,7 +111,7 @@ template <int BN, int MODE>
 struct Rings {
   static constexpr bool CV = converts(MODE);
   static constexpr int kW = CV ? 3 : BN >= 256 ? 3 : BN >= 240 ? 4 : BN >= 128 ? 5 : 6;
-  static constexpr int kQ = CV ? (BN >= 128 ? 4 : 6) : 0;
+  static constexpr int kQ = CV ? (BN >= 240 ? 2 : BN >= 128 ? 4 : 6) : 0;  // MXFP4: two K steps each
   static constexpr int kT = BN >= 64 ? 3 : 4;
 };
 
@@ -152,7 +152,8 @@ struct Layout {
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert(kTmemUsed <= 512, "TMEM budget");
   static_assert(kW <= 16 && kT <= 16 && kQ <= 16, "issue masks");
-  static_assert(!CV || BN <= 128, "converted weights run the narrow tiles");
+  static_assert(MODE != kModeQ8 || BN <= 128, "FP8 weights run the narrow tiles");
+  static_assert(MODE != kModeQ4 || BN <= 240, "the code ring takes the staging of 256-token tiles");
   static_assert(MODE != kModeF8 || BN <= 240, "the W8A8 epilogue has no staged (256-token) form");
 };
 
@@ -1418,9 +1419,10 @@ cudaError_t launch_expert_ffn(const GemmParams &p, int bn, int num_ctas, cudaStr
     }
   }
   if (p.mode == kModeQ4) {
-    switch (bn < 128 ? bn : 128) {
+    switch (bn < 240 ? bn : 240) {
       case 64: return launch_one<64, kModeQ4>(p, num_ctas, stream, pdl);
       case 128: return launch_one<128, kModeQ4>(p, num_ctas, stream, pdl);
+      case 240: return launch_one<240, kModeQ4>(p, num_ctas, stream, pdl);
       default: return cudaErrorInvalidValue;  // 32 tokens and fewer run the one-kernel form
     }
   }
