@@ -186,84 +186,125 @@ __device__ __forceinline__ bool grid_wait(const FewParams &p, unsigned *counter,
 // (32 pairs of rows for gate/up); a team of warps takes one: KS slices of K, and for
 // gate/up two warps a slice (16 gate and 16 up rows each).  The CTA's teams go their
 // own ways, each with its own units and its own barrier.
+//
+// The units are dealt out in two parts: as many whole rounds over all teams as there
+// are, with KS slices, and the rest, which would leave teams idle in a last round, with
+// at least as many slices (larger teams, shorter units).
 struct Plan {
-  int ks, ks_shift;   // K slices and their log2
-  int tw_shift;       // log2 of a team's warps
-  int rows_r, rows_s; // rows of a routed / the shared expert, multiples of 32
+  int rows_r, rows_s;    // rows of a routed / the shared expert, multiples of 32
   int steps_r, steps_s;
-  int units;
+  int units, units_a;    // all, and those of the first part
+  int ks_shift[2];       // log2 of the parts' K slices
 };
 
-// KS by the shortest makespan: rounds of units over the teams, each as long as its
-// warps' steps (about 1400 cycles of the SM's share of the memory rate, 16 warps
-// together) and the exchange of partial products (about 300).
-template <bool DOWN>
-__device__ Plan make_plan(const FewTables &tb, int rows_r, int rows_s, int steps_r, int steps_s) {
-  Plan best = {};
-  int best_cost = 0x7fffffff;
-  for (int sh = 0; sh <= (DOWN ? 4 : 3); ++sh) {
-    Plan q;
-    q.ks = 1 << sh;
-    q.ks_shift = sh;
-    q.tw_shift = DOWN ? sh : sh + 1;
-    q.rows_r = rows_r;
-    q.rows_s = rows_s;
-    q.steps_r = steps_r;
-    q.steps_s = steps_s;
-    q.units = (tb.nsh * rows_s + tb.nact * rows_r) >> 5;
-    const int teams = gridDim.x * (kFewWarps >> q.tw_shift);
-    const int rounds = (q.units + teams - 1) / teams;
-    const int cost = rounds * (((max(steps_r, tb.nsh ? steps_s : 0) + q.ks - 1) >> sh) * 1400 + 300);
-    if (cost <= best_cost) {
-      best_cost = cost;
-      best = q;
-    }
+// KS of both parts by the shortest makespan: a round lasts its warps' steps (C cycles
+// each, the 16 warps of an SM together) and the exchange of partial products (C_unit).
+// One lane tries one pair.
+template <int WT, bool DOWN>
+__device__ Plan make_plan(const FewTables &tb, int rows_r, int rows_s, int steps_r, int steps_s, int lane) {
+  constexpr int kChoices = DOWN ? 5 : 4, kStepCycles = WT ? 2000 : 1400, kUnitCycles = WT ? 2000 : 600;
+  Plan q;
+  q.rows_r = rows_r;
+  q.rows_s = rows_s;
+  q.steps_r = steps_r;
+  q.steps_s = steps_s;
+  q.units = (tb.nsh * rows_s + tb.nact * rows_r) >> 5;
+  const int a = lane / kChoices, b = lane % kChoices, steps = max(steps_r, tb.nsh ? steps_s : 0);
+  unsigned cost = 0x7fffffffu;
+  // bf16, bound by the memory: at least as many slices as leave a warp six steps, up to
+  // eight -- fewer and longer ones spread the reads (8 and 4 slices at Hy3 T = 32: 841 and
+  // 856 us; two at T = 8: 385 against 353).  MXFP4, bound by instructions, gains from few.
+  const bool near = WT || a >= 3 || steps >> (a + 1) < 6;
+  if (a < kChoices && b >= a && near) {
+    auto round = [&](int sh) { return ((steps + (1 << sh) - 1) >> sh) * kStepCycles + kUnitCycles; };
+    auto teams = [&](int sh) { return (int)gridDim.x * (kFewWarps >> (DOWN ? sh : sh + 1)); };
+    const int ra = q.units / teams(a), rest = q.units - ra * teams(a);
+    cost = (unsigned)(ra * round(a) + (rest + teams(b) - 1) / teams(b) * round(b));
   }
-  return best;
+  const unsigned best = __reduce_min_sync(0xffffffffu, cost);
+  const int win = __ffs(__ballot_sync(0xffffffffu, cost == best)) - 1;
+  q.ks_shift[0] = win / kChoices;
+  q.ks_shift[1] = win % kChoices;
+  const int ta = gridDim.x * (kFewWarps >> (DOWN ? q.ks_shift[0] : q.ks_shift[0] + 1));
+  q.units_a = q.units / ta * ta;
+  return q;
+}
+
+// A warp's place in one part: its team, K slice and units.
+struct Part {
+  int ks_shift, tw_shift;  // log2 of K slices and of a team's warps
+  int team, teams, mine;   // the team's number, how many there are, units of this one
+  int off;                 // the warp's first row in a unit
+  int s0[2], n[2];         // its first step and number of steps: routed, shared
+};
+template <bool DOWN>
+__device__ __forceinline__ Part make_part(const Plan &q, int i, int warp) {
+  Part r;
+  r.ks_shift = i ? q.ks_shift[1] : q.ks_shift[0];
+  r.tw_shift = DOWN ? r.ks_shift : r.ks_shift + 1;
+  const int ks = warp & ((1 << r.ks_shift) - 1), units = i ? q.units - q.units_a : q.units_a;
+  r.off = DOWN ? 0 : (warp >> r.ks_shift & 1) * 16;
+  r.teams = gridDim.x * (kFewWarps >> r.tw_shift);
+  // neighbouring units to neighbouring CTAs (to the teams of one CTA: 10 % slower)
+  r.team = (warp >> r.tw_shift) * gridDim.x + blockIdx.x;
+  r.mine = units > r.team ? (units - 1 - r.team) / r.teams + 1 : 0;
+  r.s0[0] = q.steps_r * ks >> r.ks_shift;
+  r.s0[1] = q.steps_s * ks >> r.ks_shift;
+  r.n[0] = (q.steps_r * (ks + 1) >> r.ks_shift) - r.s0[0];
+  r.n[1] = (q.steps_s * (ks + 1) >> r.ks_shift) - r.s0[1];
+  return r;
 }
 
 // One of a team's units, for one of its warps.
 struct Unit {
-  int w_row;           // the unit's first row of the stacked weight matrix
+  int w_row;           // this warp's first row of the stacked weight matrix
   int sh, row0, ntok;  // of the shared expert; first position; number of positions (0: past the last unit)
   int row;             // the unit's first row in its expert
   int s0, n;           // this warp's first step and its number of steps
 };
 
-// A team's units in order, decoded 32 at a time, one by each lane of a warp, and
-// read by shuffles -- which also tells the compiler that they are the warp's, not
-// the lane's.  Packed: positions (4 bits), first position (10), first row / 32 (10), shared (1).
+// A warp's units in order, decoded 32 at a time, one by each lane, and read by
+// shuffles -- which also tells the compiler that they are the warp's, not the lane's.
+// Packed: positions (4 bits), first position (10), first row / 32 (10), shared (1),
+// and the steps: first (10), number (11).
 struct UnitList {
-  int base, w_row, word;
+  int base, w_row, word, steps;
 
-  // unit i of the list is number team + i * teams of the phase
-  __device__ __forceinline__ void decode(const FewTables &tb, const Plan &q, int S, int T, int team, int teams, int first,
-                                         int lane) {
+  template <bool DOWN>
+  __device__ __forceinline__ void decode(const FewTables &tb, const Plan &q, int S, int T, int warp, int first, int lane) {
     base = first;
-    const int u = team + (first + lane) * teams, rb_s = q.rows_s >> 5, rb_r = q.rows_r >> 5, n_sh = tb.nsh * rb_s;
-    word = 0;
-    w_row = 0;
-    if (u < n_sh) {
-      const int seg = u / rb_s, rb = u - seg * rb_s;
-      w_row = rb * 32;
-      word = min(8, T - 8 * seg) | (S + 8 * seg) << 4 | rb << 14 | 1 << 24;
-    } else if (u < q.units) {
-      const int v = u - n_sh, seg = v / rb_r, rb = v - seg * rb_r;
-      w_row = tb.seg_e[seg] * q.rows_r + rb * 32;
-      word = tb.seg_n[seg] | tb.seg_row0[seg] << 4 | rb << 14;
+    const Part a = make_part<DOWN>(q, 0, warp), b = make_part<DOWN>(q, 1, warp);
+    const int i = first + lane, rb_s = q.rows_s >> 5, rb_r = q.rows_r >> 5, n_sh = tb.nsh * rb_s;
+    const bool in_a = i < a.mine;
+    const int u = in_a ? a.team + i * a.teams : i - a.mine < b.mine ? q.units_a + b.team + (i - a.mine) * b.teams : q.units;
+    const int off = in_a ? a.off : b.off;
+    word = w_row = steps = 0;
+    if (u < q.units) {
+      const bool sh = u < n_sh;
+      if (sh) {
+        const int seg = u / rb_s, rb = u - seg * rb_s;
+        w_row = rb * 32 + off;
+        word = min(8, T - 8 * seg) | (S + 8 * seg) << 4 | rb << 14 | 1 << 24;
+      } else {
+        const int v = u - n_sh, seg = v / rb_r, rb = v - seg * rb_r;
+        w_row = tb.seg_e[seg] * q.rows_r + rb * 32 + off;
+        word = tb.seg_n[seg] | tb.seg_row0[seg] << 4 | rb << 14;
+      }
+      const int s0 = sh ? (in_a ? a.s0[1] : b.s0[1]) : in_a ? a.s0[0] : b.s0[0];
+      steps = s0 | (sh ? (in_a ? a.n[1] : b.n[1]) : in_a ? a.n[0] : b.n[0]) << 10;
     }
   }
   // unit i, 0 <= i - base < 32
-  __device__ __forceinline__ Unit get(int i, const int (&s0)[2], const int (&n)[2]) const {
+  __device__ __forceinline__ Unit get(int i) const {
     Unit t;
-    const int x = __shfl_sync(0xffffffffu, word, i - base);
+    const int x = __shfl_sync(0xffffffffu, word, i - base), st = __shfl_sync(0xffffffffu, steps, i - base);
     t.w_row = __shfl_sync(0xffffffffu, w_row, i - base);
     t.ntok = x & 15;
     t.row0 = x >> 4 & 1023;
     t.row = (x >> 14 & 1023) << 5;
     t.sh = x >> 24;
-    t.s0 = t.sh ? s0[1] : s0[0];
-    t.n = t.ntok == 0 ? 0 : t.sh ? n[1] : n[0];
+    t.s0 = st & 1023;
+    t.n = st >> 10;
     return t;
   }
 };
@@ -274,16 +315,12 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
   constexpr int G = Fmt<WT>::kGroups, STAGE = Fmt<WT>::kStage;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const int K_r = DOWN ? p.I : p.H, K_s = DOWN ? p.Is : p.H;
-  const Plan q = make_plan<DOWN>(tb, DOWN ? p.H : p.I, DOWN ? p.H : p.Is, K_r / Fmt<WT>::kStep, K_s / Fmt<WT>::kStep);
-  const int tw = 1 << q.tw_shift, wi = warp & (tw - 1);  // the team's warps, this one's place
-  const int ks = wi & (q.ks - 1), off = DOWN ? 0 : (wi >> q.ks_shift) * 16;  // K slice; first row in the unit
-  const int tm = warp >> q.tw_shift, teams = gridDim.x * (kFewWarps >> q.tw_shift), team = tm * gridDim.x + blockIdx.x;
-  const int s0[2] = {q.steps_r * ks >> q.ks_shift, q.steps_s * ks >> q.ks_shift};
-  const int ns[2] = {(q.steps_r * (ks + 1) >> q.ks_shift) - s0[0], (q.steps_s * (ks + 1) >> q.ks_shift) - s0[1]};
-  const int mine = q.units > team ? (q.units - 1 - team) / teams + 1 : 0;
-  UnitList list, flist;  // of the products and of the weight stream ahead of them
-  list.decode(tb, q, p.S, p.T, team, teams, 0, lane);
-  flist = list;
+  const Plan q = make_plan<WT, DOWN>(tb, DOWN ? p.H : p.I, DOWN ? p.H : p.Is, K_r / Fmt<WT>::kStep,
+                                     K_s / Fmt<WT>::kStep, lane);
+  const int mine_a = make_part<DOWN>(q, 0, warp).mine, mine = mine_a + make_part<DOWN>(q, 1, warp).mine;
+  UnitList list{};  // of the products
+  list.decode<DOWN>(tb, q, p.S, p.T, warp, 0, lane);
+  UnitList flist = list;  // of the weight stream ahead of them
   const uint32_t my_ring = smem_u32(ring) + warp * kNst * STAGE;
 
   // ---- the weight stream: the unit and step to copy next
@@ -294,15 +331,15 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
     if (fs == fn) {    // on to the next unit in which this warp has steps
       fs = fn = 0;
       while (fi < mine && fn == 0) {
-        if (fi - flist.base == 32) flist.decode(tb, q, p.S, p.T, team, teams, fi, lane);
-        const Unit f = flist.get(fi++, s0, ns);
+        if (fi - flist.base == 32) flist.decode<DOWN>(tb, q, p.S, p.T, warp, fi, lane);
+        const Unit f = flist.get(fi++);
         fn = f.n;
         if (fn > 0) {
           const int K = f.sh ? K_s : K_r;
           const uint32_t rowb = WT ? K / 2 : K * 2;
           const uint8_t *m0 = DOWN ? (f.sh ? p.s_down : p.down) : (f.sh ? p.s_gate : p.gate);
           const uint8_t *m1 = DOWN ? m0 + 16 * rowb : (f.sh ? p.s_up : p.up);
-          const size_t at = (size_t)(f.w_row + off + g) * rowb + f.s0 * kStepBytes + t4 * 16;
+          const size_t at = (size_t)(f.w_row + g) * rowb + f.s0 * kStepBytes + t4 * 16;
           f0 = m0 + at;
           f1 = m1 + at;
           f8 = 8 * rowb;
@@ -310,7 +347,7 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
             const uint32_t sb = K / 32;
             const uint8_t *c0 = DOWN ? (f.sh ? p.s_down_scale : p.down_scale) : (f.sh ? p.s_gate_scale : p.gate_scale);
             const uint8_t *c1 = DOWN ? c0 + 16 * sb : (f.sh ? p.s_up_scale : p.up_scale);
-            fsc = (lane < 16 ? c0 : c1) + (size_t)(f.w_row + off + (lane & 15)) * sb + f.s0 * 4;
+            fsc = (lane < 16 ? c0 : c1) + (size_t)(f.w_row + (lane & 15)) * sb + f.s0 * 4;
           }
         }
       }
@@ -387,13 +424,13 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
   };
 
   int slot = 0, buf = 0;
-  Unit nxt = list.get(0, s0, ns);
+  Unit nxt = list.get(0);
   if (nxt.n > 0) first_b(nxt);
 #pragma unroll 1
   for (int ui = 0; ui < mine; ++ui) {
     const Unit t = nxt;
-    if (ui + 1 - list.base == 32) list.decode(tb, q, p.S, p.T, team, teams, ui + 1, lane);
-    nxt = list.get(ui + 1, s0, ns);
+    if (ui + 1 - list.base == 32) list.decode<DOWN>(tb, q, p.S, p.T, warp, ui + 1, lane);
+    nxt = list.get(ui + 1);
     float acc[2][4];
 #pragma unroll
     for (int a = 0; a < 2; ++a)
@@ -486,6 +523,12 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
     // ---- the team's partial products, then the sums in slice order: a warp takes the
     // unit's 32 rows of one column, a lane each.  Two buffers: the next unit's products
     // are written while these are added, and the barrier before their sums orders both.
+    // (A team of the second part is made of whole teams of the first, so its first
+    // barrier also orders what those still read; it has other barriers, as the first
+    // part's may still be in use.)
+    const int ksh = ui >= mine_a ? q.ks_shift[1] : q.ks_shift[0], tsh = DOWN ? ksh : ksh + 1;
+    const int tsh_a = DOWN ? q.ks_shift[0] : q.ks_shift[0] + 1;
+    const int tw = 1 << tsh, wi = warp & (tw - 1), n_ks = 1 << ksh;
     float *rd = red + buf * kRedFloats + (warp - wi) * 2 * kRedTile;
     buf ^= 1;
 #pragma unroll
@@ -497,14 +540,14 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
       d[kRedCol + 8] = acc[a][3];
     }
     if (tw == 1) __syncwarp();
-    else named_bar_sync(1 + tm, 32 * tw);
+    else named_bar_sync(1 + (warp >> tsh) + (tsh_a > 0 && tsh > tsh_a ? 8 : 0), 32 * tw);
     const int row = t.row + lane;
     for (int col = wi; col < t.ntok; col += tw) {
       if constexpr (!DOWN) {
         // row group lane / 16 is its KS warps' gate and up tiles
-        const float *src = rd + ((lane >> 4) << q.ks_shift) * 2 * kRedTile + col * kRedCol + (lane & 15);
+        const float *src = rd + ((lane >> 4) << ksh) * 2 * kRedTile + col * kRedCol + (lane & 15);
         float gs = 0.0f, us = 0.0f;
-        for (int k = 0; k < q.ks; ++k, src += 2 * kRedTile) {
+        for (int k = 0; k < n_ks; ++k, src += 2 * kRedTile) {
           gs += src[0];
           us += src[kRedTile];
         }
@@ -522,7 +565,7 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
       } else {
         const float *src = rd + (lane >> 4) * kRedTile + col * kRedCol + (lane & 15);
         float y = 0.0f;
-        for (int k = 0; k < q.ks; ++k, src += 2 * kRedTile) y += *src;
+        for (int k = 0; k < n_ks; ++k, src += 2 * kRedTile) y += *src;
         if (p.y != nullptr) p.y[(size_t)(t.row0 + col) * p.H + row] = y;
         else if (t.sh) p.y_shared[(size_t)(t.row0 - p.S + col) * p.H + row] = __float2bfloat16_rn(y);
         else p.y_sorted[(size_t)(t.row0 + col) * p.H + row] = __float2bfloat16_rn(y);
