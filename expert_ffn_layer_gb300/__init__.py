@@ -148,13 +148,13 @@ def _check(t, dtype, shape, name):
         return
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:  # torch.Size is a tuple
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # torch.cuda.current_stream().cuda_stream, without building the object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -445,6 +445,7 @@ class Mxfp4Experts:
 
     def __init__(self, **tensors):
         self.t = tensors  # name -> (codes uint8, scales uint8) or None
+        self.fits = None  # the dims these tensors were last found to fit
         st = MoeMxfp4Experts()
         for n in self.NAMES:
             pair = tensors.get(n)
@@ -453,6 +454,9 @@ class Mxfp4Experts:
         self.struct = st
 
     def check(self, d: MoeDims) -> None:
+        dims = (d.E, d.I, d.H, d.I_shared if d.has_shared else 0)
+        if dims == self.fits:
+            return
         shapes = {"gate": (d.E, d.I, d.H), "up": (d.E, d.I, d.H), "down": (d.E, d.H, d.I)}
         if d.has_shared:
             shapes.update(s_gate=(d.I_shared, d.H), s_up=(d.I_shared, d.H), s_down=(d.H, d.I_shared))
@@ -461,6 +465,7 @@ class Mxfp4Experts:
                 raise ValueError(f"{n}: missing")
             _check(self.t[n][0], torch.uint8, (*lead, K // 2), n + " codes")
             _check(self.t[n][1], torch.uint8, (*lead, K // 32), n + " scales")
+        self.fits = dims
 
 
 def quantize_mxfp4_experts(w_gate, w_up, w_down, ws_gate=None, ws_up=None, ws_down=None,

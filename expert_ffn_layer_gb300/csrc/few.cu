@@ -859,8 +859,7 @@ __device__ void prefetch_shared(const FewParams &p) {
 #pragma unroll
   for (int i = 0; i < 3; ++i)
     for (size_t at = ((size_t)blockIdx.x * 32 + (threadIdx.x & 31)) * kPiece; at < n; at += (size_t)gridDim.x * 32 * kPiece)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(m[i] + at), "r"((unsigned)min((size_t)kPiece, n - at))
-                   : "memory");
+      prefetch_l2_bulk(m[i] + at, (uint32_t)min((size_t)kPiece, n - at));
 }
 
 template <int WT>

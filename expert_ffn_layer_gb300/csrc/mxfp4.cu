@@ -16,6 +16,8 @@ namespace moe {
 
 namespace {
 constexpr int kMxThreads = 256;
+constexpr int kMxLoads = 4;  // 8-value pieces of a thread, all in flight before the first is used
+constexpr long long kMxTile = (long long)kMxThreads * kMxLoads;
 }  // namespace
 
 // One lane per 8 values: four lanes share a block's maximum, sixteen lanes a
@@ -26,28 +28,37 @@ __global__ void __launch_bounds__(kMxThreads) quantize_mxfp4_kernel(const __nv_b
                                                                     uint8_t *__restrict__ scales, long long n8) {
   pdl_wait();
   pdl_launch_dependents();
-  for (long long i = (long long)blockIdx.x * kMxThreads + threadIdx.x; i < n8; i += (long long)gridDim.x * kMxThreads) {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(src) + i);
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-    uint32_t top = 0;
+  const int l = threadIdx.x & 15, q = l >> 2, t = l & 3;
+  const unsigned group = 0xFu << (threadIdx.x & 28u);  // a block's lanes: n8 is a multiple of 16, so all are in range or none
+  for (long long i0 = blockIdx.x * kMxTile + threadIdx.x; i0 < n8; i0 += gridDim.x * kMxTile) {
+    uint4 v[kMxLoads];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) top = max(top, max(u[j] & 0x7FFFu, (u[j] >> 16) & 0x7FFFu));
-    // n8 is a multiple of 16, so the lanes of a block are all here
-    const unsigned group = 0xFu << (threadIdx.x & 28u);
-    top = max(top, __shfl_xor_sync(group, top, 1));
-    top = max(top, __shfl_xor_sync(group, top, 2));
-    const uint32_t ex = top >> 7;  // biased exponent of the largest magnitude
-    const uint32_t e = ex == 255u ? 255u : ex > 2u ? ex - 2u : 0u;
-    const float inv = __uint_as_float((254u - min(e, 253u)) << 23);  // 2^(127 - e)
-    float f[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __uint_as_float(u[j] << 16) * inv;
-      f[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u) * inv;
+    for (int u = 0; u < kMxLoads; ++u) {
+      const long long i = i0 + u * kMxThreads;
+      if (i < n8) v[u] = __ldcs(reinterpret_cast<const uint4 *>(src) + i);
     }
-    const int l = (int)(i & 15), q = l >> 2, t = l & 3;
-    reinterpret_cast<uint32_t *>(codes)[(i & ~15ll) + 4 * t + q] = f32x8_to_e2m1(f);
-    if (t == 0) scales[i >> 2] = (uint8_t)e;
+#pragma unroll
+    for (int u = 0; u < kMxLoads; ++u) {
+      const long long i = i0 + u * kMxThreads;
+      if (i >= n8) break;
+      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+      top = max(top, __shfl_xor_sync(group, top, 1));
+      top = max(top, __shfl_xor_sync(group, top, 2));
+      const uint32_t ex = top >> 7;  // biased exponent of the largest magnitude
+      const uint32_t e = ex == 255u ? 255u : ex > 2u ? ex - 2u : 0u;
+      const float inv = __uint_as_float((254u - min(e, 253u)) << 23);  // 2^(127 - e)
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(w[j] << 16) * inv;
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) * inv;
+      }
+      reinterpret_cast<uint32_t *>(codes)[(i & ~15ll) + 4 * t + q] = f32x8_to_e2m1(f);
+      if (t == 0) scales[i >> 2] = (uint8_t)e;
+    }
   }
 }
 
@@ -56,28 +67,45 @@ __global__ void __launch_bounds__(kMxThreads) dequantize_mxfp4_kernel(const uint
                                                                       __nv_bfloat16 *__restrict__ dst, long long n8) {
   pdl_wait();
   pdl_launch_dependents();
-  for (long long i = (long long)blockIdx.x * kMxThreads + threadIdx.x; i < n8; i += (long long)gridDim.x * kMxThreads) {
-    const int l = (int)(i & 15), q = l >> 2, t = l & 3;
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(codes) + (i & ~15ll) + 4 * t + q);
-    const float s = e8m0_value(__ldg(scales + (i >> 2)));
-    uint32_t h[4], o[4];
-    e2m1x8_to_f16(w, h);
+  const int l = threadIdx.x & 15, q = l >> 2, t = l & 3;
+  for (long long i0 = blockIdx.x * kMxTile + threadIdx.x; i0 < n8; i0 += gridDim.x * kMxTile) {
+    uint32_t w[kMxLoads], e[kMxLoads];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
-      const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
-      o[j] = *reinterpret_cast<const uint32_t *>(&b);
+    for (int u = 0; u < kMxLoads; ++u) {
+      const long long i = i0 + u * kMxThreads;
+      if (i < n8) {
+        w[u] = __ldcs(reinterpret_cast<const uint32_t *>(codes) + (i & ~15ll) + 4 * t + q);
+        e[u] = __ldcs(scales + (i >> 2));
+      }
     }
-    __stcs(reinterpret_cast<uint4 *>(dst) + i, make_uint4(o[0], o[1], o[2], o[3]));
+#pragma unroll
+    for (int u = 0; u < kMxLoads; ++u) {
+      const long long i = i0 + u * kMxThreads;
+      if (i >= n8) break;
+      const float s = e8m0_value(e[u]);
+      uint32_t h[4], o[4];
+      e2m1x8_to_f16(w[u], h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
+        o[j] = *reinterpret_cast<const uint32_t *>(&b);
+      }
+      __stcs(reinterpret_cast<uint4 *>(dst) + i, make_uint4(o[0], o[1], o[2], o[3]));
+    }
   }
 }
 
 namespace {
 unsigned stream_blocks(long long n8) {
-  int dev = 0, nsm = 0;
+  static thread_local int dev_cached = -1, nsm = 0;
+  int dev = 0;
   cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-  const long long blocks = (n8 + kMxThreads - 1) / kMxThreads, cap = (long long)(nsm > 0 ? nsm : 1) * 8;
+  if (dev != dev_cached) {
+    cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    dev_cached = dev;
+  }
+  const long long blocks = (n8 + kMxTile - 1) / kMxTile, cap = (long long)(nsm > 0 ? nsm : 1) * 8;
   return (unsigned)(blocks < cap ? blocks : cap);
 }
 }  // namespace

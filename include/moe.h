@@ -345,17 +345,17 @@ moe_status moe_dequantize_mxfp4_rows(const uint8_t *codes, const uint8_t *scales
  * in *w 16-byte aligned); arguments, layouts and errors as for those.  H, I and
  * I_shared multiples of 128 (else MOE_ERR_UNSUPPORTED).
  *   Batches of at most 32 tokens run as one kernel (for the layer: router,
- *   selection, experts and combine).  It multiplies the code values, exact in
- *   fp16, by the token values as fp16 times a power of two of each row's largest
- *   magnitude -- exact for bf16 values down to 2^-28 of it; the fp32 activation is
- *   rounded to fp16's 11 bits -- sums in fp32 and applies each block's scale to
- *   its own fp32 sum.  A scale byte of 0 counts as a zero there.  The layer's
- *   output is rounded once.
+ *   selection, experts and combine).  It multiplies the code values, exact in fp16,
+ *   by the token values as fp16 times a power of two of the row's largest magnitude
+ *   -- exact for bf16 values down to 2^-28 of it; the fp32 activation is rounded to
+ *   fp16's 11 bits, scaled likewise per 32 values -- sums in fp32 and applies each
+ *   block's scale to the block's own fp32 sum.  The layer's output is rounded once.
+ *   Such a call needs the whole device: it is a cooperative launch, whose blocks
+ *   (one per SM) are resident together.
  *   Larger batches run the chain of kernels of moe_layer_forward; its expert kernel
  *   expands the weights to bf16 in shared memory (exact) and keeps the activations
- *   between the products in bf16, as the bf16 kernel does.
- *   A call of at most 32 tokens needs the whole device: it is a cooperative launch, whose blocks
- *   (one per SM) are resident together. */
+ *   between the products in bf16, as with bf16 weights.
+ *   In the products of either form a scale byte of 0 (2^-127) counts as zero. */
 moe_status moe_expert_ffn_mxfp4(const moe_dims *d, const moe_bf16 *hidden, const int32_t *perm,
                                 const int32_t *offsets, const moe_mxfp4_experts *w, moe_bf16 *y_sorted,
                                 moe_bf16 *y_shared, void *ws, size_t ws_bytes, void *stream);
@@ -370,7 +370,8 @@ moe_status moe_layer_forward_mxfp4(const moe_dims *d, const moe_bf16 *hidden, co
  * the fp32 router weight; activations and expert outputs stay fp32 (the down
  * product takes the activation as two bf16 values, 16 bits of it) and `out` is
  * rounded once, so its results differ from moe_layer_forward's in the last bits.
- * Results do not depend on timing.  A cooperative launch, as above. */
+ * Results do not depend on timing, but the order of the sums over K depends on how
+ * many experts a batch reaches.  A cooperative launch, as above. */
 moe_status moe_layer_forward_few(const moe_dims *d, const moe_bf16 *hidden, const float *router_w,
                                  const float *expert_bias, const moe_bf16 *w_gate, const moe_bf16 *w_up,
                                  const moe_bf16 *w_down, const moe_bf16 *ws_gate, const moe_bf16 *ws_up,
