@@ -184,30 +184,14 @@ int router_ksplit(const moe_dims &d, int nsm) {
   return ks;
 }
 
-// The one-kernel layer's pieces, for batches of at most kFewMaxT tokens (they
-// share the workspace with the layout below: no call uses both).
-struct FewWs {
-  size_t logits, x16, x_unscale, act, act16, act_exp, y, total;
-};
-FewWs few_ws(const moe_dims &d) {
-  FewWs L;
-  size_t off = kWsHeaderBytes;
-  auto take = [&](size_t bytes) {
-    const size_t o = off;
-    off = align256(off + bytes);
-    return o;
-  };
-  const size_t T = (size_t)d.T, S = T * d.top_k, Is = d.has_shared ? (size_t)d.I_shared : 0;
-  L.logits = take(T * (size_t)d.E * 4);
-  L.x16 = take(T * (size_t)d.H * 2);
-  L.x_unscale = take(T * 4);
-  const size_t n_act = S * (size_t)d.I + T * Is;
-  L.act = take(n_act * 4);
-  L.act16 = take(n_act * 2);
-  L.act_exp = take(n_act / 32);
-  L.y = take((S + T) * (size_t)d.H * 4);
-  L.total = off;
-  return L;
+// Batches whose MXFP4 expert FFN runs as the one-kernel form.  Past 32 tokens it
+// pays while experts average few tokens -- each 8 of an expert's tokens are a pass
+// over its weights, while the converting kernel takes as long for 1 token as for 48
+// (Hy3 shape, this form and that: T = 33 (1.4 tokens an expert) 273 and 687 us, T = 128
+// (5.3) 434 and 933, T = 256 (10.7) 691 and 960).
+bool few_ffn(const moe_dims &d) {
+  const long long S = (long long)d.T * d.top_k;
+  return d.T <= kFewMaxT || (d.T <= kFewFfnMaxT && S <= kFewFfnMaxS && S <= 12LL * d.E);
 }
 
 WsLayout ws_layout(const moe_dims &d) {
@@ -246,8 +230,40 @@ WsLayout ws_layout(const moe_dims &d) {
   L.asc = take(S * 4);
   L.asc_s = take(T * 4);
   L.total = off;
-  if (d.T <= kFewMaxT) L.total = std::max(L.total, few_ws(d).total);
   return L;
+}
+
+// The one-kernel forms' pieces: for the whole layer in the place of the layout above
+// (no call uses both), for the expert FFN past 32 tokens, which is a stage of the
+// chain, behind it.
+struct FewWs {
+  size_t logits, x16, x_unscale, act, act16, act_exp, y, total;
+};
+FewWs few_ws(const moe_dims &d, size_t chain_total) {
+  FewWs L;
+  size_t off = d.T <= kFewMaxT ? (size_t)kWsHeaderBytes : chain_total;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align256(off + bytes);
+    return o;
+  };
+  const size_t T = (size_t)d.T, S = T * d.top_k, Is = d.has_shared ? (size_t)d.I_shared : 0;
+  const bool layer = d.T <= kFewMaxT;
+  L.logits = take(layer ? T * (size_t)d.E * 4 : 0);
+  L.x16 = take(T * (size_t)d.H * 2);
+  L.x_unscale = take(T * 4);
+  const size_t n_act = S * (size_t)d.I + T * Is;
+  L.act = take(layer ? n_act * 4 : 0);
+  L.act16 = take(n_act * 2);
+  L.act_exp = take(n_act / 32);
+  L.y = take(layer ? (S + T) * (size_t)d.H * 4 : 0);
+  L.total = off;
+  return L;
+}
+
+size_t ws_total(const moe_dims &d) {
+  const size_t chain = ws_layout(d).total;
+  return few_ffn(d) ? std::max(chain, few_ws(d, chain).total) : chain;
 }
 
 int num_sms() {
@@ -270,7 +286,7 @@ inline T *at(void *ws, size_t off) {
 
 moe_status check_ws(const moe_dims *d, void *ws, size_t ws_bytes) {
   if (ws == nullptr || !aligned256(ws)) return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < ws_layout(*d).total) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < ws_total(*d)) return MOE_ERR_WORKSPACE;
   return MOE_OK;
 }
 
@@ -548,7 +564,7 @@ bool mxfp4_ok(const moe_dims &d, const moe_mxfp4_experts *q) {
 
 // What the one-kernel layer needs whatever its weights and routing.
 FewParams few_params(const moe_dims &d, const moe_bf16 *hidden, void *ws) {
-  const FewWs L = few_ws(d);
+  const FewWs L = few_ws(d, ws_layout(d).total);
   FewParams p;
   std::memset(&p, 0, sizeof(p));
   p.hidden = reinterpret_cast<const __nv_bfloat16 *>(hidden);
@@ -595,6 +611,23 @@ void few_mxfp4(FewParams &p, const moe_mxfp4_experts &w) {
   p.s_gate_scale = w.s_gate_scale;
   p.s_up_scale = w.s_up_scale;
   p.s_down_scale = w.s_down_scale;
+}
+
+// a5-a8 with MXFP4 weights; `early` as for do_expert_phases
+moe_status do_expert_ffn_mxfp4(const moe_dims &d, const moe_bf16 *hidden, const int32_t *perm, const int32_t *offsets,
+                               const moe_mxfp4_experts &w, moe_bf16 *y_sorted, moe_bf16 *y_shared, void *ws,
+                               cudaStream_t stream, bool early) {
+  if (!few_ffn(d))
+    return do_expert_phases(d, 3, hidden, perm, offsets, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, y_sorted,
+                            y_shared, scratch_in(d, ws), stream, true, 0, nullptr, early, false, &w);
+  FewParams p = few_params(d, hidden, ws);
+  few_mxfp4(p, w);
+  p.perm = perm;
+  p.offsets = offsets;
+  p.y = nullptr;
+  p.y_sorted = reinterpret_cast<__nv_bfloat16 *>(y_sorted);
+  p.y_shared = reinterpret_cast<__nv_bfloat16 *>(y_shared);
+  return cuda_status(launch_few(p, true, num_sms(), stream));
 }
 
 // Steps a3-a9 from a given routing, with the gate and up projections of every
@@ -652,7 +685,7 @@ MOE_API moe_status moe_check_dims(const moe_dims *d) {
 
 MOE_API size_t moe_workspace_bytes(const moe_dims *d) {
   if (moe_check_dims(d) != MOE_OK) return 0;
-  return ws_layout(*d).total;
+  return ws_total(*d);
 }
 
 MOE_API moe_status moe_ws_init(void *ws, size_t ws_bytes, void *stream) {
@@ -923,18 +956,7 @@ MOE_API moe_status moe_expert_ffn_mxfp4(const moe_dims *d, const moe_bf16 *hidde
     return MOE_ERR_INVALID_ARG;
   if (d->has_shared && !ptr_ok(y_shared)) return MOE_ERR_INVALID_ARG;
   if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
-  if (d->T > kFewMaxT)
-    return do_expert_phases(*d, 3, hidden, perm, offsets, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
-                            y_sorted, y_shared, scratch_in(*d, ws), (cudaStream_t)stream, true, 0, nullptr, false,
-                            false, w);
-  FewParams p = few_params(*d, hidden, ws);
-  few_mxfp4(p, *w);
-  p.perm = perm;
-  p.offsets = offsets;
-  p.y = nullptr;
-  p.y_sorted = reinterpret_cast<__nv_bfloat16 *>(y_sorted);
-  p.y_shared = reinterpret_cast<__nv_bfloat16 *>(y_shared);
-  return cuda_status(launch_few(p, true, num_sms(), (cudaStream_t)stream));
+  return do_expert_ffn_mxfp4(*d, hidden, perm, offsets, *w, y_sorted, y_shared, ws, (cudaStream_t)stream, false);
 }
 
 MOE_API moe_status moe_layer_forward_mxfp4(const moe_dims *d, const moe_bf16 *hidden, const float *router_w,
@@ -957,9 +979,7 @@ MOE_API moe_status moe_layer_forward_mxfp4(const moe_dims *d, const moe_bf16 *hi
     moe_bf16 *y = at<moe_bf16>(ws, L.y_sorted), *z = at<moe_bf16>(ws, L.y_shared);
     if ((st = do_route(*d, hidden, router_w, expert_bias, nullptr, idx, wt, ws, s, true)) != MOE_OK) return st;
     if ((st = do_permute(*d, idx, at<int32_t>(ws, L.counts), offs, perm, inv, ws, s, true)) != MOE_OK) return st;
-    if ((st = do_expert_phases(*d, 3, hidden, perm, offs, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, y, z,
-                               scratch_in(*d, ws), s, true, 0, nullptr, true, false, w)) != MOE_OK)
-      return st;
+    if ((st = do_expert_ffn_mxfp4(*d, hidden, perm, offs, *w, y, z, ws, s, true)) != MOE_OK) return st;
     return do_combine(*d, y, z, inv, wt, out, s, true);
   }
   FewParams p = few_params(*d, hidden, ws);

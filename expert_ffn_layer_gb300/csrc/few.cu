@@ -45,8 +45,8 @@ constexpr int kFewWarps = 16, kFewThreads = kFewWarps * 32;
 constexpr int kStepBytes = 64;               // bytes of one row in a step
 constexpr int kStageW = 32 * kStepBytes;     // 32 rows: two 16-row operand tiles
 static_assert(kFewMaxT <= 2 * kFewWarps, "two tokens a warp in the selection");
-constexpr int kMaxPos = kFewMaxT * 16 + kFewMaxT;  // routed positions and shared rows
-constexpr int kMaxSegs = 256 + kFewMaxT * 16 / 8;
+constexpr int kMaxSegs = 256 + kFewFfnMaxS / 8;
+static_assert(kFewMaxT * 16 <= kFewFfnMaxS && kFewFfnMaxS + kFewFfnMaxT <= 4096, "positions in 12 bits");
 
 template <int WT>
 struct Fmt {  // weights: 0 bf16, 1 MXFP4
@@ -64,11 +64,11 @@ constexpr int kRedFloats = kFewWarps * 2 * kRedTile;  // one of two buffers
 struct FewTables {
   // segments: the active experts in order, each in pieces of at most 8 positions
   // (the columns of a product).  An expert of more re-reads its weights, by then in
-  // L2; with at most 32 tokens few have more.
-  int seg_e[kMaxSegs];
-  int seg_row0[kMaxSegs];  // first position of each
-  int seg_n[kMaxSegs];     // positions of each
-  int tok[kMaxPos];   // token of each routed position
+  // L2.
+  uint16_t seg_e[kMaxSegs];
+  uint16_t seg_row0[kMaxSegs];  // first position of each
+  uint16_t seg_n[kMaxSegs];     // positions of each
+  uint16_t tok[kFewFfnMaxS];    // token of each routed position
   int pos[kFewMaxT * 16];      // position of slot t * k + j
   float w[kFewMaxT * 16];      // combine weight of each slot
   int idx[kFewMaxT * 16];
@@ -265,7 +265,7 @@ struct Unit {
 
 // A warp's units in order, decoded 32 at a time, one by each lane, and read by
 // shuffles -- which also tells the compiler that they are the warp's, not the lane's.
-// Packed: positions (4 bits), first position (10), first row / 32 (10), shared (1),
+// Packed: positions (4 bits), first position (12), first row / 32 (10), shared (1),
 // and the steps: first (10), number (11).
 struct UnitList {
   int base, w_row, word, steps;
@@ -284,11 +284,11 @@ struct UnitList {
       if (sh) {
         const int seg = u / rb_s, rb = u - seg * rb_s;
         w_row = rb * 32 + off;
-        word = min(8, T - 8 * seg) | (S + 8 * seg) << 4 | rb << 14 | 1 << 24;
+        word = min(8, T - 8 * seg) | (S + 8 * seg) << 4 | rb << 16 | 1 << 26;
       } else {
         const int v = u - n_sh, seg = v / rb_r, rb = v - seg * rb_r;
         w_row = tb.seg_e[seg] * q.rows_r + rb * 32 + off;
-        word = tb.seg_n[seg] | tb.seg_row0[seg] << 4 | rb << 14;
+        word = tb.seg_n[seg] | tb.seg_row0[seg] << 4 | rb << 16;
       }
       const int s0 = sh ? (in_a ? a.s0[1] : b.s0[1]) : in_a ? a.s0[0] : b.s0[0];
       steps = s0 | (sh ? (in_a ? a.n[1] : b.n[1]) : in_a ? a.n[0] : b.n[0]) << 10;
@@ -300,9 +300,9 @@ struct UnitList {
     const int x = __shfl_sync(0xffffffffu, word, i - base), st = __shfl_sync(0xffffffffu, steps, i - base);
     t.w_row = __shfl_sync(0xffffffffu, w_row, i - base);
     t.ntok = x & 15;
-    t.row0 = x >> 4 & 1023;
-    t.row = (x >> 14 & 1023) << 5;
-    t.sh = x >> 24;
+    t.row0 = x >> 4 & 4095;
+    t.row = (x >> 16 & 1023) << 5;
+    t.sh = x >> 26;
     t.s0 = st & 1023;
     t.n = st >> 10;
     return t;

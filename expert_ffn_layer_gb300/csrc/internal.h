@@ -134,7 +134,8 @@ cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales,
                                     cudaStream_t stream);
 
 // ------------------------------------------------- the layer for few tokens
-constexpr int kFewMaxT = 32;  // a token per bit of an expert's mask
+constexpr int kFewMaxT = 32;                     // of the whole layer: a token per bit of an expert's mask
+constexpr int kFewFfnMaxT = 256, kFewFfnMaxS = 2048;  // of the expert FFN alone: the tables in shared memory
 struct FewParams {
   const __nv_bfloat16 *hidden;  // [T][H]
   const uint16_t *x;            // the products' token operand: hidden, or x16 with MXFP4 weights

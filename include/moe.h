@@ -344,16 +344,17 @@ moe_status moe_dequantize_mxfp4_rows(const uint8_t *codes, const uint8_t *scales
 /* moe_expert_ffn and moe_layer_forward with MXFP4 expert weights (all pointers
  * in *w 16-byte aligned); arguments, layouts and errors as for those.  H, I and
  * I_shared multiples of 128 (else MOE_ERR_UNSUPPORTED).
- *   Batches of at most 32 tokens run as one kernel (for the layer: router,
- *   selection, experts and combine).  It multiplies the code values, exact in fp16,
+ *   The layer of at most 32 tokens runs as one kernel (router, selection, experts
+ *   and combine), and so does the expert FFN of at most 32 tokens or, up to 256
+ *   tokens and 2048 slots, of at most 12 slots an expert on average.  It multiplies the code values, exact in fp16,
  *   by the token values as fp16 times a power of two of the row's largest magnitude
  *   -- exact for bf16 values down to 2^-28 of it; the fp32 activation is rounded to
  *   fp16's 11 bits, scaled likewise per 32 values -- sums in fp32 and applies each
  *   block's scale to the block's own fp32 sum.  The layer's output is rounded once.
  *   Such a call needs the whole device: it is a cooperative launch, whose blocks
  *   (one per SM) are resident together.
- *   Larger batches run the chain of kernels of moe_layer_forward; its expert kernel
- *   expands the weights to bf16 in shared memory (exact) and keeps the activations
+ *   Larger layers run the chain of kernels of moe_layer_forward, and the expert kernel
+ *   of larger batches expands the weights to bf16 in shared memory (exact) and keeps the activations
  *   between the products in bf16, as with bf16 weights.
  *   In the products of either form a scale byte of 0 (2^-127) counts as zero. */
 moe_status moe_expert_ffn_mxfp4(const moe_dims *d, const moe_bf16 *hidden, const int32_t *perm,
