@@ -536,6 +536,39 @@ def run_ours(args, rank, world, local_rank):
             del fp8, fgraph, eg, wgraph, weg
         except Exception as e:  # an auxiliary measurement: record the failure, keep the headline
             result["fp8_decode"] = {"error": f"{type(e).__name__}: {e}"}
+    # ---------------- the same decode layer in one kernel: with the bf16 weights
+    # (moe_layer_forward_few) and with MXFP4 ones (moe_layer_forward_mxfp4)
+    if world == 1 and not args.no_few:
+        try:
+            nout = torch.empty_like(out)
+
+            def few_step():
+                moe.moe_layer_forward_few(d, hidden, layer.router_w, layer.expert_bias, layer.w_gate, layer.w_up,
+                                          layer.w_down, layer.ws_gate, layer.ws_up, layer.ws_down, nout, layer.ws)
+
+            ngraph = graph_of(few_step, 1)
+            nms = float(np.sum(timed(ngraph.replay, args.steps, args.warmup))) / args.steps
+            result["few_decode"] = {"value": round(w.T / (nms * 1e-3), 1), "unit": UNIT, "ms_per_step": round(nms, 5),
+                                    "launch": "CUDA graph of one layer forward (one kernel)",
+                                    "device_error": moe.moe_ws_read_error(layer.ws)}
+            mx = moe.quantize_mxfp4_experts(layer.w_gate, layer.w_up, layer.w_down, layer.ws_gate, layer.ws_up,
+                                            layer.ws_down)
+
+            def mx_step():
+                moe.moe_layer_forward_mxfp4(d, hidden, layer.router_w, layer.expert_bias, mx, nout, layer.ws)
+
+            mgraph = graph_of(mx_step, 1)
+            mms = float(np.sum(timed(mgraph.replay, args.steps, args.warmup))) / args.steps
+            mbytes = (n_active * 3 * w.I + 3 * w.I_shared) * w.H * 17 // 32
+            result["mxfp4_decode"] = {"weights": "MXFP4: E2M1 codes, one power-of-two scale per 32 (17/32 byte a weight)",
+                                      "value": round(w.T / (mms * 1e-3), 1), "unit": UNIT,
+                                      "ms_per_step": round(mms, 5), "layer_weight_bytes": mbytes,
+                                      "layer_weight_gbs": round(mbytes / (mms * 1e-3) / 1e9, 1),
+                                      "launch": "CUDA graph of one layer forward (one kernel)",
+                                      "device_error": moe.moe_ws_read_error(layer.ws)}
+            del ngraph, mgraph, mx
+        except Exception as e:  # an auxiliary measurement: record the failure, keep the headline
+            result["few_decode"] = {"error": f"{type(e).__name__}: {e}"}
     del layer, hidden, layer_graph
     torch.cuda.empty_cache()
 
@@ -781,6 +814,7 @@ def main():
                     help="skip the skewed long-prefill (T=16384) and HunyuanImage (T=8192) measurements")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-fp8", action="store_true", help="skip the FP8-weight decode measurement")
+    ap.add_argument("--no-few", action="store_true", help="skip the one-kernel and MXFP4 decode measurements")
     ap.add_argument("--fp8", action="store_true", help="with --profile: run the layer with FP8 expert weights")
     ap.add_argument("--w8a8", action="store_true", help="with --profile: run the W8A8 layer (FP8 weights and activations)")
     ap.add_argument("--phases", action="store_true",
