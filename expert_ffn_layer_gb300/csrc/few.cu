@@ -22,7 +22,7 @@
 // to CTAs round robin; KS is chosen so that the last round is as short as it can be.
 // Nothing is added by atomics: results do not depend on timing.
 //
-// Weights travel through a ring of NST steps per warp (64 bytes of each of 32 rows)
+// Weights travel through a ring of steps per warp (64 bytes of each of 32 rows)
 // by cp.async.  Each lane copies exactly the 16-byte pieces it will read itself, so
 // the ring needs no barrier; it keeps filling across units, and before the wait
 // between the two products it already holds the first steps of the second.
@@ -53,9 +53,12 @@ struct Fmt {  // weights: 0 bf16, 1 MXFP4
   static constexpr int kStep = WT ? 128 : 32;   // K values of a step
   static constexpr int kGroups = kStep / 32;    // groups of 32 K values (two matrix instructions each)
   static constexpr int kStage = kStageW + (WT ? 128 : 0);  // with the 32 rows' four scale bytes
+  // Steps of a warp's ring.  MXFP4: three, which leaves 32 KB more of L1 to the token
+  // operand (Hy3 T = 8 expert FFN 118 -> 114 us); bf16 is better off with the fourth
+  // (Hy3 T = 1: 73 us, and 76 with three).
+  static constexpr int kNst = WT ? 3 : 4;
 };
 
-constexpr int kNst = 4;         // steps of a warp's ring (a power of two)
 constexpr int kRedCol = 20;     // floats from one column of a partial 16 x 8 tile to the next (16 rows: no bank conflicts)
 constexpr int kRedTile = 8 * kRedCol;
 constexpr int kRedFloats = kFewWarps * 2 * kRedTile;  // one of two buffers
@@ -312,7 +315,7 @@ struct UnitList {
 // One phase over this CTA's units.  DOWN: the products with w_down, else gate/up.
 template <int WT, bool DOWN>
 __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, float *red, unsigned *wait_for, bool &ok) {
-  constexpr int G = Fmt<WT>::kGroups, STAGE = Fmt<WT>::kStage;
+  constexpr int G = Fmt<WT>::kGroups, STAGE = Fmt<WT>::kStage, kNst = Fmt<WT>::kNst;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const int K_r = DOWN ? p.I : p.H, K_s = DOWN ? p.Is : p.H;
   const Plan q = make_plan<WT, DOWN>(tb, DOWN ? p.H : p.I, DOWN ? p.H : p.Is, K_r / Fmt<WT>::kStep,
@@ -371,7 +374,7 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
       ++fs;
     }
     cp_async_commit();
-    fslot = (fslot + 1) & (kNst - 1);
+    fslot = fslot + 1 == kNst ? 0 : fslot + 1;
   };
 #pragma unroll 1
   for (int i = 0; i < kNst - 1; ++i) fill();
@@ -460,7 +463,7 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
       __syncwarp();
       fill();  // into the slot read in the previous step
       const uint32_t st = my_ring + slot * STAGE;
-      slot = (slot + 1) & (kNst - 1);
+      slot = slot + 1 == kNst ? 0 : slot + 1;
       const uint32_t wa = st + g * kStepBytes + t4 * 16;
       uint4 v[4];  // tile 0 rows g, g + 8; tile 1 rows g, g + 8
 #pragma unroll
@@ -886,7 +889,7 @@ __device__ void prefetch_shared(const FewParams &p) {
 
 template <int WT>
 struct FewSmem {
-  static constexpr int kRing = kFewWarps * kNst * Fmt<WT>::kStage;
+  static constexpr int kRing = kFewWarps * Fmt<WT>::kNst * Fmt<WT>::kStage;
   static constexpr int kRed = 2 * kRedFloats * 4;
   static constexpr int kBytes = kRing + kRed + (int)sizeof(FewTables);
   static_assert(kBytes <= 232448, "shared memory budget");
