@@ -42,15 +42,18 @@ namespace moe {
 namespace {
 
 constexpr int kFewWarps = 16, kFewThreads = kFewWarps * 32;
-constexpr int kStepBytes = 64;               // bytes of one row in a step
-constexpr int kStageW = 32 * kStepBytes;     // 32 rows: two 16-row operand tiles
+constexpr int kStageW = 2048;  // weight bytes of a ring slot
 static_assert(kFewMaxT <= 2 * kFewWarps, "two tokens a warp in the selection");
 constexpr int kMaxSegs = 256 + kFewFfnMaxS / 8;
 static_assert(kFewMaxT * 16 <= kFewFfnMaxS && kFewFfnMaxS + kFewFfnMaxT <= 4096, "positions in 12 bits");
 
 template <int WT>
 struct Fmt {  // weights: 0 bf16, 1 MXFP4
-  static constexpr int kStep = WT ? 128 : 32;   // K values of a step
+  // K values of a step, and its ring slots: both 16-row tiles' 64 bytes a row in one slot
+  // (MXFP4), or a slot for each tile's 128 bytes a row (bf16: whole lines, as the memory
+  // likes them: Hy3 T = 8 356 -> 342 us, T = 32 863 -> 849 us)
+  static constexpr int kStep = WT ? 128 : 64;
+  static constexpr int kSlots = WT ? 1 : 2;
   static constexpr int kGroups = kStep / 32;    // groups of 32 K values (two matrix instructions each)
   static constexpr int kStage = kStageW + (WT ? 128 : 0);  // with the 32 rows' four scale bytes
   // Steps of a warp's ring.  MXFP4: three, which leaves 32 KB more of L1 to the token
@@ -205,7 +208,7 @@ struct Plan {
 // One lane tries one pair.
 template <int WT, bool DOWN>
 __device__ Plan make_plan(const FewTables &tb, int rows_r, int rows_s, int steps_r, int steps_s, int lane) {
-  constexpr int kChoices = DOWN ? 5 : 4, kStepCycles = WT ? 2000 : 1400, kUnitCycles = WT ? 2000 : 600;
+  constexpr int kChoices = DOWN ? 5 : 4, kStepCycles = WT ? 2000 : 2800, kUnitCycles = WT ? 2000 : 600;
   Plan q;
   q.rows_r = rows_r;
   q.rows_s = rows_s;
@@ -214,10 +217,10 @@ __device__ Plan make_plan(const FewTables &tb, int rows_r, int rows_s, int steps
   q.units = (tb.nsh * rows_s + tb.nact * rows_r) >> 5;
   const int a = lane / kChoices, b = lane % kChoices, steps = max(steps_r, tb.nsh ? steps_s : 0);
   unsigned cost = 0x7fffffffu;
-  // bf16, bound by the memory: at least as many slices as leave a warp six steps, up to
+  // bf16, bound by the memory: at least as many slices as leave a warp three steps, up to
   // eight -- fewer and longer ones spread the reads (8 and 4 slices at Hy3 T = 32: 841 and
   // 856 us; two at T = 8: 385 against 353).  MXFP4, bound by instructions, gains from few.
-  const bool near = WT || a >= 3 || steps >> (a + 1) < 6;
+  const bool near = WT || a >= 3 || steps >> (a + 1) < 3;
   if (a < kChoices && b >= a && near) {
     auto round = [&](int sh) { return ((steps + (1 << sh) - 1) >> sh) * kStepCycles + kUnitCycles; };
     auto teams = [&](int sh) { return (int)gridDim.x * (kFewWarps >> (DOWN ? sh : sh + 1)); };
@@ -315,7 +318,7 @@ struct UnitList {
 // One phase over this CTA's units.  DOWN: the products with w_down, else gate/up.
 template <int WT, bool DOWN>
 __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, float *red, unsigned *wait_for, bool &ok) {
-  constexpr int G = Fmt<WT>::kGroups, STAGE = Fmt<WT>::kStage, kNst = Fmt<WT>::kNst;
+  constexpr int G = Fmt<WT>::kGroups, STAGE = Fmt<WT>::kStage, kNst = Fmt<WT>::kNst, kSlots = Fmt<WT>::kSlots;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const int K_r = DOWN ? p.I : p.H, K_s = DOWN ? p.Is : p.H;
   const Plan q = make_plan<WT, DOWN>(tb, DOWN ? p.H : p.I, DOWN ? p.H : p.Is, K_r / Fmt<WT>::kStep,
@@ -333,7 +336,7 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
   // ---- the weight stream: the unit and step to copy next
   int fi = 0, fs = 0, fn = 0, fslot = 0;
   const uint8_t *f0 = nullptr, *f1 = nullptr, *fsc = nullptr;
-  uint32_t f8 = 0;  // bytes from a row to the one eight below
+  uint32_t f_rows = 0;  // bytes from a lane's row to its next
   auto fill = [&]() {  // copy one step and commit it (an empty group past the end)
     if (fs == fn) {    // on to the next unit in which this warp has steps
       fs = fn = 0;
@@ -346,10 +349,14 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
           const uint32_t rowb = WT ? K / 2 : K * 2;
           const uint8_t *m0 = DOWN ? (f.sh ? p.s_down : p.down) : (f.sh ? p.s_gate : p.gate);
           const uint8_t *m1 = DOWN ? m0 + 16 * rowb : (f.sh ? p.s_up : p.up);
-          const size_t at = (size_t)(f.w_row + g) * rowb + f.s0 * kStepBytes + t4 * 16;
+          // MXFP4: lane (g, t) copies the 16 bytes of rows g, g + 8 of both tiles that it will
+          // itself read; bf16: eight lanes copy a line, four rows at a time
+          const size_t at = WT ? (size_t)(f.w_row + g) * rowb + f.s0 * 64 + t4 * 16
+                               : (size_t)(f.w_row + (lane >> 3)) * rowb + f.s0 * 128 + (lane & 7) * 16;
           f0 = m0 + at;
           f1 = m1 + at;
-          f8 = 8 * rowb;
+          f_rows = (WT ? 8 : 4) * rowb;
+          fn *= kSlots;
           if constexpr (WT) {
             const uint32_t sb = K / 32;
             const uint8_t *c0 = DOWN ? (f.sh ? p.s_down_scale : p.down_scale) : (f.sh ? p.s_gate_scale : p.gate_scale);
@@ -360,16 +367,27 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
       }
     }
     if (fs < fn) {
-      const uint32_t d = my_ring + fslot * STAGE + g * kStepBytes + t4 * 16;
-      cp_async16(d, f0, pol);
-      cp_async16(d + 8 * kStepBytes, f0 + f8, pol);
-      cp_async16(d + 16 * kStepBytes, f1, pol);
-      cp_async16(d + 24 * kStepBytes, f1 + f8, pol);
-      f0 += kStepBytes;
-      f1 += kStepBytes;
+      const uint32_t d = my_ring + fslot * STAGE;
       if constexpr (WT) {
-        cp_async4(my_ring + fslot * STAGE + kStageW + lane * 4, fsc);
+        const uint32_t dw = d + g * 64 + t4 * 16;
+        cp_async16(dw, f0, pol);
+        cp_async16(dw + 512, f0 + f_rows, pol);
+        cp_async16(dw + 1024, f1, pol);
+        cp_async16(dw + 1536, f1 + f_rows, pol);
+        f0 += 64;
+        f1 += 64;
+        cp_async4(d + kStageW + lane * 4, fsc);
         fsc += 4;
+      } else {
+        // odd rows' halves change places, so that the reads below meet all banks
+        const uint32_t dw = d + (lane >> 3) * 128 + ((lane & 7) ^ (lane >> 1 & 4)) * 16;
+        const uint8_t *src = fs & 1 ? f1 : f0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cp_async16(dw + i * 512, src + i * f_rows, pol);
+        if (fs & 1) {
+          f0 += 128;
+          f1 += 128;
+        }
       }
       ++fs;
     }
@@ -388,7 +406,7 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
   // ---- the token operand: this lane's 8 values of each group of 32, for column g
   // (columns past the segment's repeat its last: their sums are not read), a step
   // ahead of their use.  MXFP4: each register is loaded anew as soon as the step has
-  // used it; bf16, whose steps are a quarter as long: a second set of registers.
+  // used it; bf16, whose steps are shorter: a second set of registers.
   constexpr int kB = (DOWN && !WT) ? 2 * G : G;
   uint4 bv[kB];
   uint32_t ex[2] = {0u, 0u};            // MXFP4 down: the groups' exponents for columns 2 t, 2 t + 1
@@ -431,6 +449,14 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
   };
 
   int slot = 0, buf = 0;
+  auto next_slot = [&]() {  // the next slot of the ring, once its copies are there
+    cp_async_wait<kNst - 2>();
+    __syncwarp();
+    fill();  // into the slot read before it
+    const uint32_t st = my_ring + slot * STAGE;
+    slot = slot + 1 == kNst ? 0 : slot + 1;
+    return st;
+  };
   Unit nxt = list.get(0);
   if (nxt.n > 0) first_b(nxt);
 #pragma unroll 1
@@ -453,22 +479,11 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
       } else if (nxt.n > 0) {
         point(nxt);
       }
-      uint4 b0[kB];
-      if constexpr (!WT) {
-#pragma unroll
-        for (int i = 0; i < kB; ++i) b0[i] = bv[i];
-        load_b(0);
-      }
-      cp_async_wait<kNst - 2>();
-      __syncwarp();
-      fill();  // into the slot read in the previous step
-      const uint32_t st = my_ring + slot * STAGE;
-      slot = slot + 1 == kNst ? 0 : slot + 1;
-      const uint32_t wa = st + g * kStepBytes + t4 * 16;
-      uint4 v[4];  // tile 0 rows g, g + 8; tile 1 rows g, g + 8
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = lds128(wa + i * 8 * kStepBytes);
       if constexpr (WT) {
+        const uint32_t st = next_slot();
+        uint4 v[4];  // tile 0 rows g, g + 8; tile 1 rows g, g + 8
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = lds128(st + g * 64 + t4 * 16 + i * 512);
         uint32_t sc[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[i] = lds32(st + kStageW + (i * 8 + g) * 4);
@@ -504,24 +519,42 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
           }
         }
       } else {
-        uint32_t bh[4] = {b0[0].x, b0[0].y, b0[0].z, b0[0].w}, bl[4];
-        if constexpr (DOWN) {  // the fp32 activation as the sum of two bf16 values (16 of its 24 bits)
-          const uint32_t xu[8] = {bh[0], bh[1], bh[2], bh[3], b0[kB - 1].x, b0[kB - 1].y, b0[kB - 1].z, b0[kB - 1].w};
+        uint32_t bh[2][4], bl[2][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float fa = __uint_as_float(xu[2 * i]), fb = __uint_as_float(xu[2 * i + 1]);
-            bh[i] = pack_bf16(fa, fb);
-            bl[i] = pack_bf16(fa - __uint_as_float(bh[i] << 16), fb - __uint_as_float(bh[i] & 0xFFFF0000u));
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (DOWN) {  // the fp32 activation as the sum of two bf16 values (16 of its 24 bits)
+            const uint4 x0 = bv[kB > 2 ? 2 * h : 0], x1 = bv[kB > 2 ? 2 * h + 1 : 0];
+            const uint32_t xu[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float fa = __uint_as_float(xu[2 * i]), fb = __uint_as_float(xu[2 * i + 1]);
+              bh[h][i] = pack_bf16(fa, fb);
+              bl[h][i] = pack_bf16(fa - __uint_as_float(bh[h][i] << 16), fb - __uint_as_float(bh[h][i] & 0xFFFF0000u));
+            }
+          } else {
+            bh[h][0] = bv[h].x, bh[h][1] = bv[h].y, bh[h][2] = bv[h].z, bh[h][3] = bv[h].w;
           }
+          load_b(h);
         }
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
-          const uint4 &r0 = v[2 * a], &r8 = v[2 * a + 1];
-          mma16<false>(acc[a], r0.x, r8.x, r0.y, r8.y, bh[0], bh[1]);
-          mma16<false>(acc[a], r0.z, r8.z, r0.w, r8.w, bh[2], bh[3]);
-          if constexpr (DOWN) {
-            mma16<false>(acc[a], r0.x, r8.x, r0.y, r8.y, bl[0], bl[1]);
-            mma16<false>(acc[a], r0.z, r8.z, r0.w, r8.w, bl[2], bl[3]);
+          const uint32_t st = next_slot() + g * 128;
+          uint4 v[2][2];  // both halves of 32 values, rows g, g + 8
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t at = st + (((t4 | h << 2) ^ (g << 2 & 4)) << 4);
+            v[h][0] = lds128(at);
+            v[h][1] = lds128(at + 1024);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 &r0 = v[h][0], &r8 = v[h][1];
+            mma16<false>(acc[a], r0.x, r8.x, r0.y, r8.y, bh[h][0], bh[h][1]);
+            mma16<false>(acc[a], r0.z, r8.z, r0.w, r8.w, bh[h][2], bh[h][3]);
+            if constexpr (DOWN) {
+              mma16<false>(acc[a], r0.x, r8.x, r0.y, r8.y, bl[h][0], bl[h][1]);
+              mma16<false>(acc[a], r0.z, r8.z, r0.w, r8.w, bl[h][2], bl[h][3]);
+            }
           }
         }
       }
