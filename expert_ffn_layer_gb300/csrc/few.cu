@@ -1,34 +1,41 @@
-// The MoE FFN layer for few tokens (at most 32) in one kernel: router, top-k,
-// the experts' gate/up, SiLU(gate) * up and down products, the shared expert and
-// the weighted combine; and, with a routing given, the expert FFN alone.
+// The MoE FFN layer for few tokens in one kernel: router, top-k, the experts'
+// gate/up, SiLU(gate) * up and down products, the shared expert and the weighted
+// combine; and, with a routing given, the expert FFN alone.
 //
-//   logits[t, e] = x[t] . Wr[e]                      (fp32, [hy3] Model facts)
-//   a[p, i]  = SiLU(x[t] . Wg[e, i]) * (x[t] . Wu[e, i])   p = (e, t), e in top-k of t
+//   logits[t, e] = x[t] . Wr[e]                            (fp32)
+//   a[p, i]  = SiLU(x[t] . Wg[e, i]) * (x[t] . Wu[e, i])   p = (e, t), e in the top-k of t
 //   y[p, h]  = a[p] . Wd[e, h]
 //   out[t]   = sum_j w[t, j] y[p(t, j)] + shared FFN(x[t])
+//
+// "hy3 -- tencent/Hy3 GGUF Converter and Inference Engine", Model facts (router, MoE
+// routing); HunyuanImage 3.0 post (easy_topk, Routed Experts, Shared MLP).  Weights
+// are bf16, or MXFP4 (mxfp4.cuh).
 //
 // What bounds it: the active experts' weights, each read once.  A token or two per
 // expert is no work for the tensor cores -- the products are matrix-vector -- so
 // every choice serves the weight stream.  mma.sync (m16n8k16) is used rather than
-// tcgen05 because its A operand comes straight from registers: weights go from
-// memory to the lane that multiplies them, with no shared tile, no barrier and no
-// conversion pass between (MXFP4 codes become fp16 in registers), and its rate is
-// an order of magnitude above what the stream can feed at 8 tokens.
+// tcgen05 because its A operand comes from registers: MXFP4 codes become fp16 there,
+// two by an instruction, with no pass through shared memory between.  Its pipe is
+// under a quarter busy.  With MXFP4 the bound is instructions: of about 300 a step
+// (32 rows x 128 codes) and warp, 64 expand codes, 64 to 100 apply the blocks' scales.
 //
-// Work.  One CTA of 16 warps per SM, all resident (cooperative launch).  A unit is
-// 16 RG gate rows and the same up rows (gate/up), or 32 RG rows of w_down (down), of
-// one expert; warp w takes row group w / KS and K slice w % KS (RG KS = 16), and the
-// KS partial products are added in a fixed order through shared memory.  Units go
-// to CTAs round robin; KS is chosen so that the last round is as short as it can be.
-// Nothing is added by atomics: results do not depend on timing.
+// Measured (GB300, Hy3 shape, time of a call and share of the measured copy bandwidth
+// that the active weights come in at): bf16 T = 1 66 us (0.76), T = 8 341 us (0.95), T =
+// 32 841 us (0.92); MXFP4 layer T = 1 39 us (0.38), T = 8 125 us (0.69); MXFP4 expert
+// FFN T = 8 114 us (0.73).
 //
-// Weights travel through a ring of steps per warp (64 bytes of each of 32 rows)
-// by cp.async.  Each lane copies exactly the 16-byte pieces it will read itself, so
-// the ring needs no barrier; it keeps filling across units, and before the wait
-// between the two products it already holds the first steps of the second.
+// Work.  One CTA of 16 warps per SM, all resident (cooperative launch).  Units of 32
+// rows go to teams of warps that split K (Plan below); the partial products are added
+// in a fixed order through shared memory, and experts' outputs in slot order by a last
+// phase.  Nothing is added by atomics: results do not depend on timing.
 //
-// Two grid-wide waits order the phases (logits -> selection, activations -> down).
-// They are bounded like every wait here: a CTA that gives up sets
+// Weights travel through a ring of steps per warp by cp.async.  No other warp reads a
+// ring, so it needs no barrier; it keeps filling across units, and before the wait
+// between the two products it already holds the first steps of the second.  (Bringing
+// more of the second's weights into L2 during that wait: no gain, T = 8 343 us.)
+//
+// Three grid-wide waits order the phases (logits -> selection, activations -> down,
+// outputs -> combine).  They are bounded like every wait here: a CTA that gives up sets
 // MOE_DEVERR_TIMEOUT and the kernel winds down.
 #include <climits>
 
@@ -43,7 +50,6 @@ namespace {
 
 constexpr int kFewWarps = 16, kFewThreads = kFewWarps * 32;
 constexpr int kStageW = 2048;  // weight bytes of a ring slot
-static_assert(kFewMaxT <= 2 * kFewWarps, "two tokens a warp in the selection");
 constexpr int kMaxSegs = 256 + kFewFfnMaxS / 8;
 static_assert(kFewMaxT * 16 <= kFewFfnMaxS && kFewFfnMaxS + kFewFfnMaxT <= 4096, "positions in 12 bits");
 
@@ -79,6 +85,7 @@ struct FewTables {
   float w[kFewMaxT * 16];      // combine weight of each slot
   int idx[kFewMaxT * 16];
   unsigned mask[256];          // tokens of each expert
+  float bias[256];             // of the keys
   int base[256];               // first position of each expert
   int scan[8];                 // build_segments' warp totals
   int nact, nsh;               // routed segments; the shared expert's pieces of 8 tokens
@@ -764,117 +771,77 @@ __device__ __forceinline__ int ordered(float f) {
   return b ^ ((b >> 31) & 0x7FFFFFFF);
 }
 
-// Selection of NT tokens (t, t + kFewWarps; past the last: none) by a warp, E <= 32 NJ,
-// with the rule and results of the router's top-k kernel.  Each lane sorts its NJ
-// experts by key once (equal keys: the lower expert first); a round takes the largest
-// head by one integer reduction over the lanes, the lower of equal experts by another.
-template <int NT, int NJ>
-__device__ __forceinline__ void select_tokens(const FewParams &p, FewTables &tb, int t, const float (&bias)[8], int lane) {
+// Selection of token t by a warp, with the rule and results of the router's top-k
+// kernel: each round the largest key by one integer reduction over the lanes, the
+// lower of equal experts by another.  Every CTA runs it once a call, so what it costs
+// is fetching its code: rolled loops over scores and keys in shared memory (2 KB a
+// warp) rather than unrolled ones in registers (Hy3 T = 1 with a cold L2: bf16 72 us against 80,
+// MXFP4 46 against 53).
+__device__ __forceinline__ void select_token(const FewParams &p, FewTables &tb, int t, float *sc, int lane) {
   const int E = p.E, k = p.top_k;
-  float sc[NT][NJ];
+  int *key = reinterpret_cast<int *>(sc + 256);
+  float v[8];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int tk = min(t + n * kFewWarps, p.T - 1);
+  for (int j = 0; j < 8; ++j) v[j] = lane + 32 * j < E ? __ldcg(p.logits + (size_t)t * E + lane + 32 * j) : -INFINITY;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
-      sc[n][j] = lane + 32 * j < E ? __ldcg(p.logits + (size_t)tk * E + lane + 32 * j) : -INFINITY;
+  for (int j = 0; j < 8; ++j) sc[lane + 32 * j] = v[j];  // a lane reads only what it wrote
+  const bool sigmoid = p.score_mode == MOE_SCORE_SIGMOID_BIAS;
+  float mx = 0.0f, sum = 1.0f;
+  if (!sigmoid) {
+    mx = -INFINITY;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) mx = fmaxf(mx, sc[e]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    sum = 0.0f;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) sum += expf(sc[e] - mx);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
-  int key[NT][NJ], order[NT];  // sorted keys, and their j's in nibbles, the head's lowest
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    if (p.score_mode == MOE_SCORE_SIGMOID_BIAS) {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) sc[n][j] = 1.0f / (1.0f + expf(-sc[n][j]));
-    } else {
-      float mx = -INFINITY, sum = 0.0f;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) mx = fmaxf(mx, sc[n][j]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        sc[n][j] = lane + 32 * j < E ? expf(sc[n][j] - mx) : 0.0f;
-        sum += sc[n][j];
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) sc[n][j] = sc[n][j] / sum;
-    }
-    int at[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const float kk = sc[n][j] + bias[j] + 0.0f;  // -0 as 0
-      key[n][j] = lane + 32 * j < E ? (kk == kk ? ordered(kk) : ordered(-INFINITY)) : INT_MIN;
-      at[j] = j;
-    }
-    // odd-even transposition: neighbours only, and only a strictly larger key passes, so
-    // equal keys keep their order
-#pragma unroll
-    for (int r = 0; r < NJ; ++r)
-#pragma unroll
-      for (int j = r & 1; j + 1 < NJ; j += 2) {
-        const bool swap = key[n][j + 1] > key[n][j];
-        const int hi = swap ? key[n][j + 1] : key[n][j], lo = swap ? key[n][j] : key[n][j + 1];
-        const int ah = swap ? at[j + 1] : at[j], al = swap ? at[j] : at[j + 1];
-        key[n][j] = hi;
-        key[n][j + 1] = lo;
-        at[j] = ah;
-        at[j + 1] = al;
-      }
-    order[n] = 0;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) order[n] |= at[j] << (4 * j);
+#pragma unroll 1
+  for (int e = lane; e < E; e += 32) {
+    const float x = expf(sigmoid ? -sc[e] : sc[e] - mx);
+    const float s = (sigmoid ? 1.0f : x) / (sigmoid ? 1.0f + x : sum);
+    const float kk = s + tb.bias[e] + 0.0f;  // -0 as 0
+    sc[e] = s;
+    key[e] = kk == kk ? ordered(kk) : ordered(-INFINITY);
   }
-  int my_e[NT] = {};
+  int my_e = 0;
 #pragma unroll 1
   for (int r = 0; r < k; ++r) {
+    int bk = INT_MIN, be = 0x7fffffff;
+    int x[8];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int head = key[n][0], mine = lane + 32 * (order[n] & 7);
-      const int top = __reduce_max_sync(0xffffffffu, head);
-      const int e = __reduce_min_sync(0xffffffffu, head == top ? mine : 0x7fffffff);
-      if (lane == r) my_e[n] = e;
-      if (e == mine) {  // the winner's list moves up
+    for (int j = 0; j < 8; ++j) x[j] = lane + 32 * j < E ? key[lane + 32 * j] : INT_MIN;
 #pragma unroll
-        for (int j = 0; j + 1 < NJ; ++j) key[n][j] = key[n][j + 1];
-        key[n][NJ - 1] = INT_MIN;
-        order[n] >>= 4;
+    for (int j = 0; j < 8; ++j)
+      if (x[j] > bk) {
+        bk = x[j];
+        be = lane + 32 * j;
       }
-    }
+    const int top = __reduce_max_sync(0xffffffffu, bk);
+    const int e = __reduce_min_sync(0xffffffffu, bk == top ? be : 0x7fffffff);
+    if (lane == r) my_e = e;
+    if (be == e) key[e] = INT_MIN;  // taken
   }
+  __syncwarp();
+  const float s = lane < k ? sc[my_e] : 0.0f;
+  float tot = s;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int tk = t + n * kFewWarps;
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const float v = __shfl_sync(0xffffffffu, sc[n][j], my_e[n] & 31);
-      if (my_e[n] >> 5 == j) s = v;
-    }
-    float tot = lane < k ? s : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-    if (lane < k && tk < p.T) {
-      tb.idx[tk * k + lane] = my_e[n];
-      tb.w[tk * k + lane] = p.score_mode == MOE_SCORE_SIGMOID_BIAS ? s / tot * p.route_scale : s / fmaxf(tot, p.renorm_eps);
-      atomicOr(&tb.mask[my_e[n]], 1u << tk);
-    }
+  for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+  if (lane < k) {
+    tb.idx[t * k + lane] = my_e;
+    tb.w[t * k + lane] = sigmoid ? s / tot * p.route_scale : s / fmaxf(tot, p.renorm_eps);
+    atomicOr(&tb.mask[my_e], 1u << t);
   }
 }
 
 // Selection and tables from the logits (tb.mask is zero).
-__device__ void tables_from_logits(const FewParams &p, FewTables &tb, const float (&bias)[8]) {
+__device__ void tables_from_logits(const FewParams &p, FewTables &tb, float *scratch) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = p.top_k;
-  if (p.T > kFewWarps) {
-    if (p.E <= 64) select_tokens<2, 2>(p, tb, warp, bias, lane);
-    else if (p.E <= 192) select_tokens<2, 6>(p, tb, warp, bias, lane);
-    else select_tokens<2, 8>(p, tb, warp, bias, lane);
-  } else if (warp < p.T) {
-    if (p.E <= 64) select_tokens<1, 2>(p, tb, warp, bias, lane);
-    else if (p.E <= 192) select_tokens<1, 6>(p, tb, warp, bias, lane);
-    else select_tokens<1, 8>(p, tb, warp, bias, lane);
-  }
+#pragma unroll 1
+  for (int t = warp; t < p.T; t += kFewWarps) select_token(p, tb, t, scratch + warp * 512, lane);
   __syncthreads();
   build_segments(tb, threadIdx.x < 256 ? __popc(tb.mask[threadIdx.x]) : 0);
   __syncthreads();
@@ -924,6 +891,7 @@ template <int WT>
 struct FewSmem {
   static constexpr int kRing = kFewWarps * Fmt<WT>::kNst * Fmt<WT>::kStage;
   static constexpr int kRed = 2 * kRedFloats * 4;
+  static_assert(kRed >= kFewWarps * 2048, "the selection's scores and keys share the reduction buffer");
   static constexpr int kBytes = kRing + kRed + (int)sizeof(FewTables);
   static_assert(kBytes <= 232448, "shared memory budget");
 };
@@ -944,12 +912,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     tb.nsh = p.has_shared ? (p.T + 7) >> 3 : 0;
   }
   if (threadIdx.x < 256) tb.mask[threadIdx.x] = 0u;
-  float bias[8];  // of this lane's experts, wanted after the first wait
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int e = (threadIdx.x & 31) + 32 * j;
-    bias[j] = p.bias != nullptr && e < p.E ? __ldg(p.bias + e) : 0.0f;
-  }
+  if (threadIdx.x < 256) tb.bias[threadIdx.x] = p.bias != nullptr && (int)threadIdx.x < p.E ? __ldg(p.bias + threadIdx.x) : 0.0f;
   if (WT)
     for (int t = gridDim.x - 1 - blockIdx.x; t < p.T; t += gridDim.x) convert_token(p, t, reinterpret_cast<unsigned *>(red));
   __syncthreads();
@@ -960,7 +923,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   bool ok = true;
   if (route || WT) ok = grid_wait(p, bar, tb);
   if (ok) {
-    if (route) tables_from_logits(p, tb, bias);
+    if (route) tables_from_logits(p, tb, red);
     run_phase<WT, false>(p, tb, ring, red, nullptr, ok);
   }
   grid_arrive(bar + 1);  // also after a wait that ran out: the others need not wait for theirs to do so
