@@ -16,13 +16,13 @@
 // every choice serves the weight stream.  mma.sync (m16n8k16) is used rather than
 // tcgen05 because its A operand comes from registers: MXFP4 codes become fp16 there,
 // two by an instruction, with no pass through shared memory between.  Its pipe is
-// under a quarter busy.  With MXFP4 the bound is instructions: of about 300 a step
+// under a quarter busy.  With MXFP4 the bound is instructions: of about 280 a step
 // (32 rows x 128 codes) and warp, 64 expand codes, 64 to 100 apply the blocks' scales.
 //
 // Measured (GB300, Hy3 shape, time of a call and share of the measured copy bandwidth
-// that the active weights come in at): bf16 T = 1 66 us (0.76), T = 8 341 us (0.95), T =
-// 32 841 us (0.92); MXFP4 layer T = 1 39 us (0.38), T = 8 125 us (0.69); MXFP4 expert
-// FFN T = 8 114 us (0.73).
+// that the active weights come in at): bf16 T = 1 63 us (0.80), T = 8 314 us (0.99), T =
+// 32 822 us (0.93); MXFP4 layer T = 1 39 us (0.36), T = 8 125 us (0.68); MXFP4 expert
+// FFN T = 8 117 us (0.70).
 //
 // Work.  One CTA of 16 warps per SM, all resident (cooperative launch).  Units of 32
 // rows go to teams of warps that split K (Plan below); the partial products are added
@@ -225,8 +225,9 @@ __device__ Plan make_plan(const FewTables &tb, int rows_r, int rows_s, int steps
   const int a = lane / kChoices, b = lane % kChoices, steps = max(steps_r, tb.nsh ? steps_s : 0);
   unsigned cost = 0x7fffffffu;
   // bf16, bound by the memory: at least as many slices as leave a warp three steps, up to
-  // eight -- fewer and longer ones spread the reads (8 and 4 slices at Hy3 T = 32: 841 and
-  // 856 us; two at T = 8: 385 against 353).  MXFP4, bound by instructions, gains from few.
+  // eight -- fewer and longer ones spread the reads (Hy3 T = 8: 348 us with four down
+  // slices, 343 with eight; 385 against 353 with two, when steps were half as wide).
+  // MXFP4, bound by instructions, gains from few.
   const bool near = WT || a >= 3 || steps >> (a + 1) < 3;
   if (a < kChoices && b >= a && near) {
     auto round = [&](int sh) { return ((steps + (1 << sh) - 1) >> sh) * kStepCycles + kUnitCycles; };

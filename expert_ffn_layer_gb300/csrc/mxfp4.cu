@@ -7,7 +7,8 @@
 // are exact but for that one rounding: a scale is a power of two.
 //
 // Both kernels stream: 2 bytes read and 17/32 written a value, or the reverse, and
-// nothing is read twice.
+// nothing is read twice, so the memory bounds them.  Both ways over 403 M values: 345
+// us, 5.9 TB/s; over 6.3 M: 6.7 us in a graph (a call of each from Python takes 11.5).
 #include "internal.h"
 #include "mxfp4.cuh"
 #include "ptx.cuh"
