@@ -120,6 +120,14 @@ def test_few_decode_widths():
     check_layer(w, inp, host_f64(few(dl)), 2.0 ** -16, "hy3 widths")
 
 
+@pytest.mark.parametrize("H,I,Is", [(16384, 64, 128), (64, 16384, 64), (4096, 64, 4096)])
+def test_few_extreme_widths(H, I, Is):
+    """The widest rows beside the narrowest, and a shared expert far wider than the routed ones."""
+    w = W.Workload("few_ext", 3, H, 4, 2, I, Is, "softmax", 1.0, 1e-8, True, "none", 0.0, 31)
+    inp = W.layer_inputs(w)
+    check_layer(w, inp, host_f64(few(DeviceLayer(w, inp))), 2.0 ** -16, f"H={H} I={I} Is={Is}")
+
+
 @pytest.mark.parametrize("T", [8, 13, 32])
 def test_few_all_tokens_on_the_same_experts(T):
     """A bias that sends every token to the same experts: T tokens in each, the others idle."""

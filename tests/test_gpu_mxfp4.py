@@ -217,6 +217,55 @@ def test_layer_mxfp4_many(w, T):
     check_layer(w, dequantised(inp), got, BF16_HALF, f"{w.name} T={T}", y_eps=BF16_HALF)
 
 
+@pytest.mark.parametrize("T,E,k", [(256, 200, 8), (256, 22, 1), (128, 171, 16), (129, 171, 16)])
+def test_expert_ffn_mxfp4_one_kernel_limits(T, E, k):
+    """The largest batches of the one-kernel form (256 tokens, 2048 slots, 12 slots an expert), and one past it."""
+    w = W.Workload("mx_lim", T, 128, E, k, 128, 128, "softmax", 1.0, 1e-8, True, "none", 0.0, 17)
+    rng = np.random.default_rng(T + E)
+    topk = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    ffn_case(w, W.layer_inputs(w), topk)
+
+
+@pytest.mark.parametrize("H,I,Is", [(16384, 128, 128), (128, 16384, 128), (2048, 128, 4096)])
+def test_expert_ffn_mxfp4_extreme_widths(H, I, Is):
+    w = W.Workload("mx_ext", 3, H, 4, 2, I, Is, "softmax", 1.0, 1e-8, True, "none", 0.0, 31)
+    ffn_case(w, W.layer_inputs(w), np.array([[0, 3], [3, 1], [1, 0]], dtype=np.int32))
+
+
+@pytest.mark.parametrize("T", [4, 64])
+def test_mxfp4_scale_bytes_at_the_ends(T):
+    """A scale byte of 255 makes the outputs that read its block non-finite and no others; 0 counts as
+    zero.  T = 4 runs the one-kernel form, T = 64 (16 slots an expert) the converting kernel."""
+    w = TINY.with_(T=T)
+    inp = W.layer_inputs(w)
+    dl = DeviceLayer(w, inp)
+    ex = experts_of(dl)
+    topk = np.tile(np.arange(4, dtype=np.int32), (T, 1))
+    _, offsets = oracle.histogram_offsets(topk, w.E)
+    perm, _ = oracle.permutation(topk, w.E)
+    y = torch.empty((T * 4, w.H), dtype=torch.bfloat16, device="cuda")
+    z = torch.empty((T, w.H), dtype=torch.bfloat16, device="cuda")
+
+    def run():
+        moe.moe_expert_ffn_mxfp4(dl.d, dl.hidden, i32_dev(perm), i32_dev(offsets), ex, y, z, dl.ws)
+        return y.clone(), z.clone()
+
+    clean, clean_z = run()
+    codes, scales = ex.t["down"]
+    kept = scales.clone()
+    scales[2, 77, 1] = 255
+    scales[1, 50, :] = 0
+    got, got_z = run()
+    rows2 = slice(int(offsets[2]), int(offsets[3]))
+    rows1 = slice(int(offsets[1]), int(offsets[2]))
+    assert not torch.isfinite(got[rows2, 77]).any()
+    assert (got[rows1, 50] == 0).all()
+    got[rows2, 77] = clean[rows2, 77]
+    got[rows1, 50] = clean[rows1, 50]
+    assert torch.equal(got, clean) and torch.equal(got_z, clean_z)
+    scales.copy_(kept)
+
+
 def test_expert_ffn_mxfp4_repeated_expert():
     """A routing that names the same expert twice for a token, and one expert for all."""
     w = ODD.with_(T=9)
