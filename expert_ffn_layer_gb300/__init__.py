@@ -161,7 +161,7 @@ def _stream(stream):
 
 
 def _call(fn: str, *args):
-    rc = getattr(load(), fn)(*args)
+    rc = getattr(_lib or load(), fn)(*args)
     if rc != MOE_OK:
         raise MoeError(fn, rc)
 
@@ -407,24 +407,26 @@ def moe_layer_forward_w8a8(d: MoeDims, hidden, router_w, expert_bias, w: Fp8Expe
           ctypes.byref(w.struct), _ptr(out), _ptr(ws), ws.numel(), _stream(stream))
 
 
+def _mxfp4_rows(values, codes, scales, name):
+    """Rows and columns of a matrix of bf16 values, its packed codes and scale bytes checked against it."""
+    shape = values.shape
+    C, lead = shape[-1], shape[:-1]
+    _check(values, torch.bfloat16, shape, name)
+    _check(codes, torch.uint8, (*lead, C // 2), "codes")
+    _check(scales, torch.uint8, (*lead, C // 32), "scales")
+    return values.numel() // C if C else 0, C
+
+
 def moe_quantize_mxfp4_rows(src, codes, scales, stream=None) -> None:
     """Packed codes [.., C / 2] uint8 and scale bytes [.., C / 32] uint8 of a bf16
     matrix [.., C] (any leading dims are rows; C a multiple of 128)."""
-    C = src.shape[-1]
-    _check(src, torch.bfloat16, src.shape, "src")
-    _check(codes, torch.uint8, (*src.shape[:-1], C // 2), "codes")
-    _check(scales, torch.uint8, (*src.shape[:-1], C // 32), "scales")
-    _call("moe_quantize_mxfp4_rows", _ptr(src), src.numel() // C if C else 0, C, _ptr(codes), _ptr(scales),
+    _call("moe_quantize_mxfp4_rows", _ptr(src), *_mxfp4_rows(src, codes, scales, "src"), _ptr(codes), _ptr(scales),
           _stream(stream))
 
 
 def moe_dequantize_mxfp4_rows(codes, scales, dst, stream=None) -> None:
     """The bf16 values [.., C] that packed codes and scale bytes stand for."""
-    C = dst.shape[-1]
-    _check(dst, torch.bfloat16, dst.shape, "dst")
-    _check(codes, torch.uint8, (*dst.shape[:-1], C // 2), "codes")
-    _check(scales, torch.uint8, (*dst.shape[:-1], C // 32), "scales")
-    _call("moe_dequantize_mxfp4_rows", _ptr(codes), _ptr(scales), dst.numel() // C if C else 0, C, _ptr(dst),
+    _call("moe_dequantize_mxfp4_rows", _ptr(codes), _ptr(scales), *_mxfp4_rows(dst, codes, scales, "dst"), _ptr(dst),
           _stream(stream))
 
 
