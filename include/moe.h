@@ -367,12 +367,13 @@ moe_status moe_layer_forward_mxfp4(const moe_dims *d, const moe_bf16 *hidden, co
 /* The whole layer (a1-a9) for few tokens, T <= 32 (else MOE_ERR_UNSUPPORTED), in
  * one kernel: arguments as for moe_layer_forward, whose chain of kernels it
  * replaces where their launches and hand-overs cost more than the work between
- * them (at Hy3's widths up to about six tokens; past eight the chain is faster).  Its logits are fp32 sums of fp32 products of the bf16 hidden state and
- * the fp32 router weight; activations and expert outputs stay fp32 (the down
- * product takes the activation as two bf16 values, 16 bits of it) and `out` is
- * rounded once, so its results differ from moe_layer_forward's in the last bits.
- * Results do not depend on timing, but the order of the sums over K depends on how
- * many experts a batch reaches.  A cooperative launch, as above. */
+ * them (at Hy3's widths up to about six tokens; past eight the chain is faster).
+ * Its logits are fp32 sums of fp32 products of the bf16 hidden state and the fp32
+ * router weight; activations and expert outputs stay fp32 (the down product takes
+ * the activation as two bf16 values, 16 bits of it) and `out` is rounded once, so
+ * its results differ from moe_layer_forward's in the last bits.  Results do not
+ * depend on timing, but the order of the sums over K depends on how many experts a
+ * batch reaches.  A cooperative launch, as above. */
 moe_status moe_layer_forward_few(const moe_dims *d, const moe_bf16 *hidden, const float *router_w,
                                  const float *expert_bias, const moe_bf16 *w_gate, const moe_bf16 *w_up,
                                  const moe_bf16 *w_down, const moe_bf16 *ws_gate, const moe_bf16 *ws_up,
