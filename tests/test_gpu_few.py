@@ -258,3 +258,21 @@ def test_few_selection_matches_the_router():
                                renorm_eps=1e-8)
     check_selection(idx.cpu().numpy(), ref, 1)
     check_layer(w, inp, host_f64(few(dl)), 2.0 ** -16)
+
+
+def test_few_without_a_bias_equals_a_zero_one():
+    w = MID.with_(T=5)
+    dl = DeviceLayer(w, W.layer_inputs(w))
+    dl.bias.zero_()
+    ref = few(dl).clone()
+    dl.bias = None
+    assert torch.equal(few(dl), ref)
+
+
+def test_few_in_place():
+    """The output over the hidden state: every row is read before any is written."""
+    w = MID.with_(T=7)
+    dl = DeviceLayer(w, W.layer_inputs(w))
+    ref = few(dl).clone()
+    few(dl, out=dl.hidden)
+    assert torch.equal(dl.hidden, ref)
