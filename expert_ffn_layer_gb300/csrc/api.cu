@@ -325,7 +325,7 @@ moe_status do_route(const moe_dims &d, const moe_bf16 *hidden, const float *rout
 }
 
 moe_status do_permute(const moe_dims &d, const int32_t *topk_idx, int32_t *counts, int32_t *offsets, int32_t *perm,
-                      int32_t *inv, void *ws, cudaStream_t stream, bool pdl) {
+                      int32_t *inv, void *ws, cudaStream_t stream, bool pdl, bool wait_first = false) {
   const WsLayout L = ws_layout(d);
   PermuteParams p;
   p.topk_idx = topk_idx;
@@ -338,6 +338,7 @@ moe_status do_permute(const moe_dims &d, const int32_t *topk_idx, int32_t *count
   p.inv = inv;
   p.S = d.T * d.top_k;
   p.E = d.E;
+  p.wait_first = wait_first;
   return cuda_status(launch_permute(p, stream, pdl));
 }
 
@@ -639,7 +640,7 @@ moe_status do_fused_moe(const moe_dims &d, const moe_bf16 *hidden, const int32_t
   int32_t *perm = at<int32_t>(ws, L.perm), *inv = at<int32_t>(ws, L.inv);
   int32_t *offs = at<int32_t>(ws, L.offsets);
   moe_bf16 *y = at<moe_bf16>(ws, L.y_sorted), *z = at<moe_bf16>(ws, L.y_shared);
-  moe_status st = do_permute(d, topk_idx, at<int32_t>(ws, L.counts), offs, perm, inv, ws, s, true);
+  moe_status st = do_permute(d, topk_idx, at<int32_t>(ws, L.counts), offs, perm, inv, ws, s, true, true);
   if (st != MOE_OK) return st;
   const size_t up = (size_t)d.I * d.H, sup = d.has_shared ? (size_t)d.I_shared * d.H : 0;
   st = do_expert_phases(d, 3, hidden, perm, offs, w_gate_up, w_gate_up + up, w_down, ws_gate_up,

@@ -681,7 +681,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
   // Routing data (perm, offsets) comes from the previous kernel.  With p.early
   // the early block's tiles (the shared expert's first row blocks) proceed
   // before it is visible, and each role waits only when it first meets a tile
-  // that needs it; otherwise every thread waits here.
+  // that needs it; otherwise every thread waits here.  (What the early tiles use --
+  // hidden, the shared weights, the header's counters -- was complete before the
+  // chain's second kernel could launch: its first one, the router's split or the
+  // permutation with wait_first, waits before it triggers.)
   if (!p.early) pdl_wait();
   const Sched q = make_sched<BN>(p);
   if (p.early && q.Rs > 0 && warp == kWWarp && lane == 0) {

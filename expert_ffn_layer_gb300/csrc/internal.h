@@ -45,6 +45,12 @@ struct PermuteParams {
   int32_t *part;            // [ceil(S / kPartSlots)][E] workspace table of the many-CTA path
   unsigned *done;           // workspace header word counting finished parts (left zero)
   int S, E;
+  // 1: the first kernel of a chain whose expert kernel starts early.  It then waits
+  // for the work before the chain before it lets the next kernel launch: the early
+  // tiles read hidden and the shared expert's weights and claim from the workspace
+  // header without a wait of their own, and each kernel's wait reaches only the one
+  // before it.
+  int wait_first;
 };
 // Batches above kPermuteOneCtaMax slots are permuted by ceil(S / kPartSlots)
 // CTAs (count + scatter kernels); smaller ones by one CTA.

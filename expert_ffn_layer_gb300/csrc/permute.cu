@@ -44,6 +44,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) permute_kernel(const PermutePar
   const int S = p.S, E = p.E;
   for (int i = threadIdx.x; i < kWarps * kMaxE; i += kThreads) (&base[0][0])[i] = 0;
 
+  if (p.wait_first) pdl_wait();
   pdl_launch_dependents();  // dependents wait for this kernel's completion themselves
   pdl_wait();               // topk_idx comes from the router
   __syncthreads();
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(kPartThreads) permute_count_kernel(const Permu
   const int g = blockIdx.x, G = gridDim.x, E = p.E;
   for (int e = threadIdx.x; e < kMaxE; e += kPartThreads) cnt[e] = 0;
 
+  if (p.wait_first) pdl_wait();
   pdl_launch_dependents();  // dependents wait for this kernel's completion themselves
   pdl_wait();               // topk_idx comes from the router
   __syncthreads();
