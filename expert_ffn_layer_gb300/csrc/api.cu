@@ -235,35 +235,54 @@ WsLayout ws_layout(const moe_dims &d) {
 
 // The one-kernel forms' pieces: for the whole layer in the place of the layout above
 // (no call uses both), for the expert FFN past 32 tokens, which is a stage of the
-// chain, behind it.
+// chain, in the place of its activations and of what follows them (the router's and
+// W8A8's pieces: unused by then, or at all).
 struct FewWs {
   size_t logits, x16, x_unscale, act, act16, act_exp, y, total;
 };
-FewWs few_ws(const moe_dims &d, size_t chain_total) {
+FewWs few_ws(const moe_dims &d) {
   FewWs L;
-  size_t off = d.T <= kFewMaxT ? (size_t)kWsHeaderBytes : chain_total;
+  const WsLayout chain = ws_layout(d);
+  const bool layer = d.T <= kFewMaxT;
+  size_t off = layer ? (size_t)kWsHeaderBytes : chain.w_hi;
   auto take = [&](size_t bytes) {
     const size_t o = off;
     off = align256(off + bytes);
     return o;
   };
   const size_t T = (size_t)d.T, S = T * d.top_k, Is = d.has_shared ? (size_t)d.I_shared : 0;
-  const bool layer = d.T <= kFewMaxT;
   L.logits = take(layer ? T * (size_t)d.E * 4 : 0);
   L.x16 = take(T * (size_t)d.H * 2);
   L.x_unscale = take(T * 4);
   const size_t n_act = S * (size_t)d.I + T * Is;
   L.act = take(layer ? n_act * 4 : 0);
-  L.act16 = take(n_act * 2);
+  L.act16 = layer ? take(n_act * 2) : chain.a_act;  // a_act and a_shared together hold as much
   L.act_exp = take(n_act / 32);
   L.y = take(layer ? (S + T) * (size_t)d.H * 4 : 0);
-  L.total = off;
+  L.total = layer ? off : std::max(off, chain.total);
   return L;
 }
 
+// What the chain's entries need, and what a call with MXFP4 weights does.
+size_t chain_bytes(const moe_dims &d) { return ws_layout(d).total; }
+size_t mxfp4_bytes(const moe_dims &d) { return few_ffn(d) ? few_ws(d).total : chain_bytes(d); }
+
+// What the neediest entry needs for d or any smaller batch: a program makes one
+// workspace for its largest batch.  The need grows with T but for the sizes at which a
+// one-kernel form ends or the router's split halves, whose needs are compared.
 size_t ws_total(const moe_dims &d) {
-  const size_t chain = ws_layout(d).total;
-  return few_ffn(d) ? std::max(chain, few_ws(d, chain).total) : chain;
+  size_t most = 0;
+  auto at = [&](long long T) {
+    if (T > d.T) return;
+    moe_dims s = d;
+    s.T = (int)T;
+    most = std::max(most, std::max(chain_bytes(s), mxfp4_bytes(s)));
+  };
+  at(d.T);
+  at(kFewMaxT);
+  at(std::min(kFewFfnMaxT, std::min(kFewFfnMaxS / d.top_k, 12 * d.E / d.top_k)));
+  for (int ks = 32; ks >= 1; ks >>= 1) at(128LL * (256 / ks));
+  return most;
 }
 
 int num_sms() {
@@ -284,9 +303,9 @@ inline T *at(void *ws, size_t off) {
   return reinterpret_cast<T *>(static_cast<uint8_t *>(ws) + off);
 }
 
-moe_status check_ws(const moe_dims *d, void *ws, size_t ws_bytes) {
+moe_status check_ws(void *ws, size_t ws_bytes, size_t need) {
   if (ws == nullptr || !aligned256(ws)) return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < ws_total(*d)) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
   return MOE_OK;
 }
 
@@ -565,7 +584,7 @@ bool mxfp4_ok(const moe_dims &d, const moe_mxfp4_experts *q) {
 
 // What the one-kernel layer needs whatever its weights and routing.
 FewParams few_params(const moe_dims &d, const moe_bf16 *hidden, void *ws) {
-  const FewWs L = few_ws(d, ws_layout(d).total);
+  const FewWs L = few_ws(d);
   FewParams p;
   std::memset(&p, 0, sizeof(p));
   p.hidden = reinterpret_cast<const __nv_bfloat16 *>(hidden);
@@ -729,7 +748,7 @@ MOE_API moe_status moe_route(const moe_dims *d, const moe_bf16 *hidden, const fl
   if (!ptr_ok(hidden) || !ptr_ok(router_w) || !ptr_ok(topk_idx) || !ptr_ok(topk_w)) return MOE_ERR_INVALID_ARG;
   if ((expert_bias != nullptr && !aligned16(expert_bias)) || (logits_out != nullptr && !aligned16(logits_out)))
     return MOE_ERR_INVALID_ARG;
-  if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, chain_bytes(*d))) != MOE_OK) return st;
   return do_route(*d, hidden, router_w, expert_bias, logits_out, topk_idx, topk_w, ws, (cudaStream_t)stream, true);
 }
 
@@ -739,7 +758,7 @@ MOE_API moe_status moe_permute(const moe_dims *d, const int32_t *topk_idx, int32
   if (st != MOE_OK) return st;
   if (!ptr_ok(counts) || !ptr_ok(offsets)) return MOE_ERR_INVALID_ARG;
   if (d->T > 0 && (!ptr_ok(topk_idx) || !ptr_ok(perm) || !ptr_ok(inv_perm))) return MOE_ERR_INVALID_ARG;
-  if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, chain_bytes(*d))) != MOE_OK) return st;
   if (d->T == 0) {
     // empty batch: counts and offsets are all zero
     cudaStream_t s = (cudaStream_t)stream;
@@ -763,7 +782,7 @@ MOE_API moe_status moe_expert_ffn(const moe_dims *d, const moe_bf16 *hidden, con
     return MOE_ERR_INVALID_ARG;
   if (d->has_shared && (!ptr_ok(ws_gate) || !ptr_ok(ws_up) || !ptr_ok(ws_down) || !ptr_ok(y_shared)))
     return MOE_ERR_INVALID_ARG;
-  if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, chain_bytes(*d))) != MOE_OK) return st;
   return do_expert_ffn(*d, hidden, perm, offsets, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, y_sorted, y_shared,
                        ws, (cudaStream_t)stream, true);
 }
@@ -778,7 +797,7 @@ MOE_API moe_status moe_expert_gate_up(const moe_dims *d, const moe_bf16 *hidden,
   if (!ptr_ok(hidden) || !ptr_ok(perm) || !ptr_ok(offsets) || !ptr_ok(w_gate) || !ptr_ok(w_up))
     return MOE_ERR_INVALID_ARG;
   if (d->has_shared && (!ptr_ok(ws_gate) || !ptr_ok(ws_up))) return MOE_ERR_INVALID_ARG;
-  if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, chain_bytes(*d))) != MOE_OK) return st;
   return do_gate_up(*d, hidden, perm, offsets, w_gate, w_up, ws_gate, ws_up, ws, (cudaStream_t)stream, true);
 }
 
@@ -790,7 +809,7 @@ MOE_API moe_status moe_expert_down(const moe_dims *d, const int32_t *offsets, co
   if (d->T == 0) return MOE_OK;
   if (!ptr_ok(offsets) || !ptr_ok(w_down) || !ptr_ok(y_sorted)) return MOE_ERR_INVALID_ARG;
   if (d->has_shared && (!ptr_ok(ws_down) || !ptr_ok(y_shared))) return MOE_ERR_INVALID_ARG;
-  if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, chain_bytes(*d))) != MOE_OK) return st;
   return do_down(*d, offsets, w_down, ws_down, y_sorted, y_shared, ws, (cudaStream_t)stream, true);
 }
 
@@ -815,7 +834,7 @@ MOE_API moe_status moe_fused_moe(const moe_dims *d, const moe_bf16 *hidden, cons
       !ptr_ok(out))
     return MOE_ERR_INVALID_ARG;
   if (d->has_shared && (!ptr_ok(ws_gate_up) || !ptr_ok(ws_down))) return MOE_ERR_INVALID_ARG;
-  if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, chain_bytes(*d))) != MOE_OK) return st;
   return do_fused_moe(*d, hidden, topk_idx, topk_w, w_gate_up, w_down, ws_gate_up, ws_down, out, ws,
                       (cudaStream_t)stream);
 }
@@ -838,7 +857,7 @@ MOE_API moe_status moe_expert_ffn_fp8(const moe_dims *d, const moe_bf16 *hidden,
   if (!ptr_ok(hidden) || !ptr_ok(perm) || !ptr_ok(offsets) || !ptr_ok(y_sorted) || !fp8_ok(*d, w))
     return MOE_ERR_INVALID_ARG;
   if (d->has_shared && !ptr_ok(y_shared)) return MOE_ERR_INVALID_ARG;
-  if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, chain_bytes(*d))) != MOE_OK) return st;
   return do_expert_phases(*d, 3, hidden, perm, offsets, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
                           y_sorted, y_shared, scratch_in(*d, ws), (cudaStream_t)stream, true, 0, w);
 }
@@ -851,7 +870,7 @@ MOE_API moe_status moe_layer_forward_fp8(const moe_dims *d, const moe_bf16 *hidd
   if (d->T == 0) return MOE_OK;
   if (!ptr_ok(hidden) || !ptr_ok(router_w) || !ptr_ok(out) || !fp8_ok(*d, w)) return MOE_ERR_INVALID_ARG;
   if (expert_bias != nullptr && !aligned16(expert_bias)) return MOE_ERR_INVALID_ARG;
-  if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, chain_bytes(*d))) != MOE_OK) return st;
   const WsLayout L = ws_layout(*d);
   cudaStream_t s = (cudaStream_t)stream;
   int32_t *idx = at<int32_t>(ws, L.topk_idx);
@@ -882,7 +901,7 @@ MOE_API moe_status moe_expert_ffn_w8a8(const moe_dims *d, const moe_bf16 *hidden
   if (!ptr_ok(hidden) || !ptr_ok(perm) || !ptr_ok(offsets) || !ptr_ok(y_sorted) || !fp8_ok(*d, w))
     return MOE_ERR_INVALID_ARG;
   if (d->has_shared && !ptr_ok(y_shared)) return MOE_ERR_INVALID_ARG;
-  if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, chain_bytes(*d))) != MOE_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
   const ExpertScratch sc = scratch_in(*d, ws);
   if (launch_quantize_rows(reinterpret_cast<const __nv_bfloat16 *>(hidden), sc.hq, sc.hs, d->T, d->H, s) !=
@@ -901,7 +920,7 @@ MOE_API moe_status moe_layer_forward_w8a8(const moe_dims *d, const moe_bf16 *hid
   if (d->T == 0) return MOE_OK;
   if (!ptr_ok(hidden) || !ptr_ok(router_w) || !ptr_ok(out) || !fp8_ok(*d, w)) return MOE_ERR_INVALID_ARG;
   if (expert_bias != nullptr && !aligned16(expert_bias)) return MOE_ERR_INVALID_ARG;
-  if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, chain_bytes(*d))) != MOE_OK) return st;
   const WsLayout L = ws_layout(*d);
   cudaStream_t s = (cudaStream_t)stream;
   const ExpertScratch sc = scratch_in(*d, ws);
@@ -956,7 +975,7 @@ MOE_API moe_status moe_expert_ffn_mxfp4(const moe_dims *d, const moe_bf16 *hidde
   if (!ptr_ok(hidden) || !ptr_ok(perm) || !ptr_ok(offsets) || !ptr_ok(y_sorted) || !mxfp4_ok(*d, w))
     return MOE_ERR_INVALID_ARG;
   if (d->has_shared && !ptr_ok(y_shared)) return MOE_ERR_INVALID_ARG;
-  if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, mxfp4_bytes(*d))) != MOE_OK) return st;
   return do_expert_ffn_mxfp4(*d, hidden, perm, offsets, *w, y_sorted, y_shared, ws, (cudaStream_t)stream, false);
 }
 
@@ -969,7 +988,7 @@ MOE_API moe_status moe_layer_forward_mxfp4(const moe_dims *d, const moe_bf16 *hi
   if (d->T == 0) return MOE_OK;
   if (!ptr_ok(hidden) || !ptr_ok(router_w) || !ptr_ok(out) || !mxfp4_ok(*d, w)) return MOE_ERR_INVALID_ARG;
   if (expert_bias != nullptr && !aligned16(expert_bias)) return MOE_ERR_INVALID_ARG;
-  if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, mxfp4_bytes(*d))) != MOE_OK) return st;
   if (d->T > kFewMaxT) {
     const WsLayout L = ws_layout(*d);
     cudaStream_t s = (cudaStream_t)stream;
@@ -1002,7 +1021,7 @@ MOE_API moe_status moe_layer_forward_few(const moe_dims *d, const moe_bf16 *hidd
     return MOE_ERR_INVALID_ARG;
   if (expert_bias != nullptr && !aligned16(expert_bias)) return MOE_ERR_INVALID_ARG;
   if (d->has_shared && (!ptr_ok(ws_gate) || !ptr_ok(ws_up) || !ptr_ok(ws_down))) return MOE_ERR_INVALID_ARG;
-  if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, few_ws(*d).total)) != MOE_OK) return st;
   FewParams p = few_params(*d, hidden, ws);
   p.gate = reinterpret_cast<const uint8_t *>(w_gate);
   p.up = reinterpret_cast<const uint8_t *>(w_up);
@@ -1026,7 +1045,7 @@ MOE_API moe_status moe_layer_forward(const moe_dims *d, const moe_bf16 *hidden, 
     return MOE_ERR_INVALID_ARG;
   if (expert_bias != nullptr && !aligned16(expert_bias)) return MOE_ERR_INVALID_ARG;
   if (d->has_shared && (!ptr_ok(ws_gate) || !ptr_ok(ws_up) || !ptr_ok(ws_down))) return MOE_ERR_INVALID_ARG;
-  if ((st = check_ws(d, ws, ws_bytes)) != MOE_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, chain_bytes(*d))) != MOE_OK) return st;
   const WsLayout L = ws_layout(*d);
   cudaStream_t s = (cudaStream_t)stream;
   int32_t *idx = at<int32_t>(ws, L.topk_idx);

@@ -29,7 +29,7 @@
  *   - Argument errors are returned before anything is launched:
  *       MOE_ERR_INVALID_ARG  null / misaligned pointer, negative size, bad mode
  *       MOE_ERR_UNSUPPORTED  a shape outside the supported set (below)
- *       MOE_ERR_WORKSPACE    ws_bytes < moe_workspace_bytes(d)
+ *       MOE_ERR_WORKSPACE    ws_bytes too few for the call (moe_workspace_bytes(d) are enough)
  *       MOE_ERR_CUDA         a launch or driver call failed
  *     Anomalies seen on the device (an index outside its range, a bounded wait
  *     that ran out) are recorded as bits in an error word at the start of the
@@ -100,8 +100,8 @@ const char *moe_status_string(moe_status s);
 /* Validate dims against the supported set; MOE_OK, INVALID_ARG or UNSUPPORTED. */
 moe_status moe_check_dims(const moe_dims *d);
 
-/* Bytes of workspace every entry point below needs for these dims (the fused
- * layer's need, which covers the others); 0 when the dims are invalid. */
+/* Bytes of workspace that are enough for every entry point below with these dims,
+ * or with a smaller T and the rest the same; 0 when the dims are invalid. */
 size_t moe_workspace_bytes(const moe_dims *d);
 
 /* Zero the workspace header (error word and tile-scheduler counters, the first
