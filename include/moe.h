@@ -356,7 +356,9 @@ moe_status moe_dequantize_mxfp4_rows(const uint8_t *codes, const uint8_t *scales
  *   Larger layers run the chain of kernels of moe_layer_forward, and the expert kernel
  *   of larger batches expands the weights to bf16 in shared memory (exact) and keeps the activations
  *   between the products in bf16, as with bf16 weights.
- *   In the products of either form a scale byte of 0 (2^-127) counts as zero. */
+ *   In the products of either form a scale byte of 0 (2^-127) counts as zero.  The
+ *   one-kernel form sums at the tokens' power of two, up to 2^15 for a row's largest
+ *   magnitude: scale bytes past 223 (2^96) may overflow there where the value would not. */
 moe_status moe_expert_ffn_mxfp4(const moe_dims *d, const moe_bf16 *hidden, const int32_t *perm,
                                 const int32_t *offsets, const moe_mxfp4_experts *w, moe_bf16 *y_sorted,
                                 moe_bf16 *y_shared, void *ws, size_t ws_bytes, void *stream);

@@ -129,3 +129,27 @@ def test_fused_moe_behind_an_expert_ffn_on_the_same_workspace(T):
     assert torch.equal(y, ref_y) and torch.equal(z, ref_z)
     assert all(torch.equal(o, ref) for o in outs)
     assert int(a.ws[:4096].sum()) == 0
+
+
+def test_fused_moe_behind_the_dequantiser_in_a_graph():
+    a = Layer(8, 1024, 16, 4, 128, 4096)
+    sets = [_codes(_normal(a.gen, a.sgu.shape, 0.02)) for _ in range(2)]
+    ref = []
+    for s in sets:
+        moe.moe_dequantize_mxfp4_rows(*s, a.sgu)
+        torch.cuda.synchronize()
+        ref.append(a.fused(a.hidden, a.new_out()))
+        torch.cuda.synchronize()
+    outs = [a.new_out() for _ in range(16)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for i, o in enumerate(outs):
+            moe.moe_dequantize_mxfp4_rows(*sets[i & 1], a.sgu)
+            a.fused(a.hidden, o)
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for i, o in enumerate(outs):
+            assert torch.equal(o, ref[i & 1]), f"call {i}"
