@@ -15,7 +15,8 @@ Function names follow the C ABI:
     moe_layer_forward_mxfp4 (MXFP4 expert weights; see Mxfp4Experts /
     quantize_mxfp4_experts / pack_mxfp4), moe_layer_forward_few (at most 32
     tokens, the whole layer in one kernel),
-    moe_workspace_bytes, moe_ws_init, moe_ws_read_error, moe_check_dims
+    moe_workspace_bytes (enough for the batch and any smaller one), moe_ws_init,
+    moe_ws_read_error, moe_check_dims
 
 Tensors are torch tensors on the current CUDA device: bf16 activations and
 weights, fp32 router weight / bias / combine weights, int32 indices, a uint8
@@ -487,7 +488,8 @@ def quantize_mxfp4_experts(w_gate, w_up, w_down, ws_gate=None, ws_up=None, ws_do
 
 def moe_expert_ffn_mxfp4(d: MoeDims, hidden, perm, offsets, w: Mxfp4Experts, y_sorted, y_shared, ws,
                          stream=None) -> None:
-    """The expert FFN with MXFP4 weights; one kernel for at most 32 tokens."""
+    """The expert FFN with MXFP4 weights; one kernel for at most 32 tokens and, up to 256
+    tokens and 2048 slots, for at most 12 slots an expert on average."""
     S = d.T * d.top_k
     _check(hidden, torch.bfloat16, (d.T, d.H), "hidden")
     _check(perm, torch.int32, (S,), "perm")

@@ -187,8 +187,10 @@ int router_ksplit(const moe_dims &d, int nsm) {
 // Batches whose MXFP4 expert FFN runs as the one-kernel form.  Past 32 tokens it
 // pays while experts average few tokens -- each 8 of an expert's tokens are a pass
 // over its weights, while the converting kernel takes as long for 1 token as for 48
-// (Hy3 shape, this form and that: T = 33 (1.4 tokens an expert) 273 and 687 us, T = 128
-// (5.3) 434 and 933, T = 256 (10.7) 691 and 960).
+// (Hy3 shape, one box, this form and that: T = 33 (1.4 tokens an expert) 273 and 687 us,
+// T = 128 (5.3) 434 and 933, T = 256 (10.7) 691 and 960).  All measured points are won
+// by this form and have I_shared = I: 12 is a limit within which it is known to pay, not
+// the crossover, and 256 and 2048 are the sizes of its tables.
 bool few_ffn(const moe_dims &d) {
   const long long S = (long long)d.T * d.top_k;
   return d.T <= kFewMaxT || (d.T <= kFewFfnMaxT && S <= kFewFfnMaxS && S <= 12LL * d.E);

@@ -1246,7 +1246,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
     // A row's four scale bytes of a code slot are one word; the four lanes of a row
     // load the words of four slots together (brought into L2 when the tile was
     // claimed) and hand them round (each lane loading each step's two bytes, a step
-    // ahead: 1482 us at Hy3 T = 4096 against 1264 us; the bf16 weights' kernel 1233 us).
+    // ahead: 17 % slower at Hy3 T = 4096, where this takes 1304 us).
     const int cw = warp - (kEpiWarp0 + EW);
     const int grp = cw >> 2, wg = cw & 3;
     const int box = wg >> 1, c = lane & 3, rlane = (lane >> 3) + (lane & 4);

@@ -16,13 +16,16 @@
 // every choice serves the weight stream.  mma.sync (m16n8k16) is used rather than
 // tcgen05 because its A operand comes from registers: MXFP4 codes become fp16 there,
 // two by an instruction, with no pass through shared memory between.  Its pipe is
-// under a quarter busy.  With MXFP4 the bound is instructions: of about 280 a step
-// (32 rows x 128 codes) and warp, 64 expand codes, 64 to 100 apply the blocks' scales.
+// under a quarter busy.  With MXFP4 no unit is: at T = 8 half the issue slots, 45 % of
+// the ALU pipe, 55 % of the memory.  Four warps a scheduler wait out the latencies of
+// steps (32 rows x 128 codes) of about 280 instructions, of which 64 expand codes and
+// 64 to 100 apply the blocks' scales.
 //
 // Measured (GB300, Hy3 shape, time of a call and share of the measured copy bandwidth
-// that the active weights come in at): bf16 T = 1 63 us (0.80), T = 8 314 us (0.99), T =
-// 32 822 us (0.93); MXFP4 layer T = 1 39 us (0.36), T = 8 125 us (0.68); MXFP4 expert
-// FFN T = 8 117 us (0.70).
+// that the active weights come in at): bf16 T = 1 64 us (0.78), T = 8 336 us (56 active
+// experts, 0.94), T = 32 818 us (0.95); MXFP4 layer T = 1 39 us (0.36), T = 8 124 us
+// (0.68); MXFP4 expert FFN T = 8 114 us (0.71).  Percentages further down compare two
+// versions of this file in turn on one box, also Hy3 shape.
 //
 // Work.  One CTA of 16 warps per SM, all resident (cooperative launch).  Units of 32
 // rows go to teams of warps that split K (Plan below); the partial products are added
@@ -32,7 +35,7 @@
 // Weights travel through a ring of steps per warp by cp.async.  No other warp reads a
 // ring, so it needs no barrier; it keeps filling across units, and before the wait
 // between the two products it already holds the first steps of the second.  (Bringing
-// more of the second's weights into L2 during that wait: no gain, T = 8 343 us.)
+// more of the second's weights into L2 during that wait: no gain at T = 8.)
 //
 // Three grid-wide waits order the phases (logits -> selection, activations -> down,
 // outputs -> combine).  They are bounded like every wait here: a CTA that gives up sets
@@ -57,14 +60,14 @@ template <int WT>
 struct Fmt {  // weights: 0 bf16, 1 MXFP4
   // K values of a step, and its ring slots: both 16-row tiles' 64 bytes a row in one slot
   // (MXFP4), or a slot for each tile's 128 bytes a row (bf16: whole lines, as the memory
-  // likes them: Hy3 T = 8 356 -> 342 us, T = 32 863 -> 849 us)
+  // likes them: 4 % less time than half lines at T = 8, 2 % at T = 32)
   static constexpr int kStep = WT ? 128 : 64;
   static constexpr int kSlots = WT ? 1 : 2;
   static constexpr int kGroups = kStep / 32;    // groups of 32 K values (two matrix instructions each)
   static constexpr int kStage = kStageW + (WT ? 128 : 0);  // with the 32 rows' four scale bytes
   // Steps of a warp's ring.  MXFP4: three, which leaves 32 KB more of L1 to the token
-  // operand (Hy3 T = 8 expert FFN 118 -> 114 us); bf16 is better off with the fourth
-  // (Hy3 T = 1: 73 us, and 76 with three).
+  // operand (expert FFN T = 8 3 % faster than with four); bf16 is better off with the
+  // fourth (T = 1 4 % faster).
   static constexpr int kNst = WT ? 3 : 4;
 };
 
@@ -225,9 +228,9 @@ __device__ Plan make_plan(const FewTables &tb, int rows_r, int rows_s, int steps
   const int a = lane / kChoices, b = lane % kChoices, steps = max(steps_r, tb.nsh ? steps_s : 0);
   unsigned cost = 0x7fffffffu;
   // bf16, bound by the memory: at least as many slices as leave a warp three steps, up to
-  // eight -- fewer and longer ones spread the reads (Hy3 T = 8: 348 us with four down
-  // slices, 343 with eight; 385 against 353 with two, when steps were half as wide).
-  // MXFP4, bound by instructions, gains from few.
+  // eight -- fewer and longer ones spread the reads (T = 8: four down slices 1.5 % slower
+  // than eight; two 9 % slower, when steps were half as wide).
+  // MXFP4, whose steps take longer than their bytes, gains from few.
   const bool near = WT || a >= 3 || steps >> (a + 1) < 3;
   if (a < kChoices && b >= a && near) {
     auto round = [&](int sh) { return ((steps + (1 << sh) - 1) >> sh) * kStepCycles + kUnitCycles; };
@@ -338,7 +341,7 @@ __device__ void run_phase(const FewParams &p, FewTables &tb, uint8_t *ring, floa
   const uint32_t my_ring = smem_u32(ring) + warp * kNst * STAGE;
   // With at most 8 tokens every weight is read once: evict-first, so that the stream
   // leaves the rest in L2 -- the code above all, whose lines every launch would fetch
-  // from memory again (Hy3 T = 1: bf16 70.8 -> 66.8 us, MXFP4 43.3 -> 39.3 us).
+  // from memory again (T = 1: 4 us less with either weights).
   const uint64_t pol = p.T <= 8 ? policy_evict_first() : policy_evict_normal();
 
   // ---- the weight stream: the unit and step to copy next
@@ -776,8 +779,7 @@ __device__ __forceinline__ int ordered(float f) {
 // kernel: each round the largest key by one integer reduction over the lanes, the
 // lower of equal experts by another.  Every CTA runs it once a call, so what it costs
 // is fetching its code: rolled loops over scores and keys in shared memory (2 KB a
-// warp) rather than unrolled ones in registers (Hy3 T = 1 with a cold L2: bf16 72 us against 80,
-// MXFP4 46 against 53).
+// warp) rather than unrolled ones in registers (T = 1 with a cold L2: 7 to 8 us less).
 __device__ __forceinline__ void select_token(const FewParams &p, FewTables &tb, int t, float *sc, int lane) {
   const int E = p.E, k = p.top_k;
   int *key = reinterpret_cast<int *>(sc + 256);

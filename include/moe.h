@@ -369,7 +369,7 @@ moe_status moe_layer_forward_mxfp4(const moe_dims *d, const moe_bf16 *hidden, co
 /* The whole layer (a1-a9) for few tokens, T <= 32 (else MOE_ERR_UNSUPPORTED), in
  * one kernel: arguments as for moe_layer_forward, whose chain of kernels it
  * replaces where their launches and hand-overs cost more than the work between
- * them (at Hy3's widths up to about six tokens; past eight the chain is faster).
+ * them (at Hy3's widths up to about five tokens; past six the chain is faster).
  * Its logits are fp32 sums of fp32 products of the bf16 hidden state and the fp32
  * router weight; activations and expert outputs stay fp32 (the down product takes
  * the activation as two bf16 values, 16 bits of it) and `out` is rounded once, so
