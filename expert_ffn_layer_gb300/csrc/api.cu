@@ -681,7 +681,7 @@ MOE_API const char *moe_status_string(moe_status s) {
     case MOE_OK: return "MOE_OK";
     case MOE_ERR_INVALID_ARG: return "MOE_ERR_INVALID_ARG: null or misaligned pointer, bad size or mode";
     case MOE_ERR_UNSUPPORTED: return "MOE_ERR_UNSUPPORTED: shape outside the supported set";
-    case MOE_ERR_WORKSPACE: return "MOE_ERR_WORKSPACE: workspace smaller than moe_workspace_bytes()";
+    case MOE_ERR_WORKSPACE: return "MOE_ERR_WORKSPACE: workspace smaller than the call needs (moe_workspace_bytes() are enough)";
     case MOE_ERR_CUDA: return "MOE_ERR_CUDA: a CUDA launch or driver call failed";
     case MOE_ERR_DEVICE_TIMEOUT: return "MOE_ERR_DEVICE_TIMEOUT: a bounded wait inside a kernel ran out";
     case MOE_ERR_DEVICE_INDEX: return "MOE_ERR_DEVICE_INDEX: an index seen on the device was out of range";
