@@ -11,6 +11,9 @@ Function names follow the C ABI:
     moe_fused_moe (routing given, stacked [E, 2I, H] gate/up weights),
     moe_quantize_fp8_rows, moe_expert_ffn_fp8, moe_layer_forward_fp8 (FP8 E4M3
     expert weights, one scale per row; see Fp8Experts / quantize_fp8_experts),
+    moe_quantize_int8_rows, moe_dequantize_int8_rows, moe_expert_ffn_int8,
+    moe_layer_forward_int8 (8-bit integer weights and activations; see Int8Experts /
+    quantize_int8_experts),
     moe_quantize_mxfp4_rows, moe_dequantize_mxfp4_rows, moe_expert_ffn_mxfp4,
     moe_layer_forward_mxfp4 (MXFP4 expert weights; see Mxfp4Experts /
     quantize_mxfp4_experts / pack_mxfp4), moe_layer_forward_few (at most 32
@@ -41,7 +44,8 @@ EXPORTS = ("moe_status_string", "moe_check_dims", "moe_workspace_bytes", "moe_ws
            "moe_route", "moe_permute", "moe_expert_ffn", "moe_expert_gate_up", "moe_expert_down", "moe_combine",
            "moe_layer_forward", "moe_fused_moe", "moe_expert_ffn_noalloc", "moe_selftest_wait_timeout",
            "moe_selftest_silu", "moe_quantize_fp8_rows", "moe_expert_ffn_fp8", "moe_layer_forward_fp8",
-           "moe_expert_ffn_w8a8", "moe_layer_forward_w8a8", "moe_quantize_mxfp4_rows", "moe_dequantize_mxfp4_rows",
+           "moe_expert_ffn_w8a8", "moe_layer_forward_w8a8", "moe_quantize_int8_rows", "moe_dequantize_int8_rows",
+           "moe_expert_ffn_int8", "moe_layer_forward_int8", "moe_quantize_mxfp4_rows", "moe_dequantize_mxfp4_rows",
            "moe_expert_ffn_mxfp4", "moe_layer_forward_mxfp4", "moe_layer_forward_few")
 
 
@@ -64,6 +68,10 @@ class MoeFp8Experts(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("gate", "up", "down", "gate_scale", "up_scale", "down_scale",
                                                 "s_gate", "s_up", "s_down", "s_gate_scale", "s_up_scale",
                                                 "s_down_scale")]
+
+
+class MoeInt8Experts(ctypes.Structure):
+    _fields_ = list(MoeFp8Experts._fields_)
 
 
 class MoeMxfp4Experts(ctypes.Structure):
@@ -108,6 +116,10 @@ def load() -> ctypes.CDLL:
         "moe_layer_forward_fp8": (st, [D, P, P, P, ctypes.POINTER(MoeFp8Experts), P, P, C, P]),
         "moe_expert_ffn_w8a8": (st, [D, P, P, P, ctypes.POINTER(MoeFp8Experts), P, P, P, C, P]),
         "moe_layer_forward_w8a8": (st, [D, P, P, P, ctypes.POINTER(MoeFp8Experts), P, P, C, P]),
+        "moe_quantize_int8_rows": (st, [P, ctypes.c_int64, ctypes.c_int, P, P, P]),
+        "moe_dequantize_int8_rows": (st, [P, P, ctypes.c_int64, ctypes.c_int, P, P]),
+        "moe_expert_ffn_int8": (st, [D, P, P, P, ctypes.POINTER(MoeInt8Experts), P, P, P, C, P]),
+        "moe_layer_forward_int8": (st, [D, P, P, P, ctypes.POINTER(MoeInt8Experts), P, P, C, P]),
         "moe_quantize_mxfp4_rows": (st, [P, ctypes.c_int64, ctypes.c_int, P, P, P]),
         "moe_dequantize_mxfp4_rows": (st, [P, P, ctypes.c_int64, ctypes.c_int, P, P]),
         "moe_expert_ffn_mxfp4": (st, [D, P, P, P, ctypes.POINTER(MoeMxfp4Experts), P, P, P, C, P]),
@@ -405,6 +417,100 @@ def moe_layer_forward_w8a8(d: MoeDims, hidden, router_w, expert_bias, w: Fp8Expe
     _check(out, torch.bfloat16, (d.T, d.H), "out")
     _check(w.t["gate"][0], torch.uint8, (d.E, d.I, d.H), "gate codes")
     _call("moe_layer_forward_w8a8", ctypes.byref(d), _ptr(hidden), _ptr(router_w), _ptr(expert_bias),
+          ctypes.byref(w.struct), _ptr(out), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def _int8_rows(values, codes, scales, name):
+    """Rows and columns of a matrix of bf16 values, its codes and row scales checked against it."""
+    shape = values.shape
+    _check(values, torch.bfloat16, shape, name)
+    _check(codes, torch.int8, shape, "codes")
+    _check(scales, torch.float32, shape[:-1], "scales")
+    return values.numel() // shape[-1] if shape[-1] else 0, shape[-1]
+
+
+def moe_quantize_int8_rows(src, codes, scales, stream=None) -> None:
+    """codes [.., C] int8 and scales [..] fp32 of a bf16 matrix [.., C] (any leading
+    dims are rows; C a multiple of 8)."""
+    _call("moe_quantize_int8_rows", _ptr(src), *_int8_rows(src, codes, scales, "src"), _ptr(codes), _ptr(scales),
+          _stream(stream))
+
+
+def moe_dequantize_int8_rows(codes, scales, dst, stream=None) -> None:
+    """The bf16 values [.., C] that codes and scales stand for (code * scale)."""
+    _call("moe_dequantize_int8_rows", _ptr(codes), _ptr(scales), *_int8_rows(dst, codes, scales, "dst"), _ptr(dst),
+          _stream(stream))
+
+
+class Int8Experts:
+    """Device tensors of 8-bit integer expert weights (codes, one fp32 scale per row)
+    and the C struct that points at them."""
+
+    NAMES = ("gate", "up", "down", "s_gate", "s_up", "s_down")
+
+    def __init__(self, **tensors):
+        self.t = tensors  # name -> (codes int8, scales fp32) or None
+        self.fits = None  # the dims these tensors were last found to fit
+        st = MoeInt8Experts()
+        for n in self.NAMES:
+            pair = tensors.get(n)
+            setattr(st, n, _ptr(pair[0]) if pair is not None else None)
+            setattr(st, n + "_scale", _ptr(pair[1]) if pair is not None else None)
+        self.struct = st
+
+    def check(self, d: MoeDims) -> None:
+        dims = (d.E, d.I, d.H, d.I_shared if d.has_shared else 0)
+        if dims == self.fits:
+            return
+        shapes = {"gate": (d.E, d.I, d.H), "up": (d.E, d.I, d.H), "down": (d.E, d.H, d.I)}
+        if d.has_shared:
+            shapes.update(s_gate=(d.I_shared, d.H), s_up=(d.I_shared, d.H), s_down=(d.H, d.I_shared))
+        for n, shape in shapes.items():
+            if self.t.get(n) is None:
+                raise ValueError(f"{n}: missing")
+            _check(self.t[n][0], torch.int8, shape, n + " codes")
+            _check(self.t[n][1], torch.float32, shape[:-1], n + " scales")
+        self.fits = dims
+
+
+def quantize_int8_experts(w_gate, w_up, w_down, ws_gate=None, ws_up=None, ws_down=None, stream=None) -> Int8Experts:
+    """Quantise bf16 expert weights (and the shared expert's, if given) with
+    moe_quantize_int8_rows on the device."""
+    out = {}
+    for n, w in zip(Int8Experts.NAMES, (w_gate, w_up, w_down, ws_gate, ws_up, ws_down)):
+        if w is None:
+            continue
+        codes = torch.empty(w.shape, dtype=torch.int8, device=w.device)
+        scales = torch.empty(w.shape[:-1], dtype=torch.float32, device=w.device)
+        moe_quantize_int8_rows(w, codes, scales, stream)
+        out[n] = (codes, scales)
+    return Int8Experts(**out)
+
+
+def moe_expert_ffn_int8(d: MoeDims, hidden, perm, offsets, w: Int8Experts, y_sorted, y_shared, ws,
+                        stream=None) -> None:
+    """The expert FFN in 8-bit integers: a scale for each weight row, and for each
+    token (hidden) and routed slot (the SiLU*up activation)."""
+    S = d.T * d.top_k
+    _check(hidden, torch.bfloat16, (d.T, d.H), "hidden")
+    _check(perm, torch.int32, (S,), "perm")
+    _check(offsets, torch.int32, (d.E + 1,), "offsets")
+    w.check(d)
+    _check(y_sorted, torch.bfloat16, (S, d.H), "y_sorted")
+    if d.has_shared:
+        _check(y_shared, torch.bfloat16, (d.T, d.H), "y_shared")
+    _call("moe_expert_ffn_int8", ctypes.byref(d), _ptr(hidden), _ptr(perm), _ptr(offsets), ctypes.byref(w.struct),
+          _ptr(y_sorted), _ptr(y_shared), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def moe_layer_forward_int8(d: MoeDims, hidden, router_w, expert_bias, w: Int8Experts, out, ws, stream=None) -> None:
+    """The layer with 8-bit integer experts."""
+    _check(hidden, torch.bfloat16, (d.T, d.H), "hidden")
+    _check(router_w, torch.float32, (d.E, d.H), "router_w")
+    _check(expert_bias, torch.float32, (d.E,), "expert_bias")
+    w.check(d)
+    _check(out, torch.bfloat16, (d.T, d.H), "out")
+    _call("moe_layer_forward_int8", ctypes.byref(d), _ptr(hidden), _ptr(router_w), _ptr(expert_bias),
           ctypes.byref(w.struct), _ptr(out), _ptr(ws), ws.numel(), _stream(stream))
 
 

@@ -265,8 +265,34 @@ FewWs few_ws(const moe_dims &d) {
   return L;
 }
 
-// What the chain's entries need, and what a call with MXFP4 weights does.
+// int8's pieces, in the place of W8A8's (no call uses both): the hidden state's codes
+// as fp16 values and their scales, the activations' row maxima per 32 columns and
+// row scales.
+struct Int8Ws {
+  size_t hx, hs, amax, amax_s, asc, asc_s, total;
+};
+Int8Ws int8_ws(const moe_dims &d) {
+  Int8Ws L;
+  size_t off = ws_layout(d).hq;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align256(off + bytes);
+    return o;
+  };
+  const size_t T = (size_t)d.T, S = T * d.top_k, Is = d.has_shared ? (size_t)d.I_shared : 0;
+  L.hx = take(T * (size_t)d.H * 2);
+  L.hs = take(T * 4);
+  L.amax = take(S * (size_t)(d.I / 32) * 4);
+  L.amax_s = take(T * (Is / 32) * 4);
+  L.asc = take(S * 4);
+  L.asc_s = take(T * 4);
+  L.total = off;
+  return L;
+}
+
+// What the chain's entries need, and what a call with int8 or MXFP4 weights does.
 size_t chain_bytes(const moe_dims &d) { return ws_layout(d).total; }
+size_t int8_bytes(const moe_dims &d) { return int8_ws(d).total; }
 size_t mxfp4_bytes(const moe_dims &d) { return few_ffn(d) ? few_ws(d).total : chain_bytes(d); }
 
 // What the neediest entry needs for d or any smaller batch: a program makes one
@@ -278,7 +304,7 @@ size_t ws_total(const moe_dims &d) {
     if (T > d.T) return;
     moe_dims s = d;
     s.T = (int)T;
-    most = std::max(most, std::max(chain_bytes(s), mxfp4_bytes(s)));
+    most = std::max({most, chain_bytes(s), mxfp4_bytes(s), int8_bytes(s)});
   };
   at(d.T);
   at(kFewMaxT);
@@ -372,6 +398,7 @@ struct ExpertScratch {
   float *hs = nullptr, *amax = nullptr, *amax_s = nullptr;
   uint8_t *aq = nullptr, *aq_s = nullptr;  // and the activations' codes and row scales
   float *asc = nullptr, *asc_s = nullptr;
+  __nv_bfloat16 *hx = nullptr;  // int8 only: the hidden state's codes as fp16 values
 };
 
 // the scratch inside a caller's workspace (moe_workspace_bytes layout)
@@ -392,6 +419,19 @@ ExpertScratch scratch_in(const moe_dims &d, void *ws) {
   return sc;
 }
 
+// the same with int8's pieces
+ExpertScratch int8_scratch_in(const moe_dims &d, void *ws) {
+  const Int8Ws L = int8_ws(d);
+  ExpertScratch sc = scratch_in(d, ws);
+  sc.hx = at<__nv_bfloat16>(ws, L.hx);
+  sc.hs = at<float>(ws, L.hs);
+  sc.amax = at<float>(ws, L.amax);
+  sc.amax_s = at<float>(ws, L.amax_s);
+  sc.asc = at<float>(ws, L.asc);
+  sc.asc_s = at<float>(ws, L.asc_s);
+  return sc;
+}
+
 // Tensor maps and pointers of the grouped expert FFN; `phases` selects gate/up
 // (1), down (2) or both in one persistent launch (3).  gu_stride: rows from one
 // expert's gate (up) matrix to the next's -- I for separate [E, I, H] tensors,
@@ -402,7 +442,7 @@ moe_status do_expert_phases(const moe_dims &d, int phases, const moe_bf16 *hidde
                             const moe_bf16 *ws_down, moe_bf16 *y_sorted, moe_bf16 *y_shared,
                             const ExpertScratch &sc, cudaStream_t stream, bool pdl, uint64_t gu_stride = 0,
                             const moe_fp8_experts *q = nullptr, bool early = false, bool w8a8 = false,
-                            const moe_mxfp4_experts *q4 = nullptr) {
+                            const moe_mxfp4_experts *q4 = nullptr, const moe_int8_experts *i8 = nullptr) {
   // tiles of one launch at the narrowest chunking (16 tokens), for the 32-bit
   // claim counter and tile numbers
   {
@@ -464,6 +504,31 @@ moe_status do_expert_phases(const moe_dims &d, int phases, const moe_bf16 *hidde
     for (int b = 0; b < 4; ++b) ok = ok && map_u8_2d_sw(&g.map_act[b], g.aq, d.I, g.S, 16u << b);
     if (d.has_shared)
       for (int b = 0; b < 4; ++b) ok = ok && map_u8_2d_sw(&g.map_acts[b], g.aq_s, g.Is, d.T, 16u << b);
+    if (!ok) return MOE_ERR_CUDA;
+    return cuda_status(launch_expert_ffn(g, bn, num_sms(), stream, pdl));
+  }
+  if (i8 != nullptr) {  // int8: maps of the codes, and the row scales; the token codes in the place of hidden
+    g.mode = 4;
+    g.hidden = sc.hx;
+    g.sc_g = i8->gate_scale;
+    g.sc_u = i8->up_scale;
+    g.sc_d = i8->down_scale;
+    g.sc_sg = i8->s_gate_scale;
+    g.sc_su = i8->s_up_scale;
+    g.sc_sd = i8->s_down_scale;
+    g.hs = sc.hs;
+    g.amax = sc.amax;
+    g.amax_s = sc.amax_s;
+    g.asc = sc.asc;
+    g.asc_s = sc.asc_s;
+    ok = map_u8_3d(&g.map_wg, i8->gate, d.H, d.I, d.E, 128) && map_u8_3d(&g.map_wu, i8->up, d.H, d.I, d.E, 128) &&
+         map_u8_3d(&g.map_wd, i8->down, d.I, d.H, d.E, 128);
+    if (d.has_shared)
+      ok = ok && map_u8_2d(&g.map_sg, i8->s_gate, d.H, g.Is, 128) && map_u8_2d(&g.map_su, i8->s_up, d.H, g.Is, 128) &&
+           map_u8_2d(&g.map_sd, i8->s_down, g.Is, d.H, 128);
+    for (int b = 0; b < 4; ++b) ok = ok && map_bf16_2d(&g.map_act[b], g.act, d.I, g.S, 16u << b);
+    if (d.has_shared)
+      for (int b = 0; b < 4; ++b) ok = ok && map_bf16_2d(&g.map_acts[b], g.act_s, g.Is, d.T, 16u << b);
     if (!ok) return MOE_ERR_CUDA;
     return cuda_status(launch_expert_ffn(g, bn, num_sms(), stream, pdl));
   }
@@ -575,6 +640,16 @@ bool fp8_ok(const moe_dims &d, const moe_fp8_experts *q) {
 }
 
 bool mxfp4_ok(const moe_dims &d, const moe_mxfp4_experts *q) {
+  if (q == nullptr || !ptr_ok(q->gate) || !ptr_ok(q->up) || !ptr_ok(q->down) || !ptr_ok(q->gate_scale) ||
+      !ptr_ok(q->up_scale) || !ptr_ok(q->down_scale))
+    return false;
+  if (d.has_shared && (!ptr_ok(q->s_gate) || !ptr_ok(q->s_up) || !ptr_ok(q->s_down) || !ptr_ok(q->s_gate_scale) ||
+                       !ptr_ok(q->s_up_scale) || !ptr_ok(q->s_down_scale)))
+    return false;
+  return true;
+}
+
+bool int8_ok(const moe_dims &d, const moe_int8_experts *q) {
   if (q == nullptr || !ptr_ok(q->gate) || !ptr_ok(q->up) || !ptr_ok(q->down) || !ptr_ok(q->gate_scale) ||
       !ptr_ok(q->up_scale) || !ptr_ok(q->down_scale))
     return false;
@@ -940,6 +1015,72 @@ MOE_API moe_status moe_layer_forward_w8a8(const moe_dims *d, const moe_bf16 *hid
   if ((st = do_permute(*d, idx, at<int32_t>(ws, L.counts), offs, perm, inv, ws, s, true)) != MOE_OK) return st;
   if ((st = do_expert_phases(*d, 3, hidden, perm, offs, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, y, z,
                              sc, s, true, 0, w, true, true)) != MOE_OK)
+    return st;
+  return do_combine(*d, y, z, inv, wt, out, s, true);
+}
+
+MOE_API moe_status moe_quantize_int8_rows(const moe_bf16 *src, int64_t rows, int cols, int8_t *codes, float *scales,
+                                          void *stream) {
+  if (rows < 0 || cols <= 0 || cols % 8 != 0 || rows > INT64_MAX / cols) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!ptr_ok(src) || !ptr_ok(codes) || scales == nullptr || ((uintptr_t)scales & 3u) != 0) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_quantize_int8(reinterpret_cast<const __nv_bfloat16 *>(src), codes, false, scales,
+                                          (long long)rows, cols, (cudaStream_t)stream));
+}
+
+MOE_API moe_status moe_dequantize_int8_rows(const int8_t *codes, const float *scales, int64_t rows, int cols,
+                                            moe_bf16 *dst, void *stream) {
+  if (rows < 0 || cols <= 0 || cols % 8 != 0 || rows > INT64_MAX / cols) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!ptr_ok(dst) || !ptr_ok(codes) || scales == nullptr || ((uintptr_t)scales & 3u) != 0) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_dequantize_int8(codes, scales, reinterpret_cast<__nv_bfloat16 *>(dst), (long long)rows, cols,
+                                            (cudaStream_t)stream));
+}
+
+MOE_API moe_status moe_expert_ffn_int8(const moe_dims *d, const moe_bf16 *hidden, const int32_t *perm,
+                                       const int32_t *offsets, const moe_int8_experts *w, moe_bf16 *y_sorted,
+                                       moe_bf16 *y_shared, void *ws, size_t ws_bytes, void *stream) {
+  moe_status st = moe_check_dims(d);
+  if (st != MOE_OK) return st;
+  if (d->T == 0) return MOE_OK;
+  if (!ptr_ok(hidden) || !ptr_ok(perm) || !ptr_ok(offsets) || !ptr_ok(y_sorted) || !int8_ok(*d, w))
+    return MOE_ERR_INVALID_ARG;
+  if (d->has_shared && !ptr_ok(y_shared)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws(ws, ws_bytes, int8_bytes(*d))) != MOE_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  const ExpertScratch sc = int8_scratch_in(*d, ws);
+  if (launch_quantize_int8(reinterpret_cast<const __nv_bfloat16 *>(hidden), sc.hx, true, sc.hs, d->T, d->H, s) !=
+      cudaSuccess)
+    return MOE_ERR_CUDA;
+  return do_expert_phases(*d, 3, hidden, perm, offsets, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, y_sorted,
+                          y_shared, sc, s, true, 0, nullptr, false, false, nullptr, w);
+}
+
+MOE_API moe_status moe_layer_forward_int8(const moe_dims *d, const moe_bf16 *hidden, const float *router_w,
+                                          const float *expert_bias, const moe_int8_experts *w, moe_bf16 *out, void *ws,
+                                          size_t ws_bytes, void *stream) {
+  moe_status st = moe_check_dims(d);
+  if (st != MOE_OK) return st;
+  if (d->T == 0) return MOE_OK;
+  if (!ptr_ok(hidden) || !ptr_ok(router_w) || !ptr_ok(out) || !int8_ok(*d, w)) return MOE_ERR_INVALID_ARG;
+  if (expert_bias != nullptr && !aligned16(expert_bias)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws(ws, ws_bytes, int8_bytes(*d))) != MOE_OK) return st;
+  const WsLayout L = ws_layout(*d);
+  cudaStream_t s = (cudaStream_t)stream;
+  const ExpertScratch sc = int8_scratch_in(*d, ws);
+  int32_t *idx = at<int32_t>(ws, L.topk_idx);
+  float *wt = at<float>(ws, L.topk_w);
+  int32_t *perm = at<int32_t>(ws, L.perm), *inv = at<int32_t>(ws, L.inv);
+  int32_t *offs = at<int32_t>(ws, L.offsets);
+  moe_bf16 *y = at<moe_bf16>(ws, L.y_sorted), *z = at<moe_bf16>(ws, L.y_shared);
+  // the hidden state first, as for W8A8
+  if (launch_quantize_int8(reinterpret_cast<const __nv_bfloat16 *>(hidden), sc.hx, true, sc.hs, d->T, d->H, s) !=
+      cudaSuccess)
+    return MOE_ERR_CUDA;
+  if ((st = do_route(*d, hidden, router_w, expert_bias, nullptr, idx, wt, ws, s, true)) != MOE_OK) return st;
+  if ((st = do_permute(*d, idx, at<int32_t>(ws, L.counts), offs, perm, inv, ws, s, true)) != MOE_OK) return st;
+  if ((st = do_expert_phases(*d, 3, hidden, perm, offs, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, y, z, sc,
+                             s, true, 0, nullptr, true, false, nullptr, w)) != MOE_OK)
     return st;
   return do_combine(*d, y, z, inv, wt, out, s, true);
 }

@@ -61,6 +61,7 @@
 #include <cuda_fp8.h>
 
 #include "fp8.cuh"
+#include "int8.cuh"
 #include "internal.h"
 #include "mxfp4.cuh"
 #include "ptx.cuh"
@@ -101,8 +102,15 @@ constexpr unsigned long long kDrainNs = 20000000ull;
 // MXFP4 weights (kModeQ4) go the way of the weight-only FP8 ones: a code slot
 // holds 128 codes of each row, two K steps, and the converters multiply each code's
 // value by its block's power of two (exact in bf16).
-constexpr int kModeBF16 = 0, kModeQ8 = 1, kModeF8 = 2, kModeQ4 = 3;
-constexpr bool converts(int mode) { return mode == kModeQ8 || mode == kModeQ4; }
+// 8-bit integers (kModeI8): every product of two codes is exact in fp16 x fp16 ->
+// fp32, and the tensor cores' integer rate is far below that form's, so the weights'
+// codes go the way of the weight-only FP8 ones, to fp16, and the activations' codes
+// are kept as fp16 values.  A sum of code products is exact while it stays under
+// 2^24 and is rounded to fp32's 24 bits past that.
+constexpr int kModeBF16 = 0, kModeQ8 = 1, kModeF8 = 2, kModeQ4 = 3, kModeI8 = 4;
+constexpr bool converts(int mode) { return mode == kModeQ8 || mode == kModeQ4 || mode == kModeI8; }
+// The activations are quantised per row between the two products (W8A8, int8).
+__host__ __device__ constexpr bool requantizes(int mode) { return mode == kModeF8 || mode == kModeI8; }
 
 // Ring depths: weight slots of 32 KB and token slots of BN x 128 bytes; with
 // FP8 weights, code slots of 16 KB (the bytes in flight from HBM) and three
@@ -154,11 +162,11 @@ struct Layout {
   static_assert(kW <= 16 && kT <= 16 && kQ <= 16, "issue masks");
   static_assert(MODE != kModeQ8 || BN <= 128, "FP8 weights run the narrow tiles");
   static_assert(MODE != kModeQ4 || BN <= 240, "the code ring takes the staging of 256-token tiles");
-  static_assert(MODE != kModeF8 || BN <= 240, "the W8A8 epilogue has no staged (256-token) form");
+  static_assert(!requantizes(MODE) || BN <= 240, "the W8A8 and int8 epilogue has no staged (256-token) form");
 };
 
 struct Tile {
-  int phase;  // 0 gate/up, 1 down, 2 W8A8 activation quantisation of one chunk
+  int phase;  // 0 gate/up, 1 down, 2 W8A8 / int8 activation quantisation of one chunk
   int seg, rb, row0, ntok, N, nk, shared;
 };
 static_assert(sizeof(Tile) == 32, "a ring entry of the decoded tiles");
@@ -444,8 +452,8 @@ __device__ void build_sched_tables(const GemmParams &p, const Sched &q, SchedMis
     }
   }
   G1 += q.Rr * C + max(0, q.Rs - q.r_e) * q.nch_s;
-  // ---- W8A8: a quantisation tile per chunk between the gate/up and the down tiles
-  const int GD = G1 + (p.mode == 2 && q.Rd > 0 ? C * quant_blocks<BN>(p, p.I) +
+  // ---- W8A8, int8: a quantisation tile per chunk between the gate/up and the down tiles
+  const int GD = G1 + (requantizes(p.mode) && q.Rd > 0 ? C * quant_blocks<BN>(p, p.I) +
                                                        (p.has_shared ? q.nch_s * quant_blocks<BN>(p, p.Is) : 0)
                                                  : 0);
   // ---- down tiles: routed segments in order, the shared row blocks spread
@@ -557,14 +565,14 @@ __device__ __forceinline__ uint4 e2m1x8_to_bf16(uint32_t w, float s) {
 // gate/up epilogue kept; the quotients as the row quantiser forms them.  The
 // 128 loader threads: rows rbase + 16 j, the 8 threads of a row taking its
 // 16-value pieces c8, c8 + 8, ...  Activations and maxima were written by other
-// CTAs: read through L2.
-template <int BN>
+// CTAs: read through L2.  int8: the codes take the activations' own place, as fp16.
+template <int BN, int MODE>
 __device__ __forceinline__ void quantize_chunk_rows(const GemmParams &p, const Tile &tl, int rbase, int c8) {
   const int ld = tl.shared ? p.Is : p.I, nb = ld >> 5, npc = ld >> 4;
   const bool split = quant_blocks<BN>(p, ld) > 1;  // this tile covers 256 columns (16 pieces) of each row
   const int pc0 = split ? tl.rb * 16 : 0, pc1 = split ? min(pc0 + 16, npc) : npc;
   const float *am = tl.shared ? p.amax_s : p.amax;
-  const __nv_bfloat16 *act = tl.shared ? p.act_s : p.act;
+  __nv_bfloat16 *act = tl.shared ? p.act_s : p.act;
   uint8_t *codes = tl.shared ? p.aq_s : p.aq;
   float *scales = tl.shared ? p.asc_s : p.asc;
 #pragma unroll 1
@@ -575,6 +583,25 @@ __device__ __forceinline__ void quantize_chunk_rows(const GemmParams &p, const T
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
     if (row >= tl.ntok) continue;
+    if constexpr (MODE == kModeI8) {
+      const Int8Row rq = int8_row(m);
+      if (c8 == 0 && pc0 == 0) scales[tl.row0 + row] = rq.scale;
+      uint4 *at = reinterpret_cast<uint4 *>(act + (size_t)(tl.row0 + row) * ld);
+      for (int pc = pc0 + c8; pc < pc1; pc += 8) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 v = __ldcg(at + 2 * pc + h);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            o[e] = int8_f16x2(int8_round(__uint_as_float(w[e] << 16), rq),
+                              int8_round(__uint_as_float(w[e] & 0xFFFF0000u), rq));
+          at[2 * pc + h] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      continue;
+    }
     const float sc = e4m3_row_scale(m), rs = __frcp_rn(sc);
     if (c8 == 0 && pc0 == 0) scales[tl.row0 + row] = sc;
     const uint4 *src = reinterpret_cast<const uint4 *>(act + (size_t)(tl.row0 + row) * ld);
@@ -599,7 +626,8 @@ __device__ __forceinline__ void quantize_chunk_rows(const GemmParams &p, const T
 template <int BN, int MODE>
 __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __grid_constant__ GemmParams p) {
   using L = Layout<BN, MODE>;
-  constexpr bool Q8 = MODE == kModeQ8, F8 = MODE == kModeF8, Q4 = MODE == kModeQ4, CV = converts(MODE);
+  constexpr bool Q8 = MODE == kModeQ8, F8 = MODE == kModeF8, Q4 = MODE == kModeQ4, I8 = MODE == kModeI8;
+  constexpr bool CV = converts(MODE), RQ = requantizes(MODE);
   constexpr int KE = F8 ? 128 : 64;  // K elements per step: one 128-byte row of a weight or token box
   constexpr int KSH = F8 ? 7 : 6;
   constexpr int KW = L::kW, KT = L::kT, KQ = L::kQ, EW = L::kEpiW;
@@ -837,7 +865,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
       // every quantisation tile of its segment, each of which needed those
       if (tl.phase >= 1 && (p.phases & 1) && tid == 0) {
         const int nch = tl.shared ? q.nch_s : cst[tl.seg + 1] - cst[tl.seg];
-        const bool on_quant = F8 && tl.phase == 1;
+        const bool on_quant = RQ && tl.phase == 1;
         const unsigned *cnt = (on_quant ? done2 : done1) + tl.seg;
         const int nq = quant_blocks<BN>(p, tl.shared ? p.Is : p.I);  // quantisation tiles per chunk
         const unsigned need = (unsigned)(on_quant ? nch * nq : nch * (tl.shared ? q.Rs : q.Rr));
@@ -854,12 +882,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
         }
         fence_proxy_async_global();  // the activations were written by other CTAs' generic stores
       }
-      if constexpr (F8) {
+      if constexpr (RQ) {
         if (tl.phase == 2) {
-          // W8A8 quantisation tile: every loader thread reads activations and
+          // quantisation tile: every loader thread reads activations and
           // their row maxima itself, after thread 0's acquire of the count
           named_bar_sync(3, kTokThreads);
-          quantize_chunk_rows<BN>(p, tl, rbase, c8);
+          quantize_chunk_rows<BN, MODE>(p, tl, rbase, c8);
           __threadfence();  // the codes and scales, before the count (release)
           named_bar_sync(3, kTokThreads);
           if (tid == 0) atomicAdd(done2 + tl.seg, 1u);
@@ -975,7 +1003,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
         if (!ok) break;
         tc_fence_after();
         const uint32_t dh = tmem + (uint32_t)(acc * 2 * BN) + (uint32_t)(half * BN);
-        const uint32_t idesc = F8 ? idesc_e4m3(128, tl.N) : idesc_bf16(128, tl.N);
+        const uint32_t idesc = F8 ? idesc_e4m3(128, tl.N) : I8 ? idesc_f16(128, tl.N) : idesc_bf16(128, tl.N);
         for (int kb = 0; kb < tl.nk; ++kb) {
           ok = mbar_wait(wfull_bar(ws), wph, err, abort_flag) && mbar_wait(tfull_bar(ts), tph, err, abort_flag);
           if (!ok) break;
@@ -1038,14 +1066,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
       ok = __all_sync(0xffffffffu, mbar_wait(afull_bar(acc), aph, err, abort_flag));
       if (!ok) break;
       tc_fence_after();
-      if constexpr (F8) {  // a down tile's activation scales come from other CTAs' quantisation tiles
+      if constexpr (RQ) {  // a down tile's activation scales come from other CTAs' quantisation tiles
         if (tl.phase == 1 && (p.phases & 1)) (void)ld_acquire_gpu(done2 + tl.seg);
       }
       const uint32_t t0 = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * 2 * BN);
-      // FP8 weights: the accumulators hold sum(value(code) * x); this lane's
+      // FP8 or int8 weights: the accumulators hold sum(value(code) * x); this lane's
       // row scales turn them into the products with the weights
       float s0 = 1.0f, s1 = 1.0f;
-      if constexpr (Q8 || F8) {
+      if constexpr (Q8 || RQ) {
         if (tl.phase == 0) {
           const int ii = tl.rb * 128 + r;
           if (ii < (tl.shared ? p.Is : p.I)) {
@@ -1146,8 +1174,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
               tmem_ld16(t0 + (uint32_t)c16, g);
               tmem_ld16(t0 + (uint32_t)(BN + c16), u);
               tmem_wait_ld();
-              if constexpr (F8) {
-                // W8A8: the accumulators hold code products; each row's weight scale
+              if constexpr (RQ) {
+                // the accumulators hold code products; each row's weight scale
                 // and each column's token scale make them gate and up.  The bf16
                 // activation is stored, and its largest magnitude over this warp's
                 // 32 rows is kept per column for the down tiles' quantisation.
@@ -1170,7 +1198,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
                   }
                 }
                 const int col = col_max16(m, lane);  // lane's column of the warp-wide maxima (in m[0])
-                if ((lane & 1) == 0 && c16 + col < tl.ntok)
+                if ((lane & 1) == 0 && c16 + col < tl.ntok && tl.rb * 4 + q < (ld >> 5))
                   (tl.shared ? p.amax_s : p.amax)[(size_t)(tl.row0 + c16 + col) * (ld >> 5) + tl.rb * 4 + q] = m[0];
               } else if (ii < ld) {
 #pragma unroll
@@ -1206,18 +1234,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
               tmem_ld16(t0 + (uint32_t)(BN + c16), vb);
               tmem_wait_ld();
               float cs = 1.0f;
-              if constexpr (F8) {
+              if constexpr (RQ) {
                 // each column's activation scale, as its quantisation tile stored it
                 const int cj = c16 + (lane & 15);
                 if (cj < tl.ntok) cs = __ldcg((tl.shared ? p.asc_s : p.asc) + tl.row0 + cj);
               }
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                const float csj = F8 ? __shfl_sync(0xffffffffu, cs, j) : 1.0f;
+                const float csj = RQ ? __shfl_sync(0xffffffffu, cs, j) : 1.0f;
                 if (c16 + j < tl.ntok) {
                   __nv_bfloat16 *row = out + (size_t)(tl.row0 + c16 + j) * p.H;
-                  if (ha < p.H) __stcs(row + ha, __float2bfloat16_rn(Q8 ? va[j] * s0 : F8 ? va[j] * s0 * csj : va[j]));
-                  if (hb < p.H) __stcs(row + hb, __float2bfloat16_rn(Q8 ? vb[j] * s1 : F8 ? vb[j] * s1 * csj : vb[j]));
+                  if (ha < p.H) __stcs(row + ha, __float2bfloat16_rn(Q8 ? va[j] * s0 : RQ ? va[j] * s0 * csj : va[j]));
+                  if (hb < p.H) __stcs(row + hb, __float2bfloat16_rn(Q8 ? vb[j] * s1 : RQ ? vb[j] * s1 * csj : vb[j]));
                 }
               }
             }
@@ -1315,9 +1343,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
         }
       }
     }
-  } else if constexpr (Q8) {
-    // ================= FP8 weights (warps 14..21): codes -> bf16 weight slots
-    // (the values of the codes; the epilogue applies each row's scale).
+  } else if constexpr (Q8 || I8) {
+    // ================= FP8 (int8) weights (warps 14..21): codes -> bf16 (fp16) weight
+    // slots (the values of the codes; the epilogue applies each row's scale).
     // Two groups of four converter warps take alternate K steps (the per-step
     // handoff -- waits, proxy fence, arrivals -- then overlaps across groups).
     // Warp wg of a group converts rows 64 (wg & 1) .. + 63 of box wg >> 1; per
@@ -1327,10 +1355,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
     // step (j - 2) needed MMA j - 5 done, which orders the slot's earlier phase
     // (MMA j - 6) before its wait; with an even number of code slots, step
     // j - KQ belonged to the same group.
-    static_assert(!Q8 || (KQ % 2 == 0 && KW == 3), "two converter groups need an even code ring and three weight slots");
+    static_assert(!(Q8 || I8) || (KQ % 2 == 0 && KW == 3), "two converter groups need an even code ring and three weight slots");
     const int cw = warp - (kEpiWarp0 + EW);
     const int grp = cw >> 2, wg = cw & 3;
     const int box = wg >> 1, c = lane & 3;
+    auto wide = [](uint32_t a, uint32_t b) {  // eight codes to 16-bit values
+      if constexpr (I8) {
+        const uint2 x = int8x4_to_f16(a), y = int8x4_to_f16(b);
+        return make_uint4(x.x, x.y, y.x, y.y);
+      } else {
+        return e4m3x8_to_bf16(a, b);
+      }
+    };
     int ws = 0, qs = 0;
     uint32_t wph = 0, qph = 0;
     unsigned kstep = 0;
@@ -1357,9 +1393,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
 #pragma unroll
           for (int it = 0; it < 8; ++it) {
             const int rr = 64 * (wg & 1) + 8 * it + (lane >> 2);
-            *reinterpret_cast<uint4 *>(dst + rr * 128 + (((2 * c) ^ (rr & 7)) << 4)) = e4m3x8_to_bf16(v[it].x, v[it].y);
-            *reinterpret_cast<uint4 *>(dst + rr * 128 + (((2 * c + 1) ^ (rr & 7)) << 4)) =
-                e4m3x8_to_bf16(v[it].z, v[it].w);
+            *reinterpret_cast<uint4 *>(dst + rr * 128 + (((2 * c) ^ (rr & 7)) << 4)) = wide(v[it].x, v[it].y);
+            *reinterpret_cast<uint4 *>(dst + rr * 128 + (((2 * c + 1) ^ (rr & 7)) << 4)) = wide(v[it].z, v[it].w);
           }
           fence_proxy_async_smem();  // generic-proxy writes read by the tensor core
           __syncwarp();
@@ -1394,7 +1429,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
       volatile unsigned *s = p.sync;
       s[kSyncClaim] = 0;
       for (int i = 0; i < p.E + p.has_shared; ++i) s[kSyncDone + i] = 0;
-      if (p.mode == kModeF8)
+      if (RQ)
         for (int i = 0; i < p.E + p.has_shared; ++i) s[kSyncQuant + i] = 0;
       __threadfence();
       s[kSyncExit] = 0;
@@ -1443,6 +1478,16 @@ cudaError_t launch_expert_ffn(const GemmParams &p, int bn, int num_ctas, cudaStr
       case 128: return launch_one<128, kModeQ4>(p, num_ctas, stream, pdl);
       case 240: return launch_one<240, kModeQ4>(p, num_ctas, stream, pdl);
       default: return cudaErrorInvalidValue;  // 32 tokens and fewer run the one-kernel form
+    }
+  }
+  if (p.mode == kModeI8) {  // as W8A8
+    switch (bn < 240 ? bn : 240) {
+      case 16: return launch_one<16, kModeI8>(p, num_ctas, stream, pdl);
+      case 32: return launch_one<32, kModeI8>(p, num_ctas, stream, pdl);
+      case 64: return launch_one<64, kModeI8>(p, num_ctas, stream, pdl);
+      case 128: return launch_one<128, kModeI8>(p, num_ctas, stream, pdl);
+      case 240: return launch_one<240, kModeI8>(p, num_ctas, stream, pdl);
+      default: return cudaErrorInvalidValue;
     }
   }
   if (p.mode == kModeF8) {  // W8A8: up to 240-token tiles (the epilogue has no staged form)

@@ -79,13 +79,16 @@ struct GemmParams {
   int mode;
   const float *sc_g, *sc_u, *sc_d;     // [E][I], [E][I], [E][H]
   const float *sc_sg, *sc_su, *sc_sd;  // [Is], [Is], [H]
+  // int8 (mode 4): maps of the codes and scales as mode 1's; hidden holds the token
+  // codes as fp16 values and hs their scales, and the gate/up epilogue's bf16
+  // activations are replaced in place by their codes as fp16 values
   // MXFP4 (mode 3): maps as mode 1's, of the packed codes (K / 2 bytes a row), and
   // the scale bytes [E][I][H / 32], [E][I][H / 32], [E][H][I / 32], shared alike
   const uint8_t *qs_g, *qs_u, *qs_d, *qs_sg, *qs_su, *qs_sd;
-  // W8A8 (mode 2): the hidden state quantised per token (codes [T][H], scales
-  // [T]), and the gate/up epilogue's per-32-column maxima of the bf16
-  // activations ([S][I/32] routed, [T][Is/32] shared) that set the down tiles'
-  // per-row activation scales
+  // W8A8 (mode 2): the hidden state quantised per token (codes [T][H]; scales
+  // [T], mode 4 too), and the gate/up epilogue's per-32-column maxima of the bf16
+  // activations ([S][I/32] routed, [T][Is/32] shared; mode 4 too) that set the down
+  // tiles' per-row activation scales
   const uint8_t *hq;
   const float *hs;
   float *amax, *amax_s;
@@ -130,6 +133,14 @@ cudaError_t launch_combine(const CombineParams &p, cudaStream_t stream, bool pdl
 // matrix, one scale per row; cols a multiple of 8, pointers 16-byte aligned
 cudaError_t launch_quantize_rows(const __nv_bfloat16 *src, uint8_t *q, float *scale, long long rows, int cols,
                                  cudaStream_t stream);
+
+// ------------------------------------------------------------------ int8
+// codes [rows][cols] (bytes, or as fp16 values) and scale [rows] fp32 of a bf16
+// [rows][cols] matrix, one scale per row, rows >= 1, cols a multiple of 8; and back
+cudaError_t launch_quantize_int8(const __nv_bfloat16 *src, void *codes, bool f16, float *scales, long long rows,
+                                 int cols, cudaStream_t stream);
+cudaError_t launch_dequantize_int8(const int8_t *codes, const float *scales, __nv_bfloat16 *dst, long long rows,
+                                   int cols, cudaStream_t stream);
 
 // ----------------------------------------------------------------- MXFP4
 // packed codes [rows][cols / 2] and scale bytes [rows][cols / 32] of n = rows * cols

@@ -304,6 +304,50 @@ moe_status moe_layer_forward_w8a8(const moe_dims *d, const moe_bf16 *hidden, con
                                   const float *expert_bias, const moe_fp8_experts *w, moe_bf16 *out, void *ws,
                                   size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------ int8
+ * 8-bit integer experts, weights and activations: the other reading of the W8A8
+ * deployments that [case] names without a format.  A row's scale is m / 127 in
+ * fp32, m its largest magnitude (1 for a row of zeros); a code is 127 w / m to
+ * the nearest integer, ties to even (nothing is rounded before that); it stands for
+ * code * scale.  A row with an infinity or NaN has a NaN scale: every output that
+ * reads it is NaN, and its codes are unspecified.  Weights have a scale for each
+ * output row (channel).  Activations are quantised by the same rule at run time:
+ * the hidden state per token before the gate/up product, and the bf16 SiLU(gate) *
+ * up activation per routed slot (per token for the shared expert) before the down
+ * product.  Each output element is (sum of code products) * row scale * column
+ * scale; products are exact, and so is their sum while it stays under 2^24 (past
+ * that it is rounded as fp32 is).  The router stays fp32. */
+typedef struct {
+  const int8_t *gate, *up;                  /* [E, I, H] codes */
+  const int8_t *down;                       /* [E, H, I] */
+  const float *gate_scale, *up_scale;       /* [E, I] fp32, one per row */
+  const float *down_scale;                  /* [E, H] */
+  const int8_t *s_gate, *s_up;              /* shared expert [I_shared, H] (unused when !has_shared) */
+  const int8_t *s_down;                     /* [H, I_shared] */
+  const float *s_gate_scale, *s_up_scale;   /* [I_shared] */
+  const float *s_down_scale;                /* [H] */
+} moe_int8_experts;
+
+/* Quantise a bf16 matrix [rows, cols] (cols a multiple of 8) row by row: codes
+ * [rows, cols] and scales [rows] fp32; and the bf16 values (code * scale, rounded
+ * to fp32 and then to bf16) that they stand for.  Pointers 16-byte aligned (scales
+ * 4-byte).  Async on `stream`. */
+moe_status moe_quantize_int8_rows(const moe_bf16 *src, int64_t rows, int cols, int8_t *codes, float *scales,
+                                  void *stream);
+moe_status moe_dequantize_int8_rows(const int8_t *codes, const float *scales, int64_t rows, int cols, moe_bf16 *dst,
+                                    void *stream);
+
+/* moe_expert_ffn and moe_layer_forward with 8-bit integer experts (all pointers in
+ * *w 16-byte aligned); arguments, shapes, layouts and errors as for those.  The
+ * expert FFN first quantises `hidden` into the workspace; tiles of at most 240
+ * tokens. */
+moe_status moe_expert_ffn_int8(const moe_dims *d, const moe_bf16 *hidden, const int32_t *perm,
+                               const int32_t *offsets, const moe_int8_experts *w, moe_bf16 *y_sorted,
+                               moe_bf16 *y_shared, void *ws, size_t ws_bytes, void *stream);
+moe_status moe_layer_forward_int8(const moe_dims *d, const moe_bf16 *hidden, const float *router_w,
+                                  const float *expert_bias, const moe_int8_experts *w, moe_bf16 *out, void *ws,
+                                  size_t ws_bytes, void *stream);
+
 /* ----------------------------------------------------------------- MXFP4
  * MXFP4 expert weights (the Ascend deployment article, section 8.2, runs the
  * routed experts with them and fixes no further detail): OCP Microscaling,
