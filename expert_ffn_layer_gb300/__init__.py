@@ -8,6 +8,8 @@ Function names follow the C ABI:
 
     moe_route, moe_permute, moe_expert_ffn (= moe_expert_gate_up + moe_expert_down),
     moe_combine, moe_layer_forward,
+    moe_balance_loss, moe_route_backward, moe_combine_backward (the router's losses
+    and the backward passes of routing and combine),
     moe_fused_moe (routing given, stacked [E, 2I, H] gate/up weights),
     moe_quantize_fp8_rows, moe_expert_ffn_fp8, moe_layer_forward_fp8 (FP8 E4M3
     expert weights, one scale per row; see Fp8Experts / quantize_fp8_experts),
@@ -42,7 +44,7 @@ SCORE_SIGMOID_BIAS, SCORE_SOFTMAX = 0, 1
 
 EXPORTS = ("moe_status_string", "moe_check_dims", "moe_workspace_bytes", "moe_ws_init", "moe_ws_read_error",
            "moe_route", "moe_permute", "moe_expert_ffn", "moe_expert_gate_up", "moe_expert_down", "moe_combine",
-           "moe_layer_forward", "moe_fused_moe", "moe_expert_ffn_noalloc", "moe_selftest_wait_timeout",
+           "moe_combine_backward", "moe_balance_loss", "moe_route_backward", "moe_layer_forward", "moe_fused_moe", "moe_expert_ffn_noalloc", "moe_selftest_wait_timeout",
            "moe_selftest_silu", "moe_quantize_fp8_rows", "moe_expert_ffn_fp8", "moe_layer_forward_fp8",
            "moe_expert_ffn_w8a8", "moe_layer_forward_w8a8", "moe_quantize_int8_rows", "moe_dequantize_int8_rows",
            "moe_expert_ffn_int8", "moe_layer_forward_int8", "moe_quantize_mxfp4_rows", "moe_dequantize_mxfp4_rows",
@@ -109,6 +111,9 @@ def load() -> ctypes.CDLL:
         "moe_expert_gate_up": (st, [D, P, P, P, P, P, P, P, P, C, P]),
         "moe_expert_down": (st, [D, P, P, P, P, P, P, C, P]),
         "moe_combine": (st, [D, P, P, P, P, P, P]),
+        "moe_combine_backward": (st, [D, P, P, P, P, P, P, P]),
+        "moe_balance_loss": (st, [D, P, P, P, ctypes.c_int, P, P, P, P, C, P]),
+        "moe_route_backward": (st, [D, P, P, P, P, P, P, ctypes.c_int, P, P, P, P, P, P, P, C, P]),
         "moe_layer_forward": (st, [D, P, P, P, P, P, P, P, P, P, P, P, C, P]),
         "moe_fused_moe": (st, [D, P, P, P, P, P, P, P, P, P, C, P]),
         "moe_quantize_fp8_rows": (st, [P, ctypes.c_int64, ctypes.c_int, P, P, P]),
@@ -268,6 +273,67 @@ def moe_combine(d: MoeDims, y_sorted, y_shared, inv_perm, topk_w, out, stream=No
     _check(out, torch.bfloat16, (d.T, d.H), "out")
     _call("moe_combine", ctypes.byref(d), _ptr(y_sorted), _ptr(y_shared), _ptr(inv_perm), _ptr(topk_w), _ptr(out),
           _stream(stream))
+
+
+def moe_combine_backward(d: MoeDims, grad_out, y_sorted, inv_perm, topk_w, grad_topk_w=None, grad_y_sorted=None,
+                         stream=None) -> None:
+    """Gradients of moe_combine with respect to its weights (needs y_sorted) and to the
+    experts' outputs (needs topk_w)."""
+    S = d.T * d.top_k
+    _check(grad_out, torch.bfloat16, (d.T, d.H), "grad_out")
+    _check(y_sorted, torch.bfloat16, (S, d.H), "y_sorted")
+    _check(inv_perm, torch.int32, (S,), "inv_perm")
+    _check(topk_w, torch.float32, (d.T, d.top_k), "topk_w")
+    _check(grad_topk_w, torch.float32, (d.T, d.top_k), "grad_topk_w")
+    _check(grad_y_sorted, torch.bfloat16, (S, d.H), "grad_y_sorted")
+    _call("moe_combine_backward", ctypes.byref(d), _ptr(grad_out), _ptr(y_sorted), _ptr(inv_perm), _ptr(topk_w),
+          _ptr(grad_topk_w), _ptr(grad_y_sorted), _stream(stream))
+
+
+def moe_balance_loss(d: MoeDims, logits, topk_idx, counts, tokens, losses, ws, seq_id=None, stream=None) -> None:
+    """counts [n_seq, E] and tokens [n_seq] int32 of each sequence, losses [2] fp32 (the
+    balance and the z loss; None: the counts alone).  seq_id [T] int32: each token's
+    sequence, negative for padding; None: one sequence."""
+    n_seq = tokens.numel()
+    _check(logits, torch.float32, (d.T, d.E), "logits")
+    _check(topk_idx, torch.int32, (d.T, d.top_k), "topk_idx")
+    _check(counts, torch.int32, (n_seq, d.E), "counts")
+    _check(tokens, torch.int32, (n_seq,), "tokens")
+    _check(losses, torch.float32, (2,), "losses")
+    _check(seq_id, torch.int32, (d.T,), "seq_id")
+    _call("moe_balance_loss", ctypes.byref(d), _ptr(logits), _ptr(topk_idx), _ptr(seq_id), n_seq, _ptr(counts),
+          _ptr(tokens), _ptr(losses), _ptr(ws), ws.numel(), _stream(stream))
+
+
+def moe_route_backward(d: MoeDims, logits, topk_idx, ws, grad_w=None, grad_losses=None, counts=None, tokens=None,
+                       seq_id=None, hidden=None, router_w=None, grad_logits=None, grad_hidden=None,
+                       grad_router_w=None, n_seq=None, stream=None) -> None:
+    """Gradients of moe_route's combine weights (grad_w [T, k]) and of both losses
+    (grad_losses [2] fp32 on the device, with moe_balance_loss's counts and tokens)
+    with respect to the logits, to hidden (needs router_w) and to router_w (needs
+    hidden); each output is written where it is given.  n_seq: the sequences of seq_id
+    where tokens is not given."""
+    if tokens is not None:
+        n_seq = tokens.numel()
+    elif n_seq is None:
+        if seq_id is not None:
+            raise ValueError("seq_id without tokens: n_seq is needed")
+        n_seq = 1
+    _check(logits, torch.float32, (d.T, d.E), "logits")
+    _check(topk_idx, torch.int32, (d.T, d.top_k), "topk_idx")
+    _check(grad_w, torch.float32, (d.T, d.top_k), "grad_w")
+    _check(grad_losses, torch.float32, (2,), "grad_losses")
+    _check(counts, torch.int32, (n_seq, d.E), "counts")
+    _check(tokens, torch.int32, (n_seq,), "tokens")
+    _check(seq_id, torch.int32, (d.T,), "seq_id")
+    _check(hidden, torch.bfloat16, (d.T, d.H), "hidden")
+    _check(router_w, torch.float32, (d.E, d.H), "router_w")
+    _check(grad_logits, torch.float32, (d.T, d.E), "grad_logits")
+    _check(grad_hidden, torch.bfloat16, (d.T, d.H), "grad_hidden")
+    _check(grad_router_w, torch.float32, (d.E, d.H), "grad_router_w")
+    _call("moe_route_backward", ctypes.byref(d), _ptr(hidden), _ptr(router_w), _ptr(logits), _ptr(topk_idx),
+          _ptr(grad_w), _ptr(seq_id), n_seq, _ptr(counts), _ptr(tokens), _ptr(grad_losses), _ptr(grad_logits),
+          _ptr(grad_hidden), _ptr(grad_router_w), _ptr(ws), ws.numel(), _stream(stream))
 
 
 def moe_layer_forward(d: MoeDims, hidden, router_w, expert_bias, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, out,

@@ -290,6 +290,25 @@ Int8Ws int8_ws(const moe_dims &d) {
   return L;
 }
 
+// The router's losses and backward pass: sums of the loss kernel's CTAs, and the
+// gradient of the logits where the caller does not take it.
+struct RouterTrainWs {
+  size_t part, dl, total;
+};
+RouterTrainWs router_train_ws(const moe_dims &d) {
+  RouterTrainWs L;
+  size_t off = kWsHeaderBytes;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align256(off + bytes);
+    return o;
+  };
+  L.part = take(kBalanceMaxCtas * 2 * sizeof(double));
+  L.dl = take((size_t)d.T * d.E * 4);
+  L.total = off;
+  return L;
+}
+
 // What the chain's entries need, and what a call with int8 or MXFP4 weights does.
 size_t chain_bytes(const moe_dims &d) { return ws_layout(d).total; }
 size_t int8_bytes(const moe_dims &d) { return int8_ws(d).total; }
@@ -304,7 +323,7 @@ size_t ws_total(const moe_dims &d) {
     if (T > d.T) return;
     moe_dims s = d;
     s.T = (int)T;
-    most = std::max({most, chain_bytes(s), mxfp4_bytes(s), int8_bytes(s)});
+    most = std::max({most, chain_bytes(s), mxfp4_bytes(s), int8_bytes(s), router_train_ws(s).total});
   };
   at(d.T);
   at(kFewMaxT);
@@ -898,6 +917,115 @@ MOE_API moe_status moe_combine(const moe_dims *d, const moe_bf16 *y_sorted, cons
   if (!ptr_ok(y_sorted) || !ptr_ok(inv_perm) || !ptr_ok(topk_w) || !ptr_ok(out)) return MOE_ERR_INVALID_ARG;
   if (d->has_shared && !ptr_ok(y_shared)) return MOE_ERR_INVALID_ARG;
   return do_combine(*d, y_sorted, y_shared, inv_perm, topk_w, out, (cudaStream_t)stream, true);
+}
+
+MOE_API moe_status moe_combine_backward(const moe_dims *d, const moe_bf16 *grad_out, const moe_bf16 *y_sorted,
+                                        const int32_t *inv_perm, const float *topk_w, float *grad_topk_w,
+                                        moe_bf16 *grad_y_sorted, void *stream) {
+  moe_status st = moe_check_dims(d);
+  if (st != MOE_OK) return st;
+  if (d->T == 0) return MOE_OK;
+  if (grad_topk_w == nullptr && grad_y_sorted == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!ptr_ok(grad_out) || !ptr_ok(inv_perm)) return MOE_ERR_INVALID_ARG;
+  if (grad_topk_w != nullptr && (!ptr_ok(grad_topk_w) || !ptr_ok(y_sorted))) return MOE_ERR_INVALID_ARG;
+  if (grad_y_sorted != nullptr && (!ptr_ok(grad_y_sorted) || !ptr_ok(topk_w))) return MOE_ERR_INVALID_ARG;
+  CombineGradParams c;
+  c.grad_out = reinterpret_cast<const __nv_bfloat16 *>(grad_out);
+  c.y_sorted = reinterpret_cast<const __nv_bfloat16 *>(y_sorted);
+  c.inv = inv_perm;
+  c.topk_w = topk_w;
+  c.grad_w = grad_topk_w;
+  c.grad_y = reinterpret_cast<__nv_bfloat16 *>(grad_y_sorted);
+  c.T = d->T;
+  c.H = d->H;
+  c.top_k = d->top_k;
+  c.S = d->T * d->top_k;
+  return cuda_status(launch_combine_grad(c, (cudaStream_t)stream));
+}
+
+// seq_id and n_seq of the router's losses and backward pass.
+moe_status check_seqs(const moe_dims &d, const int32_t *seq_id, int n_seq) {
+  if (n_seq < 1 || (seq_id == nullptr && n_seq != 1 && d.T > 0) || (seq_id != nullptr && !aligned16(seq_id)))
+    return MOE_ERR_INVALID_ARG;
+  return n_seq > kMaxSeqs ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+MOE_API moe_status moe_balance_loss(const moe_dims *d, const float *logits, const int32_t *topk_idx,
+                                    const int32_t *seq_id, int n_seq, int32_t *counts, int32_t *tokens, float *losses,
+                                    void *ws, size_t ws_bytes, void *stream) {
+  moe_status st = moe_check_dims(d);
+  if (st != MOE_OK) return st;
+  if ((st = check_seqs(*d, seq_id, n_seq)) != MOE_OK) return st;
+  if (!ptr_ok(counts) || !ptr_ok(tokens) || (losses != nullptr && ((uintptr_t)losses & 3u) != 0))
+    return MOE_ERR_INVALID_ARG;
+  if (d->T > 0 && (!ptr_ok(topk_idx) || (losses != nullptr && !ptr_ok(logits)))) return MOE_ERR_INVALID_ARG;
+  const RouterTrainWs L = router_train_ws(*d);
+  if ((st = check_ws(ws, ws_bytes, L.total)) != MOE_OK) return st;
+  BalanceParams p;
+  p.logits = logits;
+  p.topk_idx = topk_idx;
+  p.seq_id = seq_id;
+  p.counts = counts;
+  p.tokens = tokens;
+  p.losses = losses;
+  p.part = at<double>(ws, L.part);
+  p.err = at<unsigned>(ws, 0);
+  p.done = p.err + kSyncLoss;
+  p.T = d->T;
+  p.E = d->E;
+  p.top_k = d->top_k;
+  p.n_seq = n_seq;
+  p.sigmoid = d->score_mode == MOE_SCORE_SIGMOID_BIAS;
+  return cuda_status(launch_balance(p, num_sms(), (cudaStream_t)stream));
+}
+
+MOE_API moe_status moe_route_backward(const moe_dims *d, const moe_bf16 *hidden, const float *router_w,
+                                      const float *logits, const int32_t *topk_idx, const float *grad_topk_w,
+                                      const int32_t *seq_id, int n_seq, const int32_t *counts, const int32_t *tokens,
+                                      const float *grad_losses, float *grad_logits, moe_bf16 *grad_hidden,
+                                      float *grad_router_w, void *ws, size_t ws_bytes, void *stream) {
+  moe_status st = moe_check_dims(d);
+  if (st != MOE_OK) return st;
+  if ((st = check_seqs(*d, seq_id, n_seq)) != MOE_OK) return st;
+  auto opt_ok = [](const void *p) { return p == nullptr || aligned16(p); };
+  if (grad_logits == nullptr && grad_hidden == nullptr && grad_router_w == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!opt_ok(grad_logits) || !opt_ok(grad_hidden) || !opt_ok(grad_router_w)) return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (d->T == 0)
+    return grad_router_w == nullptr ? MOE_OK
+                                    : cuda_status(cudaMemsetAsync(grad_router_w, 0, (size_t)d->E * d->H * 4, s));
+  if (grad_topk_w == nullptr && grad_losses == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!ptr_ok(logits) || !opt_ok(grad_topk_w) || (grad_topk_w != nullptr && !ptr_ok(topk_idx)))
+    return MOE_ERR_INVALID_ARG;
+  if (grad_losses != nullptr && (((uintptr_t)grad_losses & 3u) != 0 || !ptr_ok(counts) || !ptr_ok(tokens)))
+    return MOE_ERR_INVALID_ARG;
+  if ((grad_hidden != nullptr && !ptr_ok(router_w)) || (grad_router_w != nullptr && !ptr_ok(hidden)))
+    return MOE_ERR_INVALID_ARG;
+  const RouterTrainWs L = router_train_ws(*d);
+  if ((st = check_ws(ws, ws_bytes, L.total)) != MOE_OK) return st;
+  RouteGradParams p;
+  p.hidden = reinterpret_cast<const __nv_bfloat16 *>(hidden);
+  p.router_w = router_w;
+  p.logits = logits;
+  p.topk_idx = topk_idx;
+  p.grad_w = grad_topk_w;
+  p.seq_id = seq_id;
+  p.counts = counts;
+  p.tokens = tokens;
+  p.grad_losses = grad_losses;
+  p.dl = grad_logits != nullptr ? grad_logits : at<float>(ws, L.dl);
+  p.grad_hidden = reinterpret_cast<__nv_bfloat16 *>(grad_hidden);
+  p.grad_router_w = grad_router_w;
+  p.err = at<unsigned>(ws, 0);
+  p.T = d->T;
+  p.H = d->H;
+  p.E = d->E;
+  p.top_k = d->top_k;
+  p.n_seq = n_seq;
+  p.sigmoid = d->score_mode == MOE_SCORE_SIGMOID_BIAS;
+  p.route_scale = d->route_scale;
+  p.renorm_eps = d->renorm_eps;
+  return cuda_status(launch_route_grad(p, num_sms(), s));
 }
 
 MOE_API moe_status moe_fused_moe(const moe_dims *d, const moe_bf16 *hidden, const int32_t *topk_idx,

@@ -1,0 +1,164 @@
+// Per-expert counts of each sequence's choices, the balance loss and the z loss of
+// the router's logits (include/moe.h, moe_balance_loss).
+//
+//   balance = sum over counted tokens t of sequence b, experts e of F_be q_te,
+//             F_be = E c_be / (k n_b) / (n_b B),  q_te the normalised score
+//   z       = mean over counted tokens of lse_t^2
+//
+// Written this way round (the counts first) the loss needs no sum per expert over
+// a sequence's tokens: each token contributes one number.  Three kernels: zero,
+// count, and the logits' pass, whose CTAs leave one pair of sums each; the last
+// CTA adds them in CTA order, so that results do not depend on timing (the counts
+// are sums of integers).
+#include "internal.h"
+#include "ptx.cuh"
+#include "scores.cuh"
+
+namespace moe {
+
+namespace {
+constexpr int kThreads = 256;
+}
+
+__global__ void __launch_bounds__(kThreads) balance_zero_kernel(int32_t *counts, int32_t *tokens, long long nc, int n_seq) {
+  pdl_wait();
+  pdl_launch_dependents();
+  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < nc + n_seq; i += (long long)gridDim.x * kThreads) {
+    if (i < nc) counts[i] = 0;
+    else tokens[i - nc] = 0;
+  }
+}
+
+// A CTA's tokens are mostly of one sequence: the choices of its first token's
+// sequence are counted in shared memory and added at the end, the others' at once.
+__global__ void __launch_bounds__(kThreads) balance_count_kernel(const BalanceParams p, int per_cta) {
+  __shared__ int hist[256];
+  __shared__ int here;
+  pdl_launch_dependents();
+  const int t0 = blockIdx.x * per_cta, t1 = min(p.T, t0 + per_cta);
+  if (threadIdx.x == 0) here = 0;
+  for (int e = threadIdx.x; e < p.E; e += kThreads) hist[e] = 0;
+  pdl_wait();
+  const int home = p.seq_id == nullptr ? 0 : __ldg(p.seq_id + t0);
+  __syncthreads();
+  for (unsigned i = (unsigned)t0 * p.top_k + threadIdx.x; i < (unsigned)t1 * p.top_k; i += kThreads) {
+    const int t = (int)(i / p.top_k);
+    const int b = token_seq(p.seq_id, p.n_seq, t, p.err);
+    if (b < 0) continue;
+    const int e = checked_expert(__ldg(p.topk_idx + i), p.E, p.err);
+    const bool first = i == (unsigned)t * p.top_k;
+    if (b == home) {
+      atomicAdd(&hist[e], 1);
+      if (first) atomicAdd(&here, 1);
+    } else {
+      atomicAdd(p.counts + (size_t)b * p.E + e, 1);
+      if (first) atomicAdd(p.tokens + b, 1);
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += kThreads)
+    if (hist[e]) atomicAdd(p.counts + (size_t)home * p.E + e, hist[e]);
+  if (threadIdx.x == 0 && here) atomicAdd(p.tokens + home, here);
+}
+
+template <bool SIGMOID>
+__global__ void __launch_bounds__(kThreads) balance_loss_kernel(const BalanceParams p) {
+  __shared__ double sums[2][kThreads / 32];
+  __shared__ int nb[2];
+  __shared__ bool last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_launch_dependents();
+  pdl_wait();
+  // sequences with tokens, and all counted tokens
+  if (threadIdx.x < 2) nb[threadIdx.x] = 0;
+  __syncthreads();
+  int full = 0, total = 0;
+  for (int b = threadIdx.x; b < p.n_seq; b += kThreads) {
+    const int n = __ldcg(p.tokens + b);
+    full += n > 0;
+    total += n;
+  }
+  full = __reduce_add_sync(0xffffffffu, full);
+  total = __reduce_add_sync(0xffffffffu, total);
+  if (lane == 0) {
+    atomicAdd(&nb[0], full);
+    atomicAdd(&nb[1], total);
+  }
+  __syncthreads();
+  double balance = 0.0, z = 0.0;
+  for (unsigned t = blockIdx.x * (kThreads / 32) + warp; t < (unsigned)p.T; t += gridDim.x * (kThreads / 32)) {
+    const int b = token_seq(p.seq_id, p.n_seq, t, p.err);
+    if (b < 0) continue;
+    const TokenScores r = token_scores<SIGMOID, true>(p.logits + (size_t)t * p.E, p.E, lane);
+    const int32_t *c = p.counts + (size_t)b * p.E;
+    float dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j)
+      if (lane + 32 * j < p.E) dot = fmaf((float)__ldcg(c + lane + 32 * j), SIGMOID ? r.s[j] : r.p[j], dot);
+    dot = warp_sum(dot);
+    const float n = (float)__ldcg(p.tokens + b);
+    balance += (double)(dot / (SIGMOID ? r.total : 1.0f)) / ((double)n * n);
+    z += (double)r.lse * r.lse;
+  }
+  if (lane == 0) {
+    sums[0][warp] = balance;
+    sums[1][warp] = z;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double a = 0.0, b = 0.0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      a += sums[0][w];
+      b += sums[1][w];
+    }
+    p.part[2 * blockIdx.x] = a;
+    p.part[2 * blockIdx.x + 1] = b;
+    __threadfence();
+    last = atomicAdd(p.done, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last || warp > 1) return;
+  __threadfence();
+  // warp 0 the balance loss, warp 1 the z loss: lane l adds CTAs l, l + 32, ..
+  double v = 0.0;
+  for (int i = lane; i < (int)gridDim.x; i += 32) v += __ldcg(p.part + 2 * i + warp);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (lane == 0) {
+    const double scale = warp == 0 ? (double)p.E / p.top_k / max(nb[0], 1) : 1.0 / max(nb[1], 1);
+    p.losses[warp] = (float)(v * scale);
+    if (warp == 0) *p.done = 0;
+  }
+}
+
+cudaError_t launch_balance(const BalanceParams &p, int num_sms, cudaStream_t stream) {
+  {
+    const long long nc = (long long)p.n_seq * p.E, n = nc + p.n_seq;
+    long long blocks = (n + 4 * kThreads - 1) / (4 * kThreads);
+    if (blocks > num_sms) blocks = num_sms;
+    int32_t *counts = p.counts, *tokens = p.tokens;
+    int n_seq = p.n_seq;
+    long long nc_ = nc;
+    void *args[] = {(void *)&counts, (void *)&tokens, (void *)&nc_, (void *)&n_seq};
+    const cudaError_t e = launch_ex((const void *)balance_zero_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream,
+                                    true, 1, args);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.T == 0) return p.losses ? cudaMemsetAsync(p.losses, 0, 2 * sizeof(float), stream) : cudaSuccess;
+  {
+    int per = 32;  // tokens of a CTA
+    while ((p.T + per - 1) / per > 4 * num_sms) per *= 2;
+    void *args[] = {(void *)&p, (void *)&per};
+    const cudaError_t e = launch_ex((const void *)balance_count_kernel, dim3((p.T + per - 1) / per), dim3(kThreads), 0,
+                                    stream, true, 1, args);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.losses == nullptr) return cudaSuccess;
+  int blocks = (p.T + kThreads / 32 - 1) / (kThreads / 32);
+  if (blocks > kBalanceMaxCtas) blocks = kBalanceMaxCtas;
+  void *args[] = {(void *)&p};
+  return launch_ex(p.sigmoid ? (const void *)balance_loss_kernel<true> : (const void *)balance_loss_kernel<false>,
+                   dim3(blocks), dim3(kThreads), 0, stream, true, 1, args);
+}
+
+}  // namespace moe

@@ -98,6 +98,75 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineParams p
   }
 }
 
+// A CTA per token: its row of grad_out against the rows of its slots, 8 values a
+// thread step.  The sums over H are added across the CTA in a fixed order.
+__global__ void __launch_bounds__(kThreads) combine_grad_kernel(const CombineGradParams p) {
+  __shared__ float sums[kThreads / 32][kMaxK];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int hv = p.H >> 3, k = p.top_k;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+    float acc[kMaxK];
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j) acc[j] = 0.0f;
+    for (int c = threadIdx.x; c < hv; c += kThreads) {
+      float g[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      acc8(g, __ldg(reinterpret_cast<const uint4 *>(p.grad_out + (size_t)t * p.H) + c), 1.0f);
+#pragma unroll
+      for (int j = 0; j < kMaxK; ++j) {
+        if (j >= k) break;
+        const size_t pos = (size_t)min(max(__ldg(p.inv + (size_t)t * k + j), 0), p.S - 1);
+        if (p.grad_w != nullptr) {
+          const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p.y_sorted + pos * p.H) + c);
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            acc[j] = fmaf(g[2 * i], __uint_as_float(u[i] << 16), acc[j]);
+            acc[j] = fmaf(g[2 * i + 1], __uint_as_float(u[i] & 0xffff0000u), acc[j]);
+          }
+        }
+        if (p.grad_y != nullptr) {
+          const float w = __ldg(p.topk_w + (size_t)t * k + j);
+          uint4 o;
+          uint32_t *ou = reinterpret_cast<uint32_t *>(&o);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(w * g[2 * i], w * g[2 * i + 1]);
+            ou[i] = *reinterpret_cast<const uint32_t *>(&b);
+          }
+          __stcs(reinterpret_cast<uint4 *>(p.grad_y + pos * p.H) + c, o);
+        }
+      }
+    }
+    if (p.grad_w == nullptr) continue;
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j) {
+      if (j >= k) break;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+      if (lane == 0) sums[warp][j] = acc[j];
+    }
+    __syncthreads();
+    if (threadIdx.x < (unsigned)k) {
+      float s = 0.0f;
+      for (int w = 0; w < kThreads / 32; ++w) s += sums[w][threadIdx.x];
+      p.grad_w[(size_t)t * k + threadIdx.x] = s;
+    }
+    __syncthreads();
+  }
+}
+
+cudaError_t launch_combine_grad(const CombineGradParams &p, cudaStream_t stream) {
+  int dev = 0, nsm = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+  const int cap = (nsm > 0 ? nsm : 1) * 8;
+  void *args[] = {(void *)&p};
+  return launch_ex((const void *)combine_grad_kernel, dim3(p.T < cap ? p.T : cap), dim3(kThreads), 0, stream, true, 1,
+                   args);
+}
+
 cudaError_t launch_combine(const CombineParams &p, cudaStream_t stream, bool pdl) {
   static thread_local int nsm = 0, dev_cached = -1;
   int dev = 0;

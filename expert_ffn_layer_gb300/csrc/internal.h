@@ -111,6 +111,7 @@ struct GemmParams {
 // every launch leaves them zero again)
 constexpr int kSyncClaim = 64, kSyncExit = 65, kSyncPermute = 66,
               kSyncFew = 67,     // the one-kernel layer's three grid-wide waits and its exit counter
+              kSyncLoss = 72,    // the balance loss's finished CTAs
               kSyncDone = 128,   // kSyncDone .. + 257: gate/up tiles finished, per segment
               kSyncQuant = 512;  // kSyncQuant .. + 257: W8A8 quantisation tiles finished, per segment
 constexpr int kWsHeaderBytes = 4096;
@@ -127,6 +128,53 @@ struct CombineParams {
   int T, H, top_k, S;
 };
 cudaError_t launch_combine(const CombineParams &p, cudaStream_t stream, bool pdl);
+
+// Gradients of the combine: grad_w[t][j] = <grad_out[t], y_sorted[inv[t k + j]]> and
+// (unless nullptr) grad_y[inv[t k + j]] = topk_w[t][j] * grad_out[t]
+struct CombineGradParams {
+  const __nv_bfloat16 *grad_out;  // [T][H]
+  const __nv_bfloat16 *y_sorted;  // [S][H], or nullptr with grad_w
+  const int32_t *inv;             // [S]
+  const float *topk_w;            // [T][k], or nullptr with grad_y
+  float *grad_w;                  // [T][k] or nullptr
+  __nv_bfloat16 *grad_y;          // [S][H] or nullptr
+  int T, H, top_k, S;
+};
+cudaError_t launch_combine_grad(const CombineGradParams &p, cudaStream_t stream);
+
+// ------------------------------------------------ the router's losses
+struct BalanceParams {
+  const float *logits;      // [T][E]
+  const int32_t *topk_idx;  // [T][k]
+  const int32_t *seq_id;    // [T] or nullptr (one sequence)
+  int32_t *counts, *tokens;  // [n_seq][E], [n_seq]
+  float *losses;             // [2]: balance, z; or nullptr (counts only)
+  double *part;              // [kBalanceMaxCtas][2] workspace
+  unsigned *err, *done;      // workspace header words (done is left zero)
+  int T, E, top_k, n_seq, sigmoid;
+};
+constexpr int kBalanceMaxCtas = 1024;
+constexpr int kMaxSeqs = 65536;  // every CTA adds up the sequences' tokens
+cudaError_t launch_balance(const BalanceParams &p, int num_sms, cudaStream_t stream);
+
+// ------------------------------------------------ the routing's backward pass
+struct RouteGradParams {
+  const __nv_bfloat16 *hidden;  // [T][H]
+  const float *router_w;        // [E][H]
+  const float *logits;          // [T][E]
+  const int32_t *topk_idx;      // [T][k]
+  const float *grad_w;          // [T][k] or nullptr
+  const int32_t *seq_id;        // [T] or nullptr
+  const int32_t *counts, *tokens;
+  const float *grad_losses;  // [2] or nullptr
+  float *dl;                 // [T][E] gradient of the logits (the caller's, or workspace)
+  __nv_bfloat16 *grad_hidden;  // [T][H] or nullptr
+  float *grad_router_w;        // [E][H] or nullptr
+  unsigned *err;
+  int T, H, E, top_k, n_seq, sigmoid;
+  float route_scale, renorm_eps;
+};
+cudaError_t launch_route_grad(const RouteGradParams &p, int num_sms, cudaStream_t stream);
 
 // ------------------------------------------------------------------- FP8
 // codes [rows][cols] uint8 (E4M3) and scale [rows] fp32 of a bf16 [rows][cols]

@@ -1,0 +1,88 @@
+// What the router's losses and its backward pass need of one token's logits, held
+// by a warp: lane l has experts l, l + 32, .. (at most 256).
+#pragma once
+#include <stdint.h>
+
+#include "../../include/moe.h"
+
+namespace moe {
+
+constexpr int kPerLane = 8;  // experts of a lane
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// The sequence of token t, or -1 where the token counts nowhere (a negative
+// number, or one past the last sequence, which is flagged).
+__device__ __forceinline__ int token_seq(const int32_t *seq_id, int n_seq, int t, unsigned *err) {
+  if (seq_id == nullptr) return 0;
+  const int b = __ldg(seq_id + t);
+  if (b >= n_seq) {
+    atomicOr(err, MOE_DEVERR_INDEX);
+    return -1;
+  }
+  return b < 0 ? -1 : b;
+}
+__device__ __forceinline__ int checked_expert(int e, int E, unsigned *err) {
+  if (e < 0 || e >= E) {
+    atomicOr(err, MOE_DEVERR_INDEX);
+    return e < 0 ? 0 : E - 1;
+  }
+  return e;
+}
+
+struct TokenScores {
+  float p[kPerLane];     // softmax of the logits (0 past the last expert)
+  float s[kPerLane];     // sigmoid mode: sigmoid of the logits
+  float miss[kPerLane];  // sigmoid mode: 1 - s, from the other end
+  float total;           // sigmoid mode: the sum of s over all experts
+  float lse;             // log of the sum of the logits' exponentials
+};
+// SM: the softmax (and lse) is wanted; it is the score in softmax mode.
+template <bool SIGMOID, bool SM>
+__device__ __forceinline__ TokenScores token_scores(const float *lg, int E, int lane) {
+  TokenScores r;
+  float v[kPerLane];
+#pragma unroll
+  for (int j = 0; j < kPerLane; ++j) v[j] = lane + 32 * j < E ? __ldg(lg + lane + 32 * j) : -INFINITY;
+  r.total = 0.0f;
+  r.lse = 0.0f;
+  if (SM) {
+    float mx = v[0];
+#pragma unroll
+    for (int j = 1; j < kPerLane; ++j) mx = fmaxf(mx, v[j]);
+    mx = warp_max(mx);
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+      r.p[j] = lane + 32 * j < E ? expf(v[j] - mx) : 0.0f;
+      sum += r.p[j];
+    }
+    sum = warp_sum(sum);
+    const float inv = 1.0f / sum;
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) r.p[j] *= inv;
+    r.lse = mx + logf(sum);
+  }
+  if (SIGMOID) {
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+      const bool on = lane + 32 * j < E;
+      r.s[j] = on ? 1.0f / (1.0f + expf(-v[j])) : 0.0f;
+      r.miss[j] = on ? 1.0f / (1.0f + expf(v[j])) : 0.0f;
+      r.total += r.s[j];
+    }
+    r.total = warp_sum(r.total);
+  }
+  return r;
+}
+
+}  // namespace moe

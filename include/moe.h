@@ -218,6 +218,66 @@ moe_status moe_expert_ffn_noalloc(const moe_dims *d, const moe_bf16 *hidden, con
 moe_status moe_combine(const moe_dims *d, const moe_bf16 *y_sorted, const moe_bf16 *y_shared,
                        const int32_t *inv_perm, const float *topk_w, moe_bf16 *out, void *stream);
 
+/* -------------------------------------------------------- training the router
+ * The pages describe inference alone; these three calls are what tuning the router
+ * of such a layer needs (its experts frozen, or trained elsewhere).
+ *
+ * Sequences: seq_id [T] int32 gives each token's sequence in [0, n_seq); a negative
+ * number marks padding, which counts nowhere, gets a zero gradient and is not read
+ * (its logits and hidden state may hold anything).  A number of n_seq or more sets
+ * MOE_DEVERR_INDEX and is taken for padding.  seq_id NULL: one sequence (n_seq = 1).
+ * 1 <= n_seq <= 65536.
+ *
+ * moe_balance_loss: per-expert counts and the router's two auxiliary losses.
+ *   logits   [T, E] fp32, as moe_route writes them (may be NULL when losses is)
+ *   topk_idx [T, top_k] int32 (an entry outside [0, E) is clamped and flagged)
+ *   counts   [n_seq, E] int32 (output): c_be, the choices of expert e by sequence b
+ *   tokens   [n_seq] int32 (output): n_b, the sequence's tokens
+ *   losses   [2] fp32, 4-byte aligned (output; NULL: counts alone)
+ *     [0] balance: mean over the sequences with tokens of
+ *           sum_e (E c_be / (top_k n_b)) (mean over the sequence's tokens of q_te),
+ *         q_t = softmax(logits_t), or sigmoid(logits_t) over their sum in sigmoid
+ *         mode (the bias and route_scale take no part): 1 when choices or scores
+ *         are even
+ *     [1] z: mean over all counted tokens of (log sum_e exp logits_te)^2
+ *   Both are 0 when no token counts.  Sums over tokens are held in 64 bits and
+ *   added in a fixed order. */
+moe_status moe_balance_loss(const moe_dims *d, const float *logits, const int32_t *topk_idx, const int32_t *seq_id,
+                            int n_seq, int32_t *counts, int32_t *tokens, float *losses, void *ws, size_t ws_bytes,
+                            void *stream);
+
+/* moe_route_backward: gradients of moe_route's combine weights and of both losses.
+ *   logits, topk_idx, seq_id, n_seq   the forward calls' (topk_idx may be NULL when
+ *               grad_topk_w is)
+ *   grad_topk_w [T, top_k] fp32: gradient of the combine weights (NULL: none)
+ *   grad_losses [2] fp32 on the device, 4-byte aligned: gradients of the balance and
+ *               z losses, their coefficients in a sum (NULL: none); with it counts
+ *               and tokens as moe_balance_loss wrote them (counts are constants: no
+ *               gradient passes through the selection, nor to expert_bias)
+ *   grad_logits   [T, E] fp32 (output, may be NULL)
+ *   grad_hidden   [T, H] bf16 (output, may be NULL) = grad_logits * router_w
+ *   grad_router_w [E, H] fp32 (output, may be NULL) = grad_logits^T * hidden
+ *   hidden [T, H] is needed for grad_router_w, router_w [E, H] for grad_hidden.
+ *   One input gradient and one output at least.  A slot that names an expert twice
+ *   counts twice.  grad_hidden is the router's share alone, added to nothing.
+ *   T = 0 zeroes grad_router_w. */
+moe_status moe_route_backward(const moe_dims *d, const moe_bf16 *hidden, const float *router_w, const float *logits,
+                              const int32_t *topk_idx, const float *grad_topk_w, const int32_t *seq_id, int n_seq,
+                              const int32_t *counts, const int32_t *tokens, const float *grad_losses,
+                              float *grad_logits, moe_bf16 *grad_hidden, float *grad_router_w, void *ws,
+                              size_t ws_bytes, void *stream);
+
+/* moe_combine_backward: gradients of moe_combine.
+ *   grad_out      [T, H] bf16; inv_perm and topk_w as moe_combine's
+ *   grad_topk_w   [T, top_k] fp32 (output, may be NULL; needs y_sorted):
+ *                 sum_h grad_out[t, h] y_sorted[inv_perm[t * top_k + j], h]
+ *   grad_y_sorted [T * top_k, H] bf16 (output, may be NULL; needs topk_w): row
+ *                 inv_perm[t * top_k + j] = topk_w[t, j] * grad_out[t]
+ *   One output at least.  The gradient of y_shared is grad_out itself. */
+moe_status moe_combine_backward(const moe_dims *d, const moe_bf16 *grad_out, const moe_bf16 *y_sorted,
+                                const int32_t *inv_perm, const float *topk_w, float *grad_topk_w,
+                                moe_bf16 *grad_y_sorted, void *stream);
+
 /* Steps a3-a9 from a given routing, with stacked fused gate/up weights: the
  * shape of the fused-MoE call of [image] ("flashinfer" path: the flattened
  * tokens, the top-k expert indices and routing weights, and the expert
