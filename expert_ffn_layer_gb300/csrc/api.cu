@@ -290,10 +290,10 @@ Int8Ws int8_ws(const moe_dims &d) {
   return L;
 }
 
-// The router's losses and backward pass: sums of the loss kernel's CTAs, and the
-// gradient of the logits where the caller does not take it.
+// The router's losses and backward pass: sums of the loss kernel's CTAs, and the bf16
+// pieces of the logits' gradient and of the router weight.
 struct RouterTrainWs {
-  size_t part, dl, total;
+  size_t part, pieces, w_pieces, total;
 };
 RouterTrainWs router_train_ws(const moe_dims &d) {
   RouterTrainWs L;
@@ -304,7 +304,8 @@ RouterTrainWs router_train_ws(const moe_dims &d) {
     return o;
   };
   L.part = take(kBalanceMaxCtas * 2 * sizeof(double));
-  L.dl = take((size_t)d.T * d.E * 4);
+  L.pieces = take(3 * (size_t)d.T * ((d.E + 63) & ~63) * 2);
+  L.w_pieces = take(2 * (size_t)d.E * d.H * 2);
   L.total = off;
   return L;
 }
@@ -1004,6 +1005,17 @@ MOE_API moe_status moe_route_backward(const moe_dims *d, const moe_bf16 *hidden,
   const RouterTrainWs L = router_train_ws(*d);
   if ((st = check_ws(ws, ws_bytes, L.total)) != MOE_OK) return st;
   RouteGradParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.Epad = (d->E + 63) & ~63;
+  if (grad_hidden != nullptr || grad_router_w != nullptr) {
+    p.pieces = at<uint16_t>(ws, L.pieces);
+    p.w_pieces = at<uint16_t>(ws, L.w_pieces);
+    bool ok = map_bf16_3d(&p.map_dl_k, p.pieces, p.Epad, d->T, 3, 128) &&
+              map_bf16_3d(&p.map_dl_mn, p.pieces, p.Epad, d->T, 3, 64);
+    if (grad_hidden != nullptr) ok = ok && map_bf16_3d(&p.map_w, p.w_pieces, d->H, d->E, 2, 64);
+    if (grad_router_w != nullptr) ok = ok && map_bf16_2d(&p.map_x, hidden, d->H, d->T, 64);
+    if (!ok) return MOE_ERR_CUDA;
+  }
   p.hidden = reinterpret_cast<const __nv_bfloat16 *>(hidden);
   p.router_w = router_w;
   p.logits = logits;
@@ -1013,7 +1025,7 @@ MOE_API moe_status moe_route_backward(const moe_dims *d, const moe_bf16 *hidden,
   p.counts = counts;
   p.tokens = tokens;
   p.grad_losses = grad_losses;
-  p.dl = grad_logits != nullptr ? grad_logits : at<float>(ws, L.dl);
+  p.dl = grad_logits;
   p.grad_hidden = reinterpret_cast<__nv_bfloat16 *>(grad_hidden);
   p.grad_router_w = grad_router_w;
   p.err = at<unsigned>(ws, 0);

@@ -159,6 +159,13 @@ cudaError_t launch_balance(const BalanceParams &p, int num_sms, cudaStream_t str
 
 // ------------------------------------------------ the routing's backward pass
 struct RouteGradParams {
+  CUtensorMap map_x;      // hidden [T][H], box {64, 64}, 128-byte swizzle (as the others)
+  CUtensorMap map_dl_k;   // pieces of dl [3][T][Epad] bf16 (workspace), box {64, 128, 1}
+  CUtensorMap map_dl_mn;  // the same, box {64, 64, 1}
+  CUtensorMap map_w;      // pieces of the router weight [2][E][H] bf16 (workspace), box {64, 64, 1}
+  uint16_t *pieces, *w_pieces;  // pieces: nullptr when only dl is wanted
+  int Epad;                     // E rounded up to 64
+  int logit_blocks, hidden_stages, w_stages, w_smem;  // set by the launcher
   const __nv_bfloat16 *hidden;  // [T][H]
   const float *router_w;        // [E][H]
   const float *logits;          // [T][E]
@@ -167,14 +174,14 @@ struct RouteGradParams {
   const int32_t *seq_id;        // [T] or nullptr
   const int32_t *counts, *tokens;
   const float *grad_losses;  // [2] or nullptr
-  float *dl;                 // [T][E] gradient of the logits (the caller's, or workspace)
+  float *dl;                 // [T][E] gradient of the logits, or nullptr
   __nv_bfloat16 *grad_hidden;  // [T][H] or nullptr
   float *grad_router_w;        // [E][H] or nullptr
   unsigned *err;
   int T, H, E, top_k, n_seq, sigmoid;
   float route_scale, renorm_eps;
 };
-cudaError_t launch_route_grad(const RouteGradParams &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_route_grad(RouteGradParams p, int num_sms, cudaStream_t stream);
 
 // ------------------------------------------------------------------- FP8
 // codes [rows][cols] uint8 (E4M3) and scale [rows] fp32 of a bf16 [rows][cols]

@@ -18,17 +18,59 @@ namespace moe {
 
 namespace {
 constexpr int kThreads = 256;
+
+// A value as three bf16 pieces whose sum it is: its first 8 bits, the next rounded to
+// nearest even, the rest (at most 8 bits).  Below 2^-110 or so the rest runs out of
+// bf16's range.  Infinities and NaN are in the first piece alone.
+struct Pieces {
+  uint32_t hi, mid, lo;  // bf16 bits
+};
+__device__ __forceinline__ Pieces pieces_of(float v) {
+  Pieces r;
+  const uint32_t u = __float_as_uint(v);
+  if ((u & 0x7F800000u) == 0x7F800000u) {
+    r.hi = (u & 0x7FFFFFu) ? 0x7FC0u : u >> 16;
+    r.mid = r.lo = 0;
+    return r;
+  }
+  r.hi = u >> 16;
+  const float rest = v - __uint_as_float(r.hi << 16);
+  const __nv_bfloat16 m = __float2bfloat16_rn(rest);
+  r.mid = __bfloat16_as_ushort(m);
+  r.lo = __bfloat16_as_ushort(__float2bfloat16_rn(rest - __bfloat162float(m)));
+  return r;
 }
+}  // namespace
 
 // A warp per token.  1 - s is taken as the sigmoid of the negated logit, which keeps
 // its digits where s is near one.
+// The CTAs past logit_blocks split the router weight into the pieces that grad_hidden takes.
 template <bool SIGMOID>
-__global__ void __launch_bounds__(kThreads) grad_logits_kernel(const RouteGradParams p) {
+__global__ void __launch_bounds__(kThreads) grad_logits_kernel(const __grid_constant__ RouteGradParams p) {
   __shared__ int nb[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = p.E, k = p.top_k;
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
+  if ((int)blockIdx.x >= p.logit_blocks) {
+    const long long n8 = (long long)E * p.H / 8;
+    for (long long i = (long long)(blockIdx.x - p.logit_blocks) * kThreads + threadIdx.x; i < n8;
+         i += (long long)(gridDim.x - p.logit_blocks) * kThreads) {
+      const float4 a = __ldg(reinterpret_cast<const float4 *>(p.router_w) + 2 * i);
+      const float4 b = __ldg(reinterpret_cast<const float4 *>(p.router_w) + 2 * i + 1);
+      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      uint32_t hi[4], mid[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const Pieces x = pieces_of(v[2 * j]), y = pieces_of(v[2 * j + 1]);
+        hi[j] = x.hi | y.hi << 16;
+        mid[j] = x.mid | y.mid << 16;
+      }
+      reinterpret_cast<uint4 *>(p.w_pieces)[i] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      reinterpret_cast<uint4 *>(p.w_pieces)[n8 + i] = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+    }
+    return;
+  }
   float full = 1.0f, total = 1.0f, g0 = 0.0f, g1 = 0.0f;
   if (p.grad_losses != nullptr) {
     if (threadIdx.x < 2) nb[threadIdx.x] = 0;
@@ -51,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) grad_logits_kernel(const RouteGradPa
     g0 = __ldg(p.grad_losses);
     g1 = __ldg(p.grad_losses + 1);
   }
-  for (unsigned t = blockIdx.x * (kThreads / 32) + warp; t < (unsigned)p.T; t += gridDim.x * (kThreads / 32)) {
+  for (unsigned t = blockIdx.x * (kThreads / 32) + warp; t < (unsigned)p.T; t += p.logit_blocks * (kThreads / 32)) {
     const int b = token_seq(p.seq_id, p.n_seq, t, p.err);
     float d[kPerLane];
 #pragma unroll
@@ -123,80 +165,393 @@ __global__ void __launch_bounds__(kThreads) grad_logits_kernel(const RouteGradPa
     }
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j)
-      if (lane + 32 * j < E) p.dl[(size_t)t * E + lane + 32 * j] = d[j];
+      if (lane + 32 * j < E && p.dl != nullptr) p.dl[(size_t)t * E + lane + 32 * j] = d[j];
+    if (p.pieces != nullptr) {
+      const size_t plane = (size_t)p.T * p.Epad;
+      uint16_t *at = p.pieces + (size_t)t * p.Epad + lane;
+#pragma unroll
+      for (int j = 0; j < kPerLane; ++j)
+        if (32 * j < p.Epad) {  // zeros past the last expert
+          const Pieces x = pieces_of(d[j]);
+          at[32 * j] = (uint16_t)x.hi;
+          at[plane + 32 * j] = (uint16_t)x.mid;
+          at[2 * plane + 32 * j] = (uint16_t)x.lo;
+        }
+    }
   }
 }
 
-// grad_hidden[t, h] = sum_e dl[t, e] W[e, h]: 16 tokens x 256 columns a CTA.
-__global__ void __launch_bounds__(kThreads) grad_hidden_kernel(const RouteGradParams p) {
-  __shared__ float dl[16][256];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int t0 = blockIdx.y * 16, h = blockIdx.x * kThreads + threadIdx.x;
-  for (int i = threadIdx.x; i < 16 * p.E; i += kThreads) {
-    const int t = i / p.E, e = i - t * p.E;
-    dl[t][e] = t0 + t < p.T ? __ldcg(p.dl + (size_t)(t0 + t) * p.E + e) : 0.0f;
+// ------------------------------------------------------------- the products
+// grad_hidden = dl W and grad_router_w = dl^T x on the tensor cores.  An fp32 factor
+// goes in as bf16 pieces that add up to it: a first piece cut off after 8 bits, the
+// next rounded, the third what is left (exact).  grad_router_w takes all three pieces
+// of dl (x is bf16: its products are exact, rounding is that of the fp32 sums);
+// grad_hidden, rounded to bf16 in the end, two pieces of dl and of W and three of
+// their four products (relative error of a product 2^-15 at most).
+//
+// grad_hidden: a CTA keeps the pieces of W's 128 columns (at most 128 KB) and walks
+// over token tiles of 128, whose pieces of dl come in a ring of 64-expert steps.
+// grad_router_w: a CTA has 128 columns of x and a part of the tokens, in steps of
+// 64; both operands lie with their row dimension inner (MN-major).  The parts of one
+// tile are a cluster, which adds its fp32 tiles over shared memory in rank order.
+constexpr int kSmemMax = 232448;  // 227 KB opt-in per block
+constexpr int kBox = 64 * 128;    // 64 rows of 128 bytes
+constexpr int kProdThreads = 192;  // warp 0 TMA, 1 MMA, 2-5 epilogue (TMEM lane quarters 2,3,0,1)
+constexpr int kMaxSplit = 8;
+
+// Shared-memory matrix descriptor of an operand with its row dimension (M or N)
+// inner, 128-byte swizzle: atoms of 64 rows x 8 of K, 1024 bytes from one group of 8
+// of K to the next, `atom` bytes from one 64 rows to the next.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t atom) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(atom >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+constexpr uint32_t kTransA = 1u << 15, kTransB = 1u << 16;  // instruction descriptor: the operand is MN-major
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          dst),
+      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// Barriers, TMEM slot and abort flag of either product, behind its operands.
+struct ProdShared {
+  uint64_t full[4], empty[4], ready[4], afull[2], aempty[2], bfull;
+  uint32_t tmem;
+  int abort;
+};
+
+__global__ void __launch_bounds__(kProdThreads, 1) grad_hidden_kernel(const __grid_constant__ RouteGradParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const int eb = p.Epad >> 6, nst = p.hidden_stages;
+  const int b_piece = eb * 2 * kBox;  // one piece of W: eb steps of two 64-column boxes
+  uint8_t *ring = smem + 2 * b_piece;
+  constexpr int kStage = 4 * kBox;  // two pieces of 128 tokens x 64 experts
+  ProdShared *sh = (ProdShared *)(ring + nst * kStage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h0 = blockIdx.x * 128, tiles = (p.T + 127) >> 7;
+  volatile int *abort_flag = &sh->abort;
+  unsigned *err = p.err;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < nst; ++s) {
+      mbar_init(smem_u32(&sh->full[s]), 1);
+      mbar_init(smem_u32(&sh->empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&sh->afull[a]), 1);
+      mbar_init(smem_u32(&sh->aempty[a]), 4);
+    }
+    mbar_init(smem_u32(&sh->bfull), 1);
+    sh->abort = 0;
+    fence_mbar_init();
   }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sh->tmem), 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
   __syncthreads();
-  if (h >= p.H) return;
-  float a[16] = {};
-  for (int e = 0; e < p.E; ++e) {
-    const float w = __ldg(p.router_w + (size_t)e * p.H + h);
-#pragma unroll
-    for (int t = 0; t < 16; ++t) a[t] = fmaf(dl[t][e], w, a[t]);
-  }
-#pragma unroll
-  for (int t = 0; t < 16; ++t)
-    if (t0 + t < p.T) p.grad_hidden[(size_t)(t0 + t) * p.H + h] = __float2bfloat16_rn(a[t]);
-}
-
-// grad_router_w[e, h] = sum_t dl[t, e] x[t, h] over counted tokens: 16 experts x 256
-// columns a CTA, sums of 64 tokens added up in fp32.
-__global__ void __launch_bounds__(kThreads) grad_router_w_kernel(const RouteGradParams p) {
-  __shared__ float dl[64][16];
-  __shared__ int live[64];
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem;
+  pdl_wait();  // the pieces come from the kernel before
   pdl_launch_dependents();
-  pdl_wait();
-  const int e0 = blockIdx.y * 16, h = blockIdx.x * kThreads + threadIdx.x;
-  float sum[16] = {};
-  for (int t0 = 0; t0 < p.T; t0 += 64) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < 64 * 16; i += kThreads) {
-      const int t = i >> 4, e = e0 + (i & 15);
-      dl[t][i & 15] = t0 + t < p.T && e < p.E ? __ldcg(p.dl + (size_t)(t0 + t) * p.E + e) : 0.0f;
+  bool ok = true;
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t bb = smem_u32(&sh->bfull);
+      mbar_arrive_expect_tx(bb, (uint32_t)(2 * b_piece));
+      for (int pc = 0; pc < 2; ++pc)
+        for (int e = 0; e < eb; ++e)
+          for (int x = 0; x < 2; ++x)
+            tma_load_3d(smem_u32(smem + pc * b_piece + (2 * e + x) * kBox), &p.map_w, bb, h0 + 64 * x, 64 * e, pc);
+      int i = 0;
+      for (int t = blockIdx.y; t < tiles && ok; t += gridDim.y)
+        for (int e = 0; e < eb && ok; ++e, ++i) {
+          const int s = i % nst;
+          ok = mbar_wait(smem_u32(&sh->empty[s]), ((uint32_t)(i / nst) & 1u) ^ 1u, err, abort_flag);
+          if (!ok) break;
+          const uint32_t fb = smem_u32(&sh->full[s]), st = smem_u32(ring + s * kStage);
+          mbar_arrive_expect_tx(fb, kStage);
+          tma_load_3d(st, &p.map_dl_k, fb, 64 * e, 128 * t, 0);
+          tma_load_3d(st + 2 * kBox, &p.map_dl_k, fb, 64 * e, 128 * t, 1);
+        }
+      if (!ok) {  // leave no copy in flight (each wait bounded, the first without consuming anything)
+        mbar_wait(bb, 0, err, nullptr);
+        for (int j = i - nst < 0 ? 0 : i - nst; j < i; ++j)
+          mbar_wait(smem_u32(&sh->full[j % nst]), (uint32_t)(j / nst) & 1u, err, nullptr);
+      }
     }
-    if (threadIdx.x < 64)
-      live[threadIdx.x] = t0 + threadIdx.x < p.T && token_seq(p.seq_id, p.n_seq, t0 + threadIdx.x, p.err) >= 0;
-    __syncthreads();
-    if (h >= p.H) continue;
-    float a[16] = {};
-    for (int t = 0; t < 64; ++t) {
-      if (!live[t]) continue;
-      const float x = __bfloat162float(p.hidden[(size_t)(t0 + t) * p.H + h]);
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16(128, 128) | kTransB;
+      ok = mbar_wait(smem_u32(&sh->bfull), 0, err, abort_flag);
+      int i = 0, na = 0;
+      for (int t = blockIdx.y; t < tiles && ok; t += gridDim.y, ++na) {
+        const int acc = na & 1;
+        ok = mbar_wait(smem_u32(&sh->aempty[acc]), ((uint32_t)(na >> 1) & 1u) ^ 1u, err, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t dst = tmem + 128u * acc;
+        for (int e = 0; e < eb; ++e, ++i) {
+          const int s = i % nst;
+          ok = mbar_wait(smem_u32(&sh->full[s]), (uint32_t)(i / nst) & 1u, err, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t st = smem_u32(ring + s * kStage), wb = smem_u32(smem + 2 * e * kBox);
+          const uint64_t a0 = sdesc_sw128(st), a1 = sdesc_sw128(st + 2 * kBox);
+          const uint64_t b0 = sdesc_mn(wb, kBox), b1 = sdesc_mn(wb + b_piece, kBox);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) a[e] = fmaf(dl[t][e], x, a[e]);
+          for (int kk = 0; kk < 4; ++kk) {  // 16 experts: 32 bytes along dl's rows, 16 rows of W
+            umma_bf16(dst, a0 + 2 * kk, b0 + 128 * kk, idesc, (e > 0 || kk > 0) ? 1u : 0u);
+            umma_bf16(dst, a0 + 2 * kk, b1 + 128 * kk, idesc, 1u);
+            umma_bf16(dst, a1 + 2 * kk, b0 + 128 * kk, idesc, 1u);
+          }
+          umma_commit(smem_u32(&sh->empty[s]));
+        }
+        if (!ok) break;
+        umma_commit(smem_u32(&sh->afull[acc]));
+      }
     }
+  } else {
+    const int q = warp & 3;
+    int na = 0;
+    for (int t = blockIdx.y; t < tiles && ok; t += gridDim.y, ++na) {
+      const int acc = na & 1, row = 128 * t + 32 * q + lane;
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh->afull[acc]), (uint32_t)(na >> 1) & 1u, err, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t base = tmem + 128u * acc + ((uint32_t)(32 * q) << 16);
+      __nv_bfloat16 *dst = p.grad_hidden + (size_t)row * p.H + h0;
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        float v[32];
+        tmem_ld32(base + (uint32_t)c, v);
+        tmem_wait_ld();
+        if (row < p.T && h0 + c < p.H) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) sum[e] += a[e];
+          for (int j = 0; j < 32; j += 8) {
+            uint32_t o[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(v[j + 2 * u], v[j + 2 * u + 1]);
+              o[u] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+            *reinterpret_cast<uint4 *>(dst + c + j) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh->aempty[acc]));
+    }
   }
-  if (h >= p.H) return;
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (e0 + e < p.E) p.grad_router_w[(size_t)(e0 + e) * p.H + h] = sum[e];
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
 }
 
-cudaError_t launch_route_grad(const RouteGradParams &p, int num_sms, cudaStream_t stream) {
-  void *args[] = {(void *)&p};
+__global__ void __launch_bounds__(kProdThreads, 1) grad_router_w_kernel(const __grid_constant__ RouteGradParams p,
+                                                                        int waited) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const int eb = p.Epad >> 6, nst = p.w_stages;
+  const int stage = (2 + 3 * eb) * kBox;  // 128 columns of x and three pieces of dl, 64 tokens
+  ProdShared *sh = (ProdShared *)(smem + p.w_smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = gridDim.x, rank = blockIdx.x, h0 = blockIdx.y * 128;
+  const int blocks = (p.T + 63) >> 6;
+  const int k0 = (int)((long long)blocks * rank / split), k1 = (int)((long long)blocks * (rank + 1) / split);
+  const bool masked = p.seq_id != nullptr;
+  volatile int *abort_flag = &sh->abort;
+  unsigned *err = p.err;
+  uint32_t tmem_cols = 32;
+  while (tmem_cols < (uint32_t)p.Epad) tmem_cols <<= 1;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < nst; ++s) {
+      mbar_init(smem_u32(&sh->full[s]), 1);
+      mbar_init(smem_u32(&sh->empty[s]), 1);
+      mbar_init(smem_u32(&sh->ready[s]), 4);
+    }
+    mbar_init(smem_u32(&sh->afull[0]), 1);
+    sh->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sh->tmem), tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem;
+  // Behind grad_hidden_kernel, whose CTAs let this kernel start once each of them has
+  // waited for the pieces, they are there already; its own end is waited for below.
+  if (!waited) pdl_wait();
+  pdl_launch_dependents();
+  bool ok = true;
+  if (warp == 0) {
+    if (lane == 0) {
+      int i = 0;
+      for (int b = k0; b < k1; ++b, ++i) {
+        const int s = i % nst;
+        ok = mbar_wait(smem_u32(&sh->empty[s]), ((uint32_t)(i / nst) & 1u) ^ 1u, err, abort_flag);
+        if (!ok) break;
+        const uint32_t fb = smem_u32(&sh->full[s]), st = smem_u32(smem + s * stage);
+        mbar_arrive_expect_tx(fb, (uint32_t)stage);
+        tma_load_2d(st, &p.map_x, fb, h0, 64 * b);
+        tma_load_2d(st + kBox, &p.map_x, fb, h0 + 64, 64 * b);
+        for (int pc = 0; pc < 3; ++pc)
+          for (int e = 0; e < eb; ++e)
+            tma_load_3d(st + (2 + pc * eb + e) * kBox, &p.map_dl_mn, fb, 64 * e, 64 * b, pc);
+      }
+      if (!ok)
+        for (int j = i - nst < 0 ? 0 : i - nst; j < i; ++j)
+          mbar_wait(smem_u32(&sh->full[j % nst]), (uint32_t)(j / nst) & 1u, err, nullptr);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(128, p.Epad) | kTransA | kTransB;
+      for (int i = 0; i < k1 - k0; ++i) {
+        const int s = i % nst;
+        ok = mbar_wait(smem_u32(masked ? &sh->ready[s] : &sh->full[s]), (uint32_t)(i / nst) & 1u, err, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t st = smem_u32(smem + s * stage);
+        const uint64_t a = sdesc_mn(st, kBox);
+#pragma unroll
+        for (int pc = 2; pc >= 0; --pc) {  // the small pieces first
+          const uint64_t bd = sdesc_mn(st + (2 + pc * eb) * kBox, kBox);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16(tmem, a + 128 * kk, bd + 128 * kk, idesc, (i > 0 || pc < 2 || kk > 0) ? 1u : 0u);
+        }
+        umma_commit(smem_u32(&sh->empty[s]));
+      }
+      umma_commit(smem_u32(&sh->afull[0]));
+    }
+  } else {
+    if (masked) {
+      // padded tokens' rows of x are overwritten with zeros before they are multiplied
+      // (their rows of dl are zero, which NaN times would not be)
+      const int tid = threadIdx.x - 64, row = tid & 63, box = tid >> 6;
+      for (int i = 0; i < k1 - k0; ++i) {
+        const int s = i % nst, t = 64 * (k0 + i) + row;
+        const bool off = t < p.T && token_seq(p.seq_id, p.n_seq, t, err) < 0;
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh->full[s]), (uint32_t)(i / nst) & 1u, err, abort_flag));
+        if (!ok) break;
+        if (off) {
+          const uint32_t at = smem_u32(smem + s * stage + box * kBox + row * 128);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) st_shared_v4(at + 16 * c, make_uint4(0u, 0u, 0u, 0u));
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh->ready[s]));
+      }
+    }
+    ok = __all_sync(0xffffffffu, ok && mbar_wait(smem_u32(&sh->afull[0]), 0, err, abort_flag));
+    if (ok) {
+      // TMEM lane: a column of x; its columns: the experts
+      tc_fence_after();
+      const int q = warp & 3, h = h0 + 32 * q + lane;
+      const uint32_t base = tmem + ((uint32_t)(32 * q) << 16);
+      float *tile = reinterpret_cast<float *>(smem);  // [E][128]: every copy and product is done
+      for (int c = 0; c < p.E; c += 16) {
+        float v[16];
+        tmem_ld16(base + (uint32_t)c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          if (c + j >= p.E) break;
+          if (split > 1) tile[(c + j) * 128 + 32 * q + lane] = v[j];
+          else if (h < p.H) p.grad_router_w[(size_t)(c + j) * p.H + h] = v[j];
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, tmem_cols);
+  }
+  if (split > 1) {
+    cluster_sync();
+    // rank r adds up experts r, r + split, ..: a warp a row of 128 columns
+    const int col = 4 * lane;
+    for (int e = rank + split * warp; e < p.E; e += split * (kProdThreads / 32)) {
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int r = 0; r < split; ++r) {
+        const uint32_t at = map_cluster(smem_u32(smem) + (uint32_t)(e * 128 + col) * 4, (uint32_t)r);
+        float4 v;
+        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(at)
+                     : "memory");
+        a = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w);
+      }
+      if (h0 + col < p.H) *reinterpret_cast<float4 *>(p.grad_router_w + (size_t)e * p.H + h0 + col) = a;
+    }
+    cluster_sync();  // nobody leaves while its tile is being read
+  }
+  if (waited) pdl_wait();  // the next kernel waits for this one alone
+}
+
+cudaError_t launch_route_grad(RouteGradParams p, int num_sms, cudaStream_t stream) {
+  static thread_local unsigned long long attr_h = 0, attr_w = 0;
+  const int eb = p.Epad >> 6, tail = (int)sizeof(ProdShared) + 1024;
   int blocks = (p.T + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 8 * num_sms) blocks = 8 * num_sms;
-  cudaError_t e = launch_ex(p.sigmoid ? (const void *)grad_logits_kernel<true> : (const void *)grad_logits_kernel<false>,
-                            dim3(blocks), dim3(kThreads), 0, stream, true, 1, args);
-  const unsigned hb = (p.H + kThreads - 1) / kThreads;
-  if (e == cudaSuccess && p.grad_hidden != nullptr)
-    e = launch_ex((const void *)grad_hidden_kernel, dim3(hb, (p.T + 15) / 16), dim3(kThreads), 0, stream, true, 1, args);
-  if (e == cudaSuccess && p.grad_router_w != nullptr)
-    e = launch_ex((const void *)grad_router_w_kernel, dim3(hb, (p.E + 15) / 16), dim3(kThreads), 0, stream, false, 1, args);
-  return e;
+  p.logit_blocks = blocks;
+  if (p.grad_hidden != nullptr) {
+    const long long n = ((long long)p.E * p.H / 8 + kThreads - 1) / kThreads;
+    blocks += (int)(n < 2 * num_sms ? n : 2 * num_sms);
+  }
+  {
+    void *args[] = {(void *)&p};
+    const cudaError_t e = launch_ex(p.sigmoid ? (const void *)grad_logits_kernel<true> : (const void *)grad_logits_kernel<false>,
+                                    dim3(blocks), dim3(kThreads), 0, stream, true, 1, args);
+    if (e != cudaSuccess) return e;
+  }
+  const int hb = (p.H + 127) >> 7;
+  if (p.grad_hidden != nullptr) {
+    const cudaError_t e0 = set_smem_attr_once((const void *)grad_hidden_kernel, kSmemMax, attr_h);
+    if (e0 != cudaSuccess) return e0;
+    const int tiles = (p.T + 127) >> 7;
+    int rows = (num_sms + hb - 1) / hb;  // CTAs that share the token tiles
+    if (rows > tiles) rows = tiles;
+    p.hidden_stages = (kSmemMax - tail - 4 * eb * kBox) / (4 * kBox);
+    if (p.hidden_stages > 4) p.hidden_stages = 4;
+    const size_t smem = (size_t)(4 * eb + 4 * p.hidden_stages) * kBox + tail;
+    void *args[] = {(void *)&p};
+    const cudaError_t e = launch_ex((const void *)grad_hidden_kernel, dim3(hb, rows), dim3(kProdThreads), smem, stream, true,
+                                    1, args);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.grad_router_w != nullptr) {
+    const cudaError_t e0 = set_smem_attr_once((const void *)grad_router_w_kernel, kSmemMax, attr_w);
+    if (e0 != cudaSuccess) return e0;
+    const int steps = (p.T + 63) >> 6, stage = (2 + 3 * eb) * kBox;
+    int split = 1;  // parts of the tokens: a cluster
+    while (2 * split <= kMaxSplit && 2 * split <= steps && hb * 2 * split <= num_sms) split *= 2;
+    p.w_stages = (kSmemMax - tail) / stage;
+    if (p.w_stages > 4) p.w_stages = 4;
+    p.w_smem = p.w_stages * stage;
+    if (p.w_smem < p.E * 512) p.w_smem = (p.E * 512 + 127) & ~127;  // the tile that the cluster adds up
+    int waited = p.grad_hidden != nullptr;
+    void *args[] = {(void *)&p, (void *)&waited};
+    return launch_ex((const void *)grad_router_w_kernel, dim3(split, hb), dim3(kProdThreads), (size_t)p.w_smem + tail, stream,
+                     true, split, args);
+  }
+  return cudaSuccess;
 }
 
 }  // namespace moe
