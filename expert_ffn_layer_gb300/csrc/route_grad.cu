@@ -192,11 +192,16 @@ __global__ void __launch_bounds__(kThreads) grad_logits_kernel(const __grid_cons
 // grad_hidden: a CTA keeps the pieces of W's 128 columns (at most 128 KB) and walks
 // over token tiles of 128, whose pieces of dl come in a ring of 64-expert steps.
 // grad_router_w: a CTA has 128 columns of x and a part of the tokens, in steps of
-// 64; both operands lie with their row dimension inner (MN-major).  The parts of one
+// 64; both operands lie with their row dimension inner (MN-major).  The tensor cores'
+// fp32 sums are cut off, not rounded, at each step, which over thousands of tokens
+// would shrink the result (by 2.4e-6 of itself over 1024): two accumulators take 128
+// tokens in turn, and the epilogue warps add them up in registers.  The parts of one
 // tile are a cluster, which adds its fp32 tiles over shared memory in rank order.
 constexpr int kSmemMax = 232448;  // 227 KB opt-in per block
 constexpr int kBox = 64 * 128;    // 64 rows of 128 bytes
 constexpr int kProdThreads = 192;  // warp 0 TMA, 1 MMA, 2-5 epilogue (TMEM lane quarters 2,3,0,1)
+constexpr int kWThreads = 320;     // of grad_router_w: two epilogue warps per lane quarter
+constexpr int kChunk = 2;          // steps of 64 tokens before the accumulator changes
 constexpr int kMaxSplit = 8;
 
 // Shared-memory matrix descriptor of an operand with its row dimension (M or N)
@@ -357,8 +362,8 @@ __global__ void __launch_bounds__(kProdThreads, 1) grad_hidden_kernel(const __gr
   }
 }
 
-__global__ void __launch_bounds__(kProdThreads, 1) grad_router_w_kernel(const __grid_constant__ RouteGradParams p,
-                                                                        int waited) {
+__global__ void __launch_bounds__(kWThreads, 1) grad_router_w_kernel(const __grid_constant__ RouteGradParams p,
+                                                                     int waited) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int eb = p.Epad >> 6, nst = p.w_stages;
@@ -372,14 +377,17 @@ __global__ void __launch_bounds__(kProdThreads, 1) grad_router_w_kernel(const __
   volatile int *abort_flag = &sh->abort;
   unsigned *err = p.err;
   uint32_t tmem_cols = 32;
-  while (tmem_cols < (uint32_t)p.Epad) tmem_cols <<= 1;
+  while (tmem_cols < 2u * p.Epad) tmem_cols <<= 1;
   if (threadIdx.x == 0) {
     for (int s = 0; s < nst; ++s) {
       mbar_init(smem_u32(&sh->full[s]), 1);
       mbar_init(smem_u32(&sh->empty[s]), 1);
       mbar_init(smem_u32(&sh->ready[s]), 4);
     }
-    mbar_init(smem_u32(&sh->afull[0]), 1);
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&sh->afull[a]), 1);
+      mbar_init(smem_u32(&sh->aempty[a]), 8);
+    }
     sh->abort = 0;
     fence_mbar_init();
   }
@@ -419,7 +427,12 @@ __global__ void __launch_bounds__(kProdThreads, 1) grad_router_w_kernel(const __
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16(128, p.Epad) | kTransA | kTransB;
       for (int i = 0; i < k1 - k0; ++i) {
-        const int s = i % nst;
+        const int s = i % nst, chunk = i / kChunk, acc = chunk & 1;
+        if (i % kChunk == 0) {
+          ok = mbar_wait(smem_u32(&sh->aempty[acc]), ((uint32_t)(chunk >> 1) & 1u) ^ 1u, err, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+        }
         ok = mbar_wait(smem_u32(masked ? &sh->ready[s] : &sh->full[s]), (uint32_t)(i / nst) & 1u, err, abort_flag);
         if (!ok) break;
         tc_fence_after();
@@ -430,50 +443,79 @@ __global__ void __launch_bounds__(kProdThreads, 1) grad_router_w_kernel(const __
           const uint64_t bd = sdesc_mn(st + (2 + pc * eb) * kBox, kBox);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_bf16(tmem, a + 128 * kk, bd + 128 * kk, idesc, (i > 0 || pc < 2 || kk > 0) ? 1u : 0u);
+            umma_bf16(tmem + (uint32_t)(acc * p.Epad), a + 128 * kk, bd + 128 * kk, idesc,
+                      (i % kChunk || pc < 2 || kk > 0) ? 1u : 0u);
         }
         umma_commit(smem_u32(&sh->empty[s]));
+        if (i % kChunk == kChunk - 1 || i == k1 - k0 - 1) umma_commit(smem_u32(&sh->afull[acc]));
       }
-      umma_commit(smem_u32(&sh->afull[0]));
     }
   } else {
-    if (masked) {
-      // padded tokens' rows of x are overwritten with zeros before they are multiplied
-      // (their rows of dl are zero, which NaN times would not be)
-      const int tid = threadIdx.x - 64, row = tid & 63, box = tid >> 6;
-      for (int i = 0; i < k1 - k0; ++i) {
-        const int s = i % nst, t = 64 * (k0 + i) + row;
-        const bool off = t < p.T && token_seq(p.seq_id, p.n_seq, t, err) < 0;
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh->full[s]), (uint32_t)(i / nst) & 1u, err, abort_flag));
-        if (!ok) break;
-        if (off) {
-          const uint32_t at = smem_u32(smem + s * stage + box * kBox + row * 128);
+    // TMEM lane: a column of x; its columns: the experts, 16-column groups of the lane
+    // quarter in turn to its two warps, whose sums stay in registers
+    const int q = warp & 3, half = (warp - 2) >> 2, h = h0 + 32 * q + lane;
+    float sum[8][16];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) st_shared_v4(at + 16 * c, make_uint4(0u, 0u, 0u, 0u));
-          fence_proxy_async_smem();
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) sum[c][j] = 0.0f;
+    // padded tokens' rows of x are overwritten with zeros before they are multiplied
+    // (their rows of dl are zero, which NaN times would not be): the first four warps
+    const bool mask = masked && half == 0;
+    const int tid = threadIdx.x - 64, row = tid & 63, box = (tid >> 6) & 1;
+    const int steps = k1 - k0, chunks = (steps + kChunk - 1) / kChunk;
+    int cleared = 0;
+    for (int n = 0; n < chunks && ok; ++n) {
+      if (mask) {
+        // up to the end of the chunk after this one, as far as the ring reaches: the
+        // products of chunk n + 1 need not wait for the sums of chunk n
+        const int until = min(steps, min(kChunk * (n + 2), kChunk * (n + 1) + nst - 1));
+        for (; cleared < until; ++cleared) {
+          const int s = cleared % nst, t = 64 * (k0 + cleared) + row;
+          const bool off = t < p.T && token_seq(p.seq_id, p.n_seq, t, err) < 0;
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh->full[s]), (uint32_t)(cleared / nst) & 1u, err, abort_flag));
+          if (!ok) break;
+          if (off) {
+            const uint32_t at = smem_u32(smem + s * stage + box * kBox + row * 128);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) st_shared_v4(at + 16 * c, make_uint4(0u, 0u, 0u, 0u));
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh->ready[s]));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh->ready[s]));
+        if (!ok) break;
       }
-    }
-    ok = __all_sync(0xffffffffu, ok && mbar_wait(smem_u32(&sh->afull[0]), 0, err, abort_flag));
-    if (ok) {
-      // TMEM lane: a column of x; its columns: the experts
+      const int acc = n & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh->afull[acc]), (uint32_t)(n >> 1) & 1u, err, abort_flag));
+      if (!ok) break;
       tc_fence_after();
-      const int q = warp & 3, h = h0 + 32 * q + lane;
-      const uint32_t base = tmem + ((uint32_t)(32 * q) << 16);
+      const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * p.Epad + 16 * half);
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (32 * c + 16 * half < p.E) {
+          float v[16];
+          tmem_ld16(base + (uint32_t)(32 * c), v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[c][j] += v[j];
+        }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh->aempty[acc]));
+    }
+    if (ok) {
       float *tile = reinterpret_cast<float *>(smem);  // [E][128]: every copy and product is done
-      for (int c = 0; c < p.E; c += 16) {
-        float v[16];
-        tmem_ld16(base + (uint32_t)c, v);
-        tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          if (c + j >= p.E) break;
-          if (split > 1) tile[(c + j) * 128 + 32 * q + lane] = v[j];
-          else if (h < p.H) p.grad_router_w[(size_t)(c + j) * p.H + h] = v[j];
+          const int e = 32 * c + 16 * half + j;
+          if (e < p.E) {
+            if (split > 1) tile[e * 128 + 32 * q + lane] = sum[c][j];
+            else if (h < p.H) p.grad_router_w[(size_t)e * p.H + h] = sum[c][j];
+          }
         }
-      }
     }
   }
   tc_fence_before();
@@ -487,7 +529,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) grad_router_w_kernel(const __
     cluster_sync();
     // rank r adds up experts r, r + split, ..: a warp a row of 128 columns
     const int col = 4 * lane;
-    for (int e = rank + split * warp; e < p.E; e += split * (kProdThreads / 32)) {
+    for (int e = rank + split * warp; e < p.E; e += split * (kWThreads / 32)) {
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int r = 0; r < split; ++r) {
         const uint32_t at = map_cluster(smem_u32(smem) + (uint32_t)(e * 128 + col) * 4, (uint32_t)r);
@@ -548,7 +590,7 @@ cudaError_t launch_route_grad(RouteGradParams p, int num_sms, cudaStream_t strea
     if (p.w_smem < p.E * 512) p.w_smem = (p.E * 512 + 127) & ~127;  // the tile that the cluster adds up
     int waited = p.grad_hidden != nullptr;
     void *args[] = {(void *)&p, (void *)&waited};
-    return launch_ex((const void *)grad_router_w_kernel, dim3(split, hb), dim3(kProdThreads), (size_t)p.w_smem + tail, stream,
+    return launch_ex((const void *)grad_router_w_kernel, dim3(split, hb), dim3(kWThreads), (size_t)p.w_smem + tail, stream,
                      true, split, args);
   }
   return cudaSuccess;
