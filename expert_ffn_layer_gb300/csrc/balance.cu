@@ -6,8 +6,8 @@
 //   z       = mean over counted tokens of lse_t^2
 //
 // Written this way round (the counts first) the loss needs no sum per expert over
-// a sequence's tokens: each token contributes one number.  Three kernels: zero,
-// count, and the logits' pass, whose CTAs leave one pair of sums each; the last
+// a sequence's tokens: each token contributes one number.  Kernels: the
+// counts (in one, or zero and count), and the logits' pass, whose CTAs leave one pair of sums each; the last
 // CTA adds them in CTA order, so that results do not depend on timing (the counts
 // are sums of integers).
 #include "internal.h"
@@ -18,6 +18,9 @@ namespace moe {
 
 namespace {
 constexpr int kThreads = 256;
+constexpr int kClusterCtas = 8, kClusterThreads = 1024;
+constexpr int kClusterCounters = 11000;   // 44 KB of shared memory
+constexpr int kClusterSlots = 32 * kClusterCtas * kClusterThreads;  // 32 choices a thread
 }
 
 __global__ void __launch_bounds__(kThreads) balance_zero_kernel(int32_t *counts, int32_t *tokens, long long nc, int n_seq) {
@@ -61,6 +64,43 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(const BalancePa
   if (threadIdx.x == 0 && here) atomicAdd(p.tokens + home, here);
 }
 
+// Zero and count in one launch where the counters of all sequences fit in shared
+// memory and there is no more to count than a few CTAs do quickly: a cluster, each
+// CTA counting a part of the choices; then each adds up a part of the counters over
+// the cluster's shared memory.
+__global__ void __launch_bounds__(kClusterThreads) balance_cluster_kernel(const BalanceParams p) {
+  extern __shared__ int hist[];  // [n_seq][E] choices, [n_seq] tokens
+  pdl_wait();
+  pdl_launch_dependents();
+  const int n = p.n_seq * p.E + p.n_seq, parts = gridDim.x, rank = blockIdx.x;
+  for (int i = threadIdx.x; i < n; i += kClusterThreads) hist[i] = 0;
+  __syncthreads();
+  const int S = p.T * p.top_k;
+  for (int i = rank * kClusterThreads + threadIdx.x; i < S; i += parts * kClusterThreads) {
+    const int t = i / p.top_k;
+    const int b = token_seq(p.seq_id, p.n_seq, t, p.err);
+    if (b < 0) continue;
+    atomicAdd(&hist[b * p.E + checked_expert(__ldg(p.topk_idx + i), p.E, p.err)], 1);
+    if (i == t * p.top_k) atomicAdd(&hist[p.n_seq * p.E + b], 1);
+  }
+  cluster_sync();
+  for (int i = rank * kClusterThreads + threadIdx.x; i < n; i += parts * kClusterThreads) {
+    int v[kClusterCtas];
+#pragma unroll
+    for (int r = 0; r < kClusterCtas; ++r) {
+      v[r] = 0;
+      if (r < parts)
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v[r]) : "r"(map_cluster(smem_u32(hist + i), (uint32_t)r)) : "memory");
+    }
+    int sum = 0;
+#pragma unroll
+    for (int r = 0; r < kClusterCtas; ++r) sum += v[r];
+    if (i < p.n_seq * p.E) p.counts[i] = sum;
+    else p.tokens[i - p.n_seq * p.E] = sum;
+  }
+  cluster_sync();  // nobody leaves while its counters are being read
+}
+
 template <bool SIGMOID>
 __global__ void __launch_bounds__(kThreads) balance_loss_kernel(const BalanceParams p) {
   __shared__ double sums[2][kThreads / 32];
@@ -69,36 +109,24 @@ __global__ void __launch_bounds__(kThreads) balance_loss_kernel(const BalancePar
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_launch_dependents();
   pdl_wait();
-  // sequences with tokens, and all counted tokens
-  if (threadIdx.x < 2) nb[threadIdx.x] = 0;
-  __syncthreads();
-  int full = 0, total = 0;
-  for (int b = threadIdx.x; b < p.n_seq; b += kThreads) {
-    const int n = __ldcg(p.tokens + b);
-    full += n > 0;
-    total += n;
-  }
-  full = __reduce_add_sync(0xffffffffu, full);
-  total = __reduce_add_sync(0xffffffffu, total);
-  if (lane == 0) {
-    atomicAdd(&nb[0], full);
-    atomicAdd(&nb[1], total);
-  }
-  __syncthreads();
   double balance = 0.0, z = 0.0;
   for (unsigned t = blockIdx.x * (kThreads / 32) + warp; t < (unsigned)p.T; t += gridDim.x * (kThreads / 32)) {
     const int b = token_seq(p.seq_id, p.n_seq, t, p.err);
     if (b < 0) continue;
-    const TokenScores r = token_scores<SIGMOID, true>(p.logits + (size_t)t * p.E, p.E, lane);
-    const int32_t *c = p.counts + (size_t)b * p.E;
+    float v[kPerLane];
+    int c[kPerLane];
+    load_logits(p.logits + (size_t)t * p.E, p.E, lane, v);
+    const int32_t *of = p.counts + (size_t)b * p.E;
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) c[j] = lane + 32 * j < p.E ? __ldcg(of + lane + 32 * j) : 0;
+    const float n = (float)__ldcg(p.tokens + b);
+    const TokenScores r = token_scores<SIGMOID>(v, p.E, lane);
     float dot = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j)
-      if (lane + 32 * j < p.E) dot = fmaf((float)__ldcg(c + lane + 32 * j), SIGMOID ? r.s[j] : r.p[j], dot);
+    for (int j = 0; j < kPerLane; ++j) dot = fmaf((float)c[j], SIGMOID ? r.s[j] : r.p[j], dot);
     dot = warp_sum(dot);
-    const float n = (float)__ldcg(p.tokens + b);
-    balance += (double)(dot / (SIGMOID ? r.total : 1.0f)) / ((double)n * n);
-    z += (double)r.lse * r.lse;
+    balance += (double)(dot / ((SIGMOID ? r.total : 1.0f) * n) / n);
+    z += (double)(r.lse * r.lse);
   }
   if (lane == 0) {
     sums[0][warp] = balance;
@@ -117,7 +145,9 @@ __global__ void __launch_bounds__(kThreads) balance_loss_kernel(const BalancePar
     last = atomicAdd(p.done, 1u) == gridDim.x - 1;
   }
   __syncthreads();
-  if (!last || warp > 1) return;
+  if (!last) return;
+  const int2 nt = sequence_totals(p.tokens, p.n_seq, nb);
+  if (warp > 1) return;
   __threadfence();
   // warp 0 the balance loss, warp 1 the z loss: lane l adds CTAs l, l + 32, ..
   double v = 0.0;
@@ -125,14 +155,23 @@ __global__ void __launch_bounds__(kThreads) balance_loss_kernel(const BalancePar
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if (lane == 0) {
-    const double scale = warp == 0 ? (double)p.E / p.top_k / max(nb[0], 1) : 1.0 / max(nb[1], 1);
+    const double scale = warp == 0 ? (double)p.E / p.top_k / max(nt.x, 1) : 1.0 / max(nt.y, 1);
     p.losses[warp] = (float)(v * scale);
     if (warp == 0) *p.done = 0;
   }
 }
 
 cudaError_t launch_balance(const BalanceParams &p, int num_sms, cudaStream_t stream) {
-  {
+  const long long counters = (long long)p.n_seq * p.E + p.n_seq, slots = (long long)p.T * p.top_k;
+  const bool one = counters <= kClusterCounters && slots <= kClusterSlots;
+  if (one) {
+    int parts = 1;
+    while (parts < kClusterCtas && parts * kClusterThreads < slots) parts *= 2;
+    void *args[] = {(void *)&p};
+    const cudaError_t e = launch_ex((const void *)balance_cluster_kernel, dim3(parts), dim3(kClusterThreads),
+                                    (size_t)counters * 4, stream, true, parts, args);
+    if (e != cudaSuccess) return e;
+  } else {
     const long long nc = (long long)p.n_seq * p.E, n = nc + p.n_seq;
     long long blocks = (n + 4 * kThreads - 1) / (4 * kThreads);
     if (blocks > num_sms) blocks = num_sms;
@@ -145,7 +184,7 @@ cudaError_t launch_balance(const BalanceParams &p, int num_sms, cudaStream_t str
     if (e != cudaSuccess) return e;
   }
   if (p.T == 0) return p.losses ? cudaMemsetAsync(p.losses, 0, 2 * sizeof(float), stream) : cudaSuccess;
-  {
+  if (!one) {
     int per = 32;  // tokens of a CTA
     while ((p.T + per - 1) / per > 4 * num_sms) per *= 2;
     void *args[] = {(void *)&p, (void *)&per};

@@ -42,14 +42,106 @@ __device__ __forceinline__ Pieces pieces_of(float v) {
 }
 }  // namespace
 
-// A warp per token.  1 - s is taken as the sigmoid of the negated logit, which keeps
-// its digits where s is near one.
-// The CTAs past logit_blocks split the router weight into the pieces that grad_hidden takes.
+// What the losses' gradient needs of the whole batch.
+struct BatchTerms {
+  float load, gz, g0;  // E / (k B), 2 G1 / n, G0
+};
+__device__ __forceinline__ BatchTerms batch_terms(const RouteGradParams &p, int *sh) {
+  BatchTerms r = {0.0f, 0.0f, 0.0f};
+  if (p.grad_losses == nullptr) return r;
+  r.g0 = __ldg(p.grad_losses);
+  const float g1 = __ldg(p.grad_losses + 1);
+  const int2 nt = sequence_totals(p.tokens, p.n_seq, sh);
+  r.load = (float)p.E / (float)p.top_k / (float)max(nt.x, 1);
+  r.gz = g1 * 2.0f / (float)max(nt.y, 1);
+  return r;
+}
+
+// The gradient of token t's logits, by a warp.  1 - s is taken as the sigmoid of the
+// negated logit, which keeps its digits where s is near one.
+template <bool SIGMOID>
+__device__ __forceinline__ void token_grad(const RouteGradParams &p, const BatchTerms &bt, int t, int lane,
+                                           float (&d)[kPerLane]) {
+  const int E = p.E, k = p.top_k;
+#pragma unroll
+  for (int j = 0; j < kPerLane; ++j) d[j] = 0.0f;
+  // everything that is read goes out first; a padded token's is not used
+  const int b = token_seq(p.seq_id, p.n_seq, t, p.err);
+  float v[kPerLane];
+  load_logits(p.logits + (size_t)t * E, E, lane, v);
+  int e = 0;
+  float g = 0.0f;  // lane i < k holds slot i
+  if (p.grad_w != nullptr && lane < k) {
+    e = __ldg(p.topk_idx + (size_t)t * k + lane);
+    g = __ldg(p.grad_w + (size_t)t * k + lane);
+  }
+  if (b < 0) return;
+  int c[kPerLane];
+  float n = 1.0f;
+  if (p.grad_losses != nullptr) {
+    const int32_t *of = p.counts + (size_t)b * E;
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) c[j] = lane + 32 * j < E ? __ldg(of + lane + 32 * j) : 0;
+    n = (float)max(__ldg(p.tokens + b), 1);
+  }
+  const TokenScores r = token_scores<SIGMOID>(v, E, lane);
+  if (p.grad_losses != nullptr) {
+    const float load = bt.load / n / n, inv = SIGMOID ? 1.0f / r.total : 1.0f;
+    float dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) dot = fmaf((float)c[j] * load, (SIGMOID ? r.s[j] : r.p[j]) * inv, dot);
+    dot = warp_sum(dot);
+    const float gz = bt.gz * r.lse;
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+      const float q = (SIGMOID ? r.s[j] : r.p[j]) * inv;
+      d[j] = bt.g0 * q * ((float)c[j] * load - dot) * (SIGMOID ? r.miss[j] : 1.0f) + gz * r.p[j];
+    }
+  }
+  if (p.grad_w != nullptr) {
+    if (lane < k) e = checked_expert(e, E, p.err);
+    float score = 0.0f, rest = 0.0f;  // of the slot's expert, from the lane that has it
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+      const float a = __shfl_sync(0xffffffffu, SIGMOID ? r.s[j] : r.p[j], e & 31);
+      if (e >> 5 == j) score = a;
+      if (SIGMOID) {
+        const float m = __shfl_sync(0xffffffffu, r.miss[j], e & 31);
+        if (e >> 5 == j) rest = m;
+      }
+    }
+    if (lane >= k) score = 0.0f;
+    const float sel = warp_sum(score);
+    float w;  // the slot's contribution to its expert's logit
+    float spread = 0.0f;
+    if (!SIGMOID && !(sel >= p.renorm_eps)) {  // the clamp acts: the weight is p / eps
+      w = g / p.renorm_eps * score;
+      spread = warp_sum(w);
+    } else {
+      const float u = score / sel, mean = warp_sum(g * u);
+      w = u * (g - mean) * (SIGMOID ? p.route_scale * rest : 1.0f);
+    }
+    for (int i = 0; i < k; ++i) {
+      const int ei = __shfl_sync(0xffffffffu, e, i);
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+      for (int j = 0; j < kPerLane; ++j)
+        if (ei == lane + 32 * j) d[j] += wi;
+    }
+    if (spread != 0.0f) {
+#pragma unroll
+      for (int j = 0; j < kPerLane; ++j) d[j] = fmaf(-spread, r.p[j], d[j]);
+    }
+  }
+}
+
+// A warp per token.  The CTAs past logit_blocks split the router weight into the
+// pieces that grad_hidden takes.
 template <bool SIGMOID>
 __global__ void __launch_bounds__(kThreads) grad_logits_kernel(const __grid_constant__ RouteGradParams p) {
-  __shared__ int nb[2];
+  __shared__ int sh[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int E = p.E, k = p.top_k;
+  const int E = p.E;
   pdl_wait();
   pdl_launch_dependents();
   if ((int)blockIdx.x >= p.logit_blocks) {
@@ -71,101 +163,15 @@ __global__ void __launch_bounds__(kThreads) grad_logits_kernel(const __grid_cons
     }
     return;
   }
-  float full = 1.0f, total = 1.0f, g0 = 0.0f, g1 = 0.0f;
-  if (p.grad_losses != nullptr) {
-    if (threadIdx.x < 2) nb[threadIdx.x] = 0;
-    __syncthreads();
-    int f = 0, n = 0;
-    for (int b = threadIdx.x; b < p.n_seq; b += kThreads) {
-      const int m = __ldg(p.tokens + b);
-      f += m > 0;
-      n += m;
-    }
-    f = __reduce_add_sync(0xffffffffu, f);
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) {
-      atomicAdd(&nb[0], f);
-      atomicAdd(&nb[1], n);
-    }
-    __syncthreads();
-    full = (float)max(nb[0], 1);
-    total = (float)max(nb[1], 1);
-    g0 = __ldg(p.grad_losses);
-    g1 = __ldg(p.grad_losses + 1);
-  }
+  const BatchTerms bt = batch_terms(p, sh);
   for (unsigned t = blockIdx.x * (kThreads / 32) + warp; t < (unsigned)p.T; t += p.logit_blocks * (kThreads / 32)) {
-    const int b = token_seq(p.seq_id, p.n_seq, t, p.err);
     float d[kPerLane];
+    token_grad<SIGMOID>(p, bt, (int)t, lane, d);
+    if (p.dl != nullptr) {
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) d[j] = 0.0f;
-    if (b >= 0) {
-      const TokenScores r = token_scores<SIGMOID, true>(p.logits + (size_t)t * E, E, lane);
-      if (p.grad_losses != nullptr) {
-        const int32_t *c = p.counts + (size_t)b * E;
-        const float n = (float)max(__ldg(p.tokens + b), 1);
-        const float load = (float)E / (float)k / (n * n) / full, inv = SIGMOID ? 1.0f / r.total : 1.0f;
-        float F[kPerLane], dot = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kPerLane; ++j) {
-          F[j] = lane + 32 * j < E ? (float)__ldg(c + lane + 32 * j) * load : 0.0f;
-          dot = fmaf(F[j], (SIGMOID ? r.s[j] : r.p[j]) * inv, dot);
-        }
-        dot = warp_sum(dot);
-        const float gz = g1 * 2.0f * r.lse / total;
-#pragma unroll
-        for (int j = 0; j < kPerLane; ++j) {
-          const float q = (SIGMOID ? r.s[j] : r.p[j]) * inv;
-          d[j] = g0 * q * (F[j] - dot) * (SIGMOID ? r.miss[j] : 1.0f) + gz * r.p[j];
-        }
-      }
-      if (p.grad_w != nullptr) {
-        // lane i < k holds slot i
-        int e = 0;
-        float g = 0.0f;
-        if (lane < k) {
-          e = checked_expert(__ldg(p.topk_idx + (size_t)t * k + lane), E, p.err);
-          g = __ldg(p.grad_w + (size_t)t * k + lane);
-        }
-        float score = 0.0f, rest = 0.0f;  // of the slot's expert, from the lane that has it
-#pragma unroll
-        for (int j = 0; j < kPerLane; ++j) {
-          const float a = __shfl_sync(0xffffffffu, SIGMOID ? r.s[j] : r.p[j], e & 31);
-          if (e >> 5 == j) score = a;
-          if (SIGMOID) {
-            const float m = __shfl_sync(0xffffffffu, r.miss[j], e & 31);
-            if (e >> 5 == j) rest = m;
-          }
-        }
-        if (lane >= k) score = 0.0f;
-        const float sel = warp_sum(score);
-        float v;  // the slot's contribution to its expert's logit
-        float spread = 0.0f;
-        if (!SIGMOID && !(sel >= p.renorm_eps)) {  // the clamp acts: w = p / eps
-          const float a = g / p.renorm_eps;
-          spread = warp_sum(a * score);
-          v = a * score;
-        } else {
-          const float u = score / sel, mean = warp_sum(g * u);
-          v = u * (g - mean) * (SIGMOID ? p.route_scale * rest : 1.0f);
-        }
-        for (int i = 0; i < k; ++i) {
-          const int ei = __shfl_sync(0xffffffffu, e, i);
-          const float vi = __shfl_sync(0xffffffffu, v, i);
-          if ((ei & 31) == lane) {
-#pragma unroll
-            for (int j = 0; j < kPerLane; ++j)
-              if (ei >> 5 == j) d[j] += vi;
-          }
-        }
-        if (spread != 0.0f) {
-#pragma unroll
-          for (int j = 0; j < kPerLane; ++j) d[j] = fmaf(-spread, r.p[j], d[j]);
-        }
-      }
+      for (int j = 0; j < kPerLane; ++j)
+        if (lane + 32 * j < E) p.dl[(size_t)t * E + lane + 32 * j] = d[j];
     }
-#pragma unroll
-    for (int j = 0; j < kPerLane; ++j)
-      if (lane + 32 * j < E && p.dl != nullptr) p.dl[(size_t)t * E + lane + 32 * j] = d[j];
     if (p.pieces != nullptr) {
       const size_t plane = (size_t)p.T * p.Epad;
       uint16_t *at = p.pieces + (size_t)t * p.Epad + lane;
@@ -181,6 +187,70 @@ __global__ void __launch_bounds__(kThreads) grad_logits_kernel(const __grid_cons
   }
 }
 
+// The whole pass for few tokens in one kernel: every CTA forms all the logits'
+// gradients itself (a warp two tokens) and takes 32 columns of both products in
+// fp32.  The products are a read and a write of the router weight's size, and a
+// launch less to wait for.
+constexpr int kFewTokens = 16;
+template <bool SIGMOID>
+__global__ void __launch_bounds__(kThreads) grad_few_kernel(const __grid_constant__ RouteGradParams p) {
+  __shared__ int sh[2];
+  __shared__ float dl[kFewTokens][256];
+  __shared__ float part[kThreads / 32][kFewTokens][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int E = p.E, T = p.T, h = blockIdx.x * 32 + lane;
+  constexpr int kWarps = kThreads / 32;
+  pdl_wait();
+  pdl_launch_dependents();
+  const BatchTerms bt = batch_terms(p, sh);
+  for (int t = warp; t < T; t += kWarps) {
+    float d[kPerLane];
+    token_grad<SIGMOID>(p, bt, t, lane, d);
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+      dl[t][lane + 32 * j] = d[j];
+      if (p.dl != nullptr && blockIdx.x == 0 && lane + 32 * j < E) p.dl[(size_t)t * E + lane + 32 * j] = d[j];
+    }
+  }
+  __syncthreads();
+  // this lane's column: warp w takes experts w, w + 8, .. of both products
+  if (p.grad_router_w != nullptr) {
+    float x[kFewTokens];
+#pragma unroll
+    for (int t = 0; t < kFewTokens; ++t) {
+      x[t] = 0.0f;
+      if (t < T && token_seq(p.seq_id, p.n_seq, t, p.err) >= 0) x[t] = __bfloat162float(p.hidden[(size_t)t * p.H + h]);
+    }
+    for (int e = warp; e < E; e += kWarps) {
+      float a = 0.0f;
+#pragma unroll
+      for (int t = 0; t < kFewTokens; ++t)
+        if (t < T) a = fmaf(dl[t][e], x[t], a);
+      p.grad_router_w[(size_t)e * p.H + h] = a;
+    }
+  }
+  if (p.grad_hidden == nullptr) return;
+  float a[kFewTokens];
+#pragma unroll
+  for (int t = 0; t < kFewTokens; ++t) a[t] = 0.0f;
+#pragma unroll 4
+  for (int e = warp; e < E; e += kWarps) {
+    const float w = __ldg(p.router_w + (size_t)e * p.H + h);
+#pragma unroll
+    for (int t = 0; t < kFewTokens; ++t)
+      if (t < T) a[t] = fmaf(dl[t][e], w, a[t]);
+  }
+#pragma unroll
+  for (int t = 0; t < kFewTokens; ++t) part[warp][t][lane] = a[t];
+  __syncthreads();
+  for (int t = warp; t < T; t += kWarps) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += part[w][t][lane];
+    p.grad_hidden[(size_t)t * p.H + h] = __float2bfloat16_rn(s);
+  }
+}
+
 // ------------------------------------------------------------- the products
 // grad_hidden = dl W and grad_router_w = dl^T x on the tensor cores.  An fp32 factor
 // goes in as bf16 pieces that add up to it: a first piece cut off after 8 bits, the
@@ -192,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) grad_logits_kernel(const __grid_cons
 // grad_hidden: a CTA keeps the pieces of W's 128 columns (at most 128 KB) and walks
 // over token tiles of 128, whose pieces of dl come in a ring of 64-expert steps.
 // grad_router_w: a CTA has 128 columns of x and a part of the tokens, in steps of
-// 64; both operands lie with their row dimension inner (MN-major).  The tensor cores'
+// 32; both operands lie with their row dimension inner (MN-major).  The tensor cores'
 // fp32 sums are cut off, not rounded, at each step, which over thousands of tokens
 // would shrink the result (by 2.4e-6 of itself over 1024): two accumulators take 128
 // tokens in turn, and the epilogue warps add them up in registers.  The parts of one
@@ -201,7 +271,9 @@ constexpr int kSmemMax = 232448;  // 227 KB opt-in per block
 constexpr int kBox = 64 * 128;    // 64 rows of 128 bytes
 constexpr int kProdThreads = 192;  // warp 0 TMA, 1 MMA, 2-5 epilogue (TMEM lane quarters 2,3,0,1)
 constexpr int kWThreads = 320;     // of grad_router_w: two epilogue warps per lane quarter
-constexpr int kChunk = 2;          // steps of 64 tokens before the accumulator changes
+constexpr int kStep = 32;          // tokens of a step of grad_router_w
+constexpr int kWBox = kStep * 128;  // its boxes: 32 rows of 128 bytes
+constexpr int kChunk = 4;          // steps before the accumulator changes
 constexpr int kMaxSplit = 8;
 
 // Shared-memory matrix descriptor of an operand with its row dimension (M or N)
@@ -223,7 +295,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, 
 
 // Barriers, TMEM slot and abort flag of either product, behind its operands.
 struct ProdShared {
-  uint64_t full[4], empty[4], ready[4], afull[2], aempty[2], bfull;
+  uint64_t full[8], empty[8], ready[8], afull[2], aempty[2], bfull;
   uint32_t tmem;
   int abort;
 };
@@ -367,11 +439,11 @@ __global__ void __launch_bounds__(kWThreads, 1) grad_router_w_kernel(const __gri
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int eb = p.Epad >> 6, nst = p.w_stages;
-  const int stage = (2 + 3 * eb) * kBox;  // 128 columns of x and three pieces of dl, 64 tokens
+  const int stage = (2 + 3 * eb) * kWBox;  // 128 columns of x and three pieces of dl
   ProdShared *sh = (ProdShared *)(smem + p.w_smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = gridDim.x, rank = blockIdx.x, h0 = blockIdx.y * 128;
-  const int blocks = (p.T + 63) >> 6;
+  const int blocks = (p.T + kStep - 1) / kStep;
   const int k0 = (int)((long long)blocks * rank / split), k1 = (int)((long long)blocks * (rank + 1) / split);
   const bool masked = p.seq_id != nullptr;
   volatile int *abort_flag = &sh->abort;
@@ -413,11 +485,11 @@ __global__ void __launch_bounds__(kWThreads, 1) grad_router_w_kernel(const __gri
         if (!ok) break;
         const uint32_t fb = smem_u32(&sh->full[s]), st = smem_u32(smem + s * stage);
         mbar_arrive_expect_tx(fb, (uint32_t)stage);
-        tma_load_2d(st, &p.map_x, fb, h0, 64 * b);
-        tma_load_2d(st + kBox, &p.map_x, fb, h0 + 64, 64 * b);
+        tma_load_2d(st, &p.map_x, fb, h0, kStep * b);
+        tma_load_2d(st + kWBox, &p.map_x, fb, h0 + 64, kStep * b);
         for (int pc = 0; pc < 3; ++pc)
           for (int e = 0; e < eb; ++e)
-            tma_load_3d(st + (2 + pc * eb + e) * kBox, &p.map_dl_mn, fb, 64 * e, 64 * b, pc);
+            tma_load_3d(st + (2 + pc * eb + e) * kWBox, &p.map_dl_mn, fb, 64 * e, kStep * b, pc);
       }
       if (!ok)
         for (int j = i - nst < 0 ? 0 : i - nst; j < i; ++j)
@@ -437,12 +509,12 @@ __global__ void __launch_bounds__(kWThreads, 1) grad_router_w_kernel(const __gri
         if (!ok) break;
         tc_fence_after();
         const uint32_t st = smem_u32(smem + s * stage);
-        const uint64_t a = sdesc_mn(st, kBox);
+        const uint64_t a = sdesc_mn(st, kWBox);
 #pragma unroll
         for (int pc = 2; pc >= 0; --pc) {  // the small pieces first
-          const uint64_t bd = sdesc_mn(st + (2 + pc * eb) * kBox, kBox);
+          const uint64_t bd = sdesc_mn(st + (2 + pc * eb) * kWBox, kWBox);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
+          for (int kk = 0; kk < kStep / 16; ++kk)
             umma_bf16(tmem + (uint32_t)(acc * p.Epad), a + 128 * kk, bd + 128 * kk, idesc,
                       (i % kChunk || pc < 2 || kk > 0) ? 1u : 0u);
         }
@@ -462,7 +534,7 @@ __global__ void __launch_bounds__(kWThreads, 1) grad_router_w_kernel(const __gri
     // padded tokens' rows of x are overwritten with zeros before they are multiplied
     // (their rows of dl are zero, which NaN times would not be): the first four warps
     const bool mask = masked && half == 0;
-    const int tid = threadIdx.x - 64, row = tid & 63, box = (tid >> 6) & 1;
+    const int tid = threadIdx.x - 64, row = tid & (kStep - 1), piece = (tid / kStep) & 3;
     const int steps = k1 - k0, chunks = (steps + kChunk - 1) / kChunk;
     int cleared = 0;
     for (int n = 0; n < chunks && ok; ++n) {
@@ -471,14 +543,14 @@ __global__ void __launch_bounds__(kWThreads, 1) grad_router_w_kernel(const __gri
         // products of chunk n + 1 need not wait for the sums of chunk n
         const int until = min(steps, min(kChunk * (n + 2), kChunk * (n + 1) + nst - 1));
         for (; cleared < until; ++cleared) {
-          const int s = cleared % nst, t = 64 * (k0 + cleared) + row;
+          const int s = cleared % nst, t = kStep * (k0 + cleared) + row;
           const bool off = t < p.T && token_seq(p.seq_id, p.n_seq, t, err) < 0;
           ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh->full[s]), (uint32_t)(cleared / nst) & 1u, err, abort_flag));
           if (!ok) break;
           if (off) {
-            const uint32_t at = smem_u32(smem + s * stage + box * kBox + row * 128);
+            const uint32_t at = smem_u32(smem + s * stage + (piece >> 1) * kWBox + row * 128 + (piece & 1) * 64);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) st_shared_v4(at + 16 * c, make_uint4(0u, 0u, 0u, 0u));
+            for (int c = 0; c < 4; ++c) st_shared_v4(at + 16 * c, make_uint4(0u, 0u, 0u, 0u));
             fence_proxy_async_smem();
           }
           __syncwarp();
@@ -531,15 +603,19 @@ __global__ void __launch_bounds__(kWThreads, 1) grad_router_w_kernel(const __gri
     const int col = 4 * lane;
     for (int e = rank + split * warp; e < p.E; e += split * (kWThreads / 32)) {
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int r = 0; r < split; ++r) {
-        const uint32_t at = map_cluster(smem_u32(smem) + (uint32_t)(e * 128 + col) * 4, (uint32_t)r);
-        float4 v;
-        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                     : "r"(at)
-                     : "memory");
-        a = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w);
-      }
+      float4 v[kMaxSplit];
+#pragma unroll
+      for (int r = 0; r < kMaxSplit; ++r)
+        if (r < split) {
+          const uint32_t at = map_cluster(smem_u32(smem) + (uint32_t)(e * 128 + col) * 4, (uint32_t)r);
+          asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                       : "=f"(v[r].x), "=f"(v[r].y), "=f"(v[r].z), "=f"(v[r].w)
+                       : "r"(at)
+                       : "memory");
+        }
+#pragma unroll
+      for (int r = 0; r < kMaxSplit; ++r)
+        if (r < split) a = make_float4(a.x + v[r].x, a.y + v[r].y, a.z + v[r].z, a.w + v[r].w);
       if (h0 + col < p.H) *reinterpret_cast<float4 *>(p.grad_router_w + (size_t)e * p.H + h0 + col) = a;
     }
     cluster_sync();  // nobody leaves while its tile is being read
@@ -550,6 +626,11 @@ __global__ void __launch_bounds__(kWThreads, 1) grad_router_w_kernel(const __gri
 cudaError_t launch_route_grad(RouteGradParams p, int num_sms, cudaStream_t stream) {
   static thread_local unsigned long long attr_h = 0, attr_w = 0;
   const int eb = p.Epad >> 6, tail = (int)sizeof(ProdShared) + 1024;
+  if (p.T <= kFewTokens && p.pieces != nullptr) {
+    void *args[] = {(void *)&p};
+    return launch_ex(p.sigmoid ? (const void *)grad_few_kernel<true> : (const void *)grad_few_kernel<false>,
+                     dim3(p.H / 32), dim3(kThreads), 0, stream, true, 1, args);
+  }
   int blocks = (p.T + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 8 * num_sms) blocks = 8 * num_sms;
   p.logit_blocks = blocks;
@@ -568,7 +649,8 @@ cudaError_t launch_route_grad(RouteGradParams p, int num_sms, cudaStream_t strea
     const cudaError_t e0 = set_smem_attr_once((const void *)grad_hidden_kernel, kSmemMax, attr_h);
     if (e0 != cudaSuccess) return e0;
     const int tiles = (p.T + 127) >> 7;
-    int rows = (num_sms + hb - 1) / hb;  // CTAs that share the token tiles
+    int rows = num_sms / hb;  // CTAs that share the token tiles: one wave
+    if (rows < 1) rows = 1;
     if (rows > tiles) rows = tiles;
     p.hidden_stages = (kSmemMax - tail - 4 * eb * kBox) / (4 * kBox);
     if (p.hidden_stages > 4) p.hidden_stages = 4;
@@ -581,11 +663,11 @@ cudaError_t launch_route_grad(RouteGradParams p, int num_sms, cudaStream_t strea
   if (p.grad_router_w != nullptr) {
     const cudaError_t e0 = set_smem_attr_once((const void *)grad_router_w_kernel, kSmemMax, attr_w);
     if (e0 != cudaSuccess) return e0;
-    const int steps = (p.T + 63) >> 6, stage = (2 + 3 * eb) * kBox;
+    const int steps = (p.T + kStep - 1) / kStep, stage = (2 + 3 * eb) * kWBox;
     int split = 1;  // parts of the tokens: a cluster
     while (2 * split <= kMaxSplit && 2 * split <= steps && hb * 2 * split <= num_sms) split *= 2;
     p.w_stages = (kSmemMax - tail) / stage;
-    if (p.w_stages > 4) p.w_stages = 4;
+    if (p.w_stages > 8) p.w_stages = 8;
     p.w_smem = p.w_stages * stage;
     if (p.w_smem < p.E * 512) p.w_smem = (p.E * 512 + 127) & ~127;  // the tile that the cluster adds up
     int waited = p.grad_hidden != nullptr;

@@ -39,6 +39,30 @@ __device__ __forceinline__ int checked_expert(int e, int E, unsigned *err) {
   return e;
 }
 
+// Sequences with tokens, and all counted tokens, by the whole CTA (`sh` is shared).
+__device__ __forceinline__ int2 sequence_totals(const int32_t *tokens, int n_seq, int *sh) {
+  if (n_seq == 1) {
+    const int n = __ldcg(tokens);
+    return make_int2(n > 0, n);
+  }
+  if (threadIdx.x < 2) sh[threadIdx.x] = 0;
+  __syncthreads();
+  int full = 0, total = 0;
+  for (int b = threadIdx.x; b < n_seq; b += blockDim.x) {
+    const int n = __ldcg(tokens + b);
+    full += n > 0;
+    total += n;
+  }
+  full = __reduce_add_sync(0xffffffffu, full);
+  total = __reduce_add_sync(0xffffffffu, total);
+  if ((threadIdx.x & 31) == 0 && full) {
+    atomicAdd(&sh[0], full);
+    atomicAdd(&sh[1], total);
+  }
+  __syncthreads();
+  return make_int2(sh[0], sh[1]);
+}
+
 struct TokenScores {
   float p[kPerLane];     // softmax of the logits (0 past the last expert)
   float s[kPerLane];     // sigmoid mode: sigmoid of the logits
@@ -46,16 +70,14 @@ struct TokenScores {
   float total;           // sigmoid mode: the sum of s over all experts
   float lse;             // log of the sum of the logits' exponentials
 };
-// SM: the softmax (and lse) is wanted; it is the score in softmax mode.
-template <bool SIGMOID, bool SM>
-__device__ __forceinline__ TokenScores token_scores(const float *lg, int E, int lane) {
-  TokenScores r;
-  float v[kPerLane];
+__device__ __forceinline__ void load_logits(const float *lg, int E, int lane, float (&v)[kPerLane]) {
 #pragma unroll
   for (int j = 0; j < kPerLane; ++j) v[j] = lane + 32 * j < E ? __ldg(lg + lane + 32 * j) : -INFINITY;
-  r.total = 0.0f;
-  r.lse = 0.0f;
-  if (SM) {
+}
+template <bool SIGMOID>
+__device__ __forceinline__ TokenScores token_scores(const float (&v)[kPerLane], int E, int lane) {
+  TokenScores r;
+  {
     float mx = v[0];
 #pragma unroll
     for (int j = 1; j < kPerLane; ++j) mx = fmaxf(mx, v[j]);
@@ -72,6 +94,7 @@ __device__ __forceinline__ TokenScores token_scores(const float *lg, int E, int 
     for (int j = 0; j < kPerLane; ++j) r.p[j] *= inv;
     r.lse = mx + logf(sum);
   }
+  r.total = 0.0f;
   if (SIGMOID) {
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) {
