@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) balance_loss_kernel(const BalancePar
     load_logits(p.logits + (size_t)t * p.E, p.E, lane, v);
     const int32_t *of = p.counts + (size_t)b * p.E;
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) c[j] = lane + 32 * j < p.E ? __ldcg(of + lane + 32 * j) : 0;
+    for (int j = 0; j < kPerLane; ++j) c[j] = expert_of(lane, j) < p.E ? __ldcg(of + expert_of(lane, j)) : 0;
     const float n = (float)__ldcg(p.tokens + b);
     const TokenScores r = token_scores<SIGMOID>(v, p.E, lane);
     float dot = 0.0f;

@@ -159,9 +159,9 @@ cudaError_t launch_balance(const BalanceParams &p, int num_sms, cudaStream_t str
 
 // ------------------------------------------------ the routing's backward pass
 struct RouteGradParams {
-  CUtensorMap map_x;      // hidden [T][H], box {64, 32}, 128-byte swizzle (as the others)
+  CUtensorMap map_x;      // hidden [T][H], box {64, 64}, 128-byte swizzle (as the others)
   CUtensorMap map_dl_k;   // pieces of dl [3][T][Epad] bf16 (workspace), box {64, 128, 1}
-  CUtensorMap map_dl_mn;  // the same, box {64, 32, 1}
+  CUtensorMap map_dl_mn;  // the same, box {64, 64, 1}
   CUtensorMap map_w;      // pieces of the router weight [2][E][H] bf16 (workspace), box {64, 64, 1}
   uint16_t *pieces, *w_pieces;  // pieces: nullptr when only dl is wanted
   int Epad;                     // E rounded up to 64

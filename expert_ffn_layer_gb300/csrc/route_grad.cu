@@ -81,7 +81,7 @@ __device__ __forceinline__ void token_grad(const RouteGradParams &p, const Batch
   if (p.grad_losses != nullptr) {
     const int32_t *of = p.counts + (size_t)b * E;
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) c[j] = lane + 32 * j < E ? __ldg(of + lane + 32 * j) : 0;
+    for (int j = 0; j < kPerLane; ++j) c[j] = expert_of(lane, j) < E ? __ldg(of + expert_of(lane, j)) : 0;
     n = (float)max(__ldg(p.tokens + b), 1);
   }
   const TokenScores r = token_scores<SIGMOID>(v, E, lane);
@@ -103,11 +103,11 @@ __device__ __forceinline__ void token_grad(const RouteGradParams &p, const Batch
     float score = 0.0f, rest = 0.0f;  // of the slot's expert, from the lane that has it
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) {
-      const float a = __shfl_sync(0xffffffffu, SIGMOID ? r.s[j] : r.p[j], e & 31);
-      if (e >> 5 == j) score = a;
+      const float a = __shfl_sync(0xffffffffu, SIGMOID ? r.s[j] : r.p[j], lane_of(e));
+      if (slot_of(e) == j) score = a;
       if (SIGMOID) {
-        const float m = __shfl_sync(0xffffffffu, r.miss[j], e & 31);
-        if (e >> 5 == j) rest = m;
+        const float m = __shfl_sync(0xffffffffu, r.miss[j], lane_of(e));
+        if (slot_of(e) == j) rest = m;
       }
     }
     if (lane >= k) score = 0.0f;
@@ -126,7 +126,7 @@ __device__ __forceinline__ void token_grad(const RouteGradParams &p, const Batch
       const float wi = __shfl_sync(0xffffffffu, w, i);
 #pragma unroll
       for (int j = 0; j < kPerLane; ++j)
-        if (ei == lane + 32 * j) d[j] += wi;
+        if (ei == expert_of(lane, j)) d[j] += wi;
     }
     if (spread != 0.0f) {
 #pragma unroll
@@ -170,18 +170,19 @@ __global__ void __launch_bounds__(kThreads) grad_logits_kernel(const __grid_cons
     if (p.dl != nullptr) {
 #pragma unroll
       for (int j = 0; j < kPerLane; ++j)
-        if (lane + 32 * j < E) p.dl[(size_t)t * E + lane + 32 * j] = d[j];
+        if (expert_of(lane, j) < E) p.dl[(size_t)t * E + expert_of(lane, j)] = d[j];
     }
     if (p.pieces != nullptr) {
       const size_t plane = (size_t)p.T * p.Epad;
-      uint16_t *at = p.pieces + (size_t)t * p.Epad + lane;
+      uint16_t *row = p.pieces + (size_t)t * p.Epad + 2 * lane;
 #pragma unroll
-      for (int j = 0; j < kPerLane; ++j)
+      for (int j = 0; j < kPerLane; j += 2)
         if (32 * j < p.Epad) {  // zeros past the last expert
-          const Pieces x = pieces_of(d[j]);
-          at[32 * j] = (uint16_t)x.hi;
-          at[plane + 32 * j] = (uint16_t)x.mid;
-          at[2 * plane + 32 * j] = (uint16_t)x.lo;
+          const Pieces x = pieces_of(d[j]), y = pieces_of(d[j + 1]);
+          uint32_t *at = reinterpret_cast<uint32_t *>(row + 32 * j);
+          at[0] = x.hi | y.hi << 16;
+          at[plane / 2] = x.mid | y.mid << 16;
+          at[plane] = x.lo | y.lo << 16;
         }
     }
   }
@@ -208,8 +209,8 @@ __global__ void __launch_bounds__(kThreads) grad_few_kernel(const __grid_constan
     token_grad<SIGMOID>(p, bt, t, lane, d);
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) {
-      dl[t][lane + 32 * j] = d[j];
-      if (p.dl != nullptr && blockIdx.x == 0 && lane + 32 * j < E) p.dl[(size_t)t * E + lane + 32 * j] = d[j];
+      dl[t][expert_of(lane, j)] = d[j];
+      if (p.dl != nullptr && blockIdx.x == 0 && expert_of(lane, j) < E) p.dl[(size_t)t * E + expert_of(lane, j)] = d[j];
     }
   }
   __syncthreads();
@@ -259,21 +260,22 @@ __global__ void __launch_bounds__(kThreads) grad_few_kernel(const __grid_constan
 // grad_hidden, rounded to bf16 in the end, two pieces of dl and of W and three of
 // their four products (relative error of a product 2^-15 at most).
 //
-// grad_hidden: a CTA keeps the pieces of W's 128 columns (at most 128 KB) and walks
-// over token tiles of 128, whose pieces of dl come in a ring of 64-expert steps.
+// grad_hidden: a CTA keeps the pieces of W's 128 columns (at most 128 KB) as the M
+// operand and walks over 256 tokens at a time as the N one (128 tokens as M and 128
+// columns as N read shared memory faster than it answers: 79 us against 65 at 16384
+// tokens), their pieces of dl in a ring of 64-expert steps.
 // grad_router_w: a CTA has 128 columns of x and a part of the tokens, in steps of
-// 32; both operands lie with their row dimension inner (MN-major).  The tensor cores'
+// 64; both operands lie with their row dimension inner (MN-major).  The tensor cores'
 // fp32 sums are cut off, not rounded, at each step, which over thousands of tokens
 // would shrink the result (by 2.4e-6 of itself over 1024): two accumulators take 128
 // tokens in turn, and the epilogue warps add them up in registers.  The parts of one
 // tile are a cluster, which adds its fp32 tiles over shared memory in rank order.
 constexpr int kSmemMax = 232448;  // 227 KB opt-in per block
 constexpr int kBox = 64 * 128;    // 64 rows of 128 bytes
-constexpr int kProdThreads = 192;  // warp 0 TMA, 1 MMA, 2-5 epilogue (TMEM lane quarters 2,3,0,1)
-constexpr int kWThreads = 320;     // of grad_router_w: two epilogue warps per lane quarter
-constexpr int kStep = 32;          // tokens of a step of grad_router_w
-constexpr int kWBox = kStep * 128;  // its boxes: 32 rows of 128 bytes
-constexpr int kChunk = 4;          // steps before the accumulator changes
+constexpr int kProdThreads = 320;  // warp 0 TMA, 1 MMA, 2-9 epilogue (TMEM lane quarters 2,3,0,1, twice)
+constexpr int kStep = 64;          // tokens of a step of grad_router_w
+constexpr int kWBox = kStep * 128;  // its boxes: 64 rows of 128 bytes
+constexpr int kChunk = 2;          // steps before the accumulator changes
 constexpr int kMaxSplit = 8;
 
 // Shared-memory matrix descriptor of an operand with its row dimension (M or N)
@@ -304,12 +306,12 @@ __global__ void __launch_bounds__(kProdThreads, 1) grad_hidden_kernel(const __gr
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int eb = p.Epad >> 6, nst = p.hidden_stages;
-  const int b_piece = eb * 2 * kBox;  // one piece of W: eb steps of two 64-column boxes
-  uint8_t *ring = smem + 2 * b_piece;
-  constexpr int kStage = 4 * kBox;  // two pieces of 128 tokens x 64 experts
+  const int w_piece = eb * 2 * kBox;  // one piece of W: eb steps of two 64-column boxes
+  uint8_t *ring = smem + 2 * w_piece;
+  constexpr int kStage = 4 * kBox;  // one piece of dl: 256 tokens x 64 experts
   ProdShared *sh = (ProdShared *)(ring + nst * kStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h0 = blockIdx.x * 128, tiles = (p.T + 127) >> 7;
+  const int h0 = blockIdx.x * 128, tiles = (p.T + 255) >> 8;
   volatile int *abort_flag = &sh->abort;
   unsigned *err = p.err;
   if (threadIdx.x == 0) {
@@ -319,14 +321,14 @@ __global__ void __launch_bounds__(kProdThreads, 1) grad_hidden_kernel(const __gr
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&sh->afull[a]), 1);
-      mbar_init(smem_u32(&sh->aempty[a]), 4);
+      mbar_init(smem_u32(&sh->aempty[a]), 8);
     }
     mbar_init(smem_u32(&sh->bfull), 1);
     sh->abort = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&sh->tmem), 256);
+    tmem_alloc(smem_u32(&sh->tmem), 512);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -339,23 +341,25 @@ __global__ void __launch_bounds__(kProdThreads, 1) grad_hidden_kernel(const __gr
   if (warp == 0) {
     if (lane == 0) {
       const uint32_t bb = smem_u32(&sh->bfull);
-      mbar_arrive_expect_tx(bb, (uint32_t)(2 * b_piece));
+      mbar_arrive_expect_tx(bb, (uint32_t)(2 * w_piece));
       for (int pc = 0; pc < 2; ++pc)
         for (int e = 0; e < eb; ++e)
           for (int x = 0; x < 2; ++x)
-            tma_load_3d(smem_u32(smem + pc * b_piece + (2 * e + x) * kBox), &p.map_w, bb, h0 + 64 * x, 64 * e, pc);
+            tma_load_3d(smem_u32(smem + pc * w_piece + (2 * e + x) * kBox), &p.map_w, bb, h0 + 64 * x, 64 * e, pc);
       int i = 0;
-      for (int t = blockIdx.y; t < tiles && ok; t += gridDim.y)
-        for (int e = 0; e < eb && ok; ++e, ++i) {
+      for (int t = blockIdx.y; t < tiles && ok; t += gridDim.y) {
+        const bool both = p.T - 256 * t > 128;  // boxes of 128 tokens
+        for (int j = 0; j < 2 * eb; ++j, ++i) {  // step j: 64 experts j / 2, piece j % 2
           const int s = i % nst;
           ok = mbar_wait(smem_u32(&sh->empty[s]), ((uint32_t)(i / nst) & 1u) ^ 1u, err, abort_flag);
           if (!ok) break;
           const uint32_t fb = smem_u32(&sh->full[s]), st = smem_u32(ring + s * kStage);
-          mbar_arrive_expect_tx(fb, kStage);
-          tma_load_3d(st, &p.map_dl_k, fb, 64 * e, 128 * t, 0);
-          tma_load_3d(st + 2 * kBox, &p.map_dl_k, fb, 64 * e, 128 * t, 1);
+          mbar_arrive_expect_tx(fb, both ? kStage : kStage / 2);
+          tma_load_3d(st, &p.map_dl_k, fb, 32 * (j & ~1), 256 * t, j & 1);
+          if (both) tma_load_3d(st + 2 * kBox, &p.map_dl_k, fb, 32 * (j & ~1), 256 * t + 128, j & 1);
         }
-      if (!ok) {  // leave no copy in flight (each wait bounded, the first without consuming anything)
+      }
+      if (!ok) {  // leave no copy in flight
         mbar_wait(bb, 0, err, nullptr);
         for (int j = i - nst < 0 ? 0 : i - nst; j < i; ++j)
           mbar_wait(smem_u32(&sh->full[j % nst]), (uint32_t)(j / nst) & 1u, err, nullptr);
@@ -363,28 +367,26 @@ __global__ void __launch_bounds__(kProdThreads, 1) grad_hidden_kernel(const __gr
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16(128, 128) | kTransB;
       ok = mbar_wait(smem_u32(&sh->bfull), 0, err, abort_flag);
       int i = 0, na = 0;
       for (int t = blockIdx.y; t < tiles && ok; t += gridDim.y, ++na) {
-        const int acc = na & 1;
+        const int acc = na & 1, n = min(256, (p.T - 256 * t + 15) & ~15);
         ok = mbar_wait(smem_u32(&sh->aempty[acc]), ((uint32_t)(na >> 1) & 1u) ^ 1u, err, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t dst = tmem + 128u * acc;
-        for (int e = 0; e < eb; ++e, ++i) {
+        const uint32_t dst = tmem + 256u * acc, idesc = idesc_bf16(128, n) | kTransA;
+        for (int j = 0; j < 2 * eb; ++j, ++i) {
           const int s = i % nst;
           ok = mbar_wait(smem_u32(&sh->full[s]), (uint32_t)(i / nst) & 1u, err, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t st = smem_u32(ring + s * kStage), wb = smem_u32(smem + 2 * e * kBox);
-          const uint64_t a0 = sdesc_sw128(st), a1 = sdesc_sw128(st + 2 * kBox);
-          const uint64_t b0 = sdesc_mn(wb, kBox), b1 = sdesc_mn(wb + b_piece, kBox);
+          const uint32_t wb = smem_u32(smem + (j & ~1) * kBox);
+          const uint64_t bd = sdesc_sw128(smem_u32(ring + s * kStage));
+          const uint64_t a0 = sdesc_mn(wb, kBox), a1 = sdesc_mn(wb + w_piece, kBox);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {  // 16 experts: 32 bytes along dl's rows, 16 rows of W
-            umma_bf16(dst, a0 + 2 * kk, b0 + 128 * kk, idesc, (e > 0 || kk > 0) ? 1u : 0u);
-            umma_bf16(dst, a0 + 2 * kk, b1 + 128 * kk, idesc, 1u);
-            umma_bf16(dst, a1 + 2 * kk, b0 + 128 * kk, idesc, 1u);
+          for (int kk = 0; kk < 4; ++kk) {  // 16 experts: 16 rows of W, 32 bytes along dl's rows
+            umma_bf16(dst, a0 + 128 * kk, bd + 2 * kk, idesc, (j > 0 || kk > 0) ? 1u : 0u);
+            if (!(j & 1)) umma_bf16(dst, a1 + 128 * kk, bd + 2 * kk, idesc, 1u);
           }
           umma_commit(smem_u32(&sh->empty[s]));
         }
@@ -393,31 +395,36 @@ __global__ void __launch_bounds__(kProdThreads, 1) grad_hidden_kernel(const __gr
       }
     }
   } else {
-    const int q = warp & 3;
+    // TMEM lane: a column of W; its columns: tokens, 128 of the lane quarter's 256 to
+    // each of its two warps.  Four lanes swap four tokens' values, so that each
+    // stores four neighbouring columns of one token.
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int h = h0 + 32 * q + (lane & ~3), sub = lane & 3;
     int na = 0;
     for (int t = blockIdx.y; t < tiles && ok; t += gridDim.y, ++na) {
-      const int acc = na & 1, row = 128 * t + 32 * q + lane;
+      const int acc = na & 1, t0 = 256 * t + 128 * half;
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh->afull[acc]), (uint32_t)(na >> 1) & 1u, err, abort_flag));
       if (!ok) break;
       tc_fence_after();
-      const uint32_t base = tmem + 128u * acc + ((uint32_t)(32 * q) << 16);
-      __nv_bfloat16 *dst = p.grad_hidden + (size_t)row * p.H + h0;
+      const uint32_t base = tmem + 256u * acc + 128u * half + ((uint32_t)(32 * q) << 16);
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 32) {
+      for (int c = 0; c < 128 && t0 + c < p.T; c += 32) {
         float v[32];
         tmem_ld32(base + (uint32_t)c, v);
         tmem_wait_ld();
-        if (row < p.T && h0 + c < p.H) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            uint32_t o[4];
+        for (int j = 0; j < 32; j += 4) {
+          uint32_t w[2];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(v[j + 2 * u], v[j + 2 * u + 1]);
-              o[u] = *reinterpret_cast<const uint32_t *>(&b);
-            }
-            *reinterpret_cast<uint4 *>(dst + c + j) = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int u = 0; u < 2; ++u) {  // lanes l and l ^ 1: tokens j + 2 u and the next
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[j + 2 * u], v[j + 2 * u + 1]);
+            const uint32_t mine = *reinterpret_cast<const uint32_t *>(&b), other = __shfl_xor_sync(0xffffffffu, mine, 1);
+            w[u] = lane & 1 ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
           }
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 2 ? w[0] : w[1], 2);
+          const uint2 o = lane & 2 ? make_uint2(got, w[1]) : make_uint2(w[0], got);
+          const int tok = t0 + c + j + sub;
+          if (tok < p.T && h < p.H) *reinterpret_cast<uint2 *>(p.grad_hidden + (size_t)tok * p.H + h) = o;
         }
       }
       tc_fence_before();
@@ -430,11 +437,11 @@ __global__ void __launch_bounds__(kProdThreads, 1) grad_hidden_kernel(const __gr
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 512);
   }
 }
 
-__global__ void __launch_bounds__(kWThreads, 1) grad_router_w_kernel(const __grid_constant__ RouteGradParams p,
+__global__ void __launch_bounds__(kProdThreads, 1) grad_router_w_kernel(const __grid_constant__ RouteGradParams p,
                                                                      int waited) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -534,7 +541,7 @@ __global__ void __launch_bounds__(kWThreads, 1) grad_router_w_kernel(const __gri
     // padded tokens' rows of x are overwritten with zeros before they are multiplied
     // (their rows of dl are zero, which NaN times would not be): the first four warps
     const bool mask = masked && half == 0;
-    const int tid = threadIdx.x - 64, row = tid & (kStep - 1), piece = (tid / kStep) & 3;
+    const int tid = threadIdx.x - 64, row = tid & (kStep - 1), box = (tid / kStep) & 1;
     const int steps = k1 - k0, chunks = (steps + kChunk - 1) / kChunk;
     int cleared = 0;
     for (int n = 0; n < chunks && ok; ++n) {
@@ -548,9 +555,9 @@ __global__ void __launch_bounds__(kWThreads, 1) grad_router_w_kernel(const __gri
           ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh->full[s]), (uint32_t)(cleared / nst) & 1u, err, abort_flag));
           if (!ok) break;
           if (off) {
-            const uint32_t at = smem_u32(smem + s * stage + (piece >> 1) * kWBox + row * 128 + (piece & 1) * 64);
+            const uint32_t at = smem_u32(smem + s * stage + box * kWBox + row * 128);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) st_shared_v4(at + 16 * c, make_uint4(0u, 0u, 0u, 0u));
+            for (int c = 0; c < 8; ++c) st_shared_v4(at + 16 * c, make_uint4(0u, 0u, 0u, 0u));
             fence_proxy_async_smem();
           }
           __syncwarp();
@@ -601,7 +608,7 @@ __global__ void __launch_bounds__(kWThreads, 1) grad_router_w_kernel(const __gri
     cluster_sync();
     // rank r adds up experts r, r + split, ..: a warp a row of 128 columns
     const int col = 4 * lane;
-    for (int e = rank + split * warp; e < p.E; e += split * (kWThreads / 32)) {
+    for (int e = rank + split * warp; e < p.E; e += split * (kProdThreads / 32)) {
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
       float4 v[kMaxSplit];
 #pragma unroll
@@ -648,7 +655,7 @@ cudaError_t launch_route_grad(RouteGradParams p, int num_sms, cudaStream_t strea
   if (p.grad_hidden != nullptr) {
     const cudaError_t e0 = set_smem_attr_once((const void *)grad_hidden_kernel, kSmemMax, attr_h);
     if (e0 != cudaSuccess) return e0;
-    const int tiles = (p.T + 127) >> 7;
+    const int tiles = (p.T + 255) >> 8;
     int rows = num_sms / hb;  // CTAs that share the token tiles: one wave
     if (rows < 1) rows = 1;
     if (rows > tiles) rows = tiles;
@@ -672,7 +679,7 @@ cudaError_t launch_route_grad(RouteGradParams p, int num_sms, cudaStream_t strea
     if (p.w_smem < p.E * 512) p.w_smem = (p.E * 512 + 127) & ~127;  // the tile that the cluster adds up
     int waited = p.grad_hidden != nullptr;
     void *args[] = {(void *)&p, (void *)&waited};
-    return launch_ex((const void *)grad_router_w_kernel, dim3(split, hb), dim3(kWThreads), (size_t)p.w_smem + tail, stream,
+    return launch_ex((const void *)grad_router_w_kernel, dim3(split, hb), dim3(kProdThreads), (size_t)p.w_smem + tail, stream,
                      true, split, args);
   }
   return cudaSuccess;

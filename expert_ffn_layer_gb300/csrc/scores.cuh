@@ -1,5 +1,6 @@
-// What the router's losses and its backward pass need of one token's logits, held
-// by a warp: lane l has experts l, l + 32, .. (at most 256).
+// What the router's losses and its backward pass need of one token's logits, held by
+// a warp: lane l has experts 2 l, 2 l + 1, 64 + 2 l, .. (at most 256), so that two
+// neighbours' 16-bit values go out in one store.
 #pragma once
 #include <stdint.h>
 
@@ -8,6 +9,9 @@
 namespace moe {
 
 constexpr int kPerLane = 8;  // experts of a lane
+__device__ __forceinline__ int expert_of(int lane, int j) { return 64 * (j >> 1) + 2 * lane + (j & 1); }
+__device__ __forceinline__ int lane_of(int e) { return (e & 63) >> 1; }
+__device__ __forceinline__ int slot_of(int e) { return 2 * (e >> 6) + (e & 1); }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -72,7 +76,7 @@ struct TokenScores {
 };
 __device__ __forceinline__ void load_logits(const float *lg, int E, int lane, float (&v)[kPerLane]) {
 #pragma unroll
-  for (int j = 0; j < kPerLane; ++j) v[j] = lane + 32 * j < E ? __ldg(lg + lane + 32 * j) : -INFINITY;
+  for (int j = 0; j < kPerLane; ++j) v[j] = expert_of(lane, j) < E ? __ldg(lg + expert_of(lane, j)) : -INFINITY;
 }
 template <bool SIGMOID>
 __device__ __forceinline__ TokenScores token_scores(const float (&v)[kPerLane], int E, int lane) {
@@ -85,7 +89,7 @@ __device__ __forceinline__ TokenScores token_scores(const float (&v)[kPerLane], 
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) {
-      r.p[j] = lane + 32 * j < E ? expf(v[j] - mx) : 0.0f;
+      r.p[j] = expert_of(lane, j) < E ? expf(v[j] - mx) : 0.0f;
       sum += r.p[j];
     }
     sum = warp_sum(sum);
@@ -98,7 +102,7 @@ __device__ __forceinline__ TokenScores token_scores(const float (&v)[kPerLane], 
   if (SIGMOID) {
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) {
-      const bool on = lane + 32 * j < E;
+      const bool on = expert_of(lane, j) < E;
       r.s[j] = on ? 1.0f / (1.0f + expf(-v[j])) : 0.0f;
       r.miss[j] = on ? 1.0f / (1.0f + expf(v[j])) : 0.0f;
       r.total += r.s[j];
