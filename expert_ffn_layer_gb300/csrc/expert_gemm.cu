@@ -118,8 +118,11 @@ __host__ __device__ constexpr bool requantizes(int mode) { return mode == kModeF
 template <int BN, int MODE>
 struct Rings {
   static constexpr bool CV = converts(MODE);
-  static constexpr int kW = CV ? 3 : BN >= 256 ? 3 : BN >= 240 ? 4 : BN >= 128 ? 5 : 6;
-  static constexpr int kQ = CV ? (BN >= 240 ? 2 : BN >= 128 ? 4 : 6) : 0;  // MXFP4: two K steps each
+  // int8 at 240 tokens: with two code slots (and three weight slots) the SM waits for
+  // HBM most of the time
+  static constexpr bool kI8Wide = MODE == kModeI8 && BN >= 240;
+  static constexpr int kW = kI8Wide ? 2 : CV ? 3 : BN >= 256 ? 3 : BN >= 240 ? 4 : BN >= 128 ? 5 : 6;
+  static constexpr int kQ = kI8Wide ? 4 : CV ? (BN >= 240 ? 2 : BN >= 128 ? 4 : 6) : 0;  // MXFP4: two K steps each
   static constexpr int kT = BN >= 64 ? 3 : 4;
 };
 
@@ -149,7 +152,8 @@ struct Layout {
   static constexpr int kCstOff = kSegOffOff + 4 * kMaxSeg;    // routed chunk prefix [E + 1]
   static constexpr int kRunStartOff = kCstOff + 4 * kMaxSeg;  // first tile of each run [runs + 1]
   static constexpr int kRunDescOff = kRunStartOff + 4 * (kMaxRuns + 1);
-  static constexpr int kBytes = kRunDescOff + 4 * kMaxRuns;
+  static constexpr int kRowsOff = (kRunDescOff + 4 * kMaxRuns + 15) & ~15;  // int8: a quantisation tile's row factors
+  static constexpr int kBytes = kRowsOff + (MODE == kModeI8 ? 8 * BN : 0);
   static constexpr size_t kSmem = 1024 + kBytes;
   // accumulator pairs of 2 x BN columns: two while they fit in 512 columns, else one
   static constexpr int kAccBufs = 4 * BN <= 512 ? 2 : 1;
@@ -565,14 +569,14 @@ __device__ __forceinline__ uint4 e2m1x8_to_bf16(uint32_t w, float s) {
 // gate/up epilogue kept; the quotients as the row quantiser forms them.  The
 // 128 loader threads: rows rbase + 16 j, the 8 threads of a row taking its
 // 16-value pieces c8, c8 + 8, ...  Activations and maxima were written by other
-// CTAs: read through L2.  int8: the codes take the activations' own place, as fp16.
-template <int BN, int MODE>
+// CTAs: read through L2.
+template <int BN>
 __device__ __forceinline__ void quantize_chunk_rows(const GemmParams &p, const Tile &tl, int rbase, int c8) {
   const int ld = tl.shared ? p.Is : p.I, nb = ld >> 5, npc = ld >> 4;
   const bool split = quant_blocks<BN>(p, ld) > 1;  // this tile covers 256 columns (16 pieces) of each row
   const int pc0 = split ? tl.rb * 16 : 0, pc1 = split ? min(pc0 + 16, npc) : npc;
   const float *am = tl.shared ? p.amax_s : p.amax;
-  __nv_bfloat16 *act = tl.shared ? p.act_s : p.act;
+  const __nv_bfloat16 *act = tl.shared ? p.act_s : p.act;
   uint8_t *codes = tl.shared ? p.aq_s : p.aq;
   float *scales = tl.shared ? p.asc_s : p.asc;
 #pragma unroll 1
@@ -583,25 +587,6 @@ __device__ __forceinline__ void quantize_chunk_rows(const GemmParams &p, const T
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
     if (row >= tl.ntok) continue;
-    if constexpr (MODE == kModeI8) {
-      const Int8Row rq = int8_row(m);
-      if (c8 == 0 && pc0 == 0) scales[tl.row0 + row] = rq.scale;
-      uint4 *at = reinterpret_cast<uint4 *>(act + (size_t)(tl.row0 + row) * ld);
-      for (int pc = pc0 + c8; pc < pc1; pc += 8) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 v = __ldcg(at + 2 * pc + h);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            o[e] = int8_f16x2(int8_round(__uint_as_float(w[e] << 16), rq),
-                              int8_round(__uint_as_float(w[e] & 0xFFFF0000u), rq));
-          at[2 * pc + h] = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-      }
-      continue;
-    }
     const float sc = e4m3_row_scale(m), rs = __frcp_rn(sc);
     if (c8 == 0 && pc0 == 0) scales[tl.row0 + row] = sc;
     const uint4 *src = reinterpret_cast<const uint4 *>(act + (size_t)(tl.row0 + row) * ld);
@@ -617,6 +602,71 @@ __device__ __forceinline__ void quantize_chunk_rows(const GemmParams &p, const T
       }
       dst[pc] = make_uint4(e4m3_pack4(f[0], f[1], f[2], f[3]), e4m3_pack4(f[4], f[5], f[6], f[7]),
                            e4m3_pack4(f[8], f[9], f[10], f[11]), e4m3_pack4(f[12], f[13], f[14], f[15]));
+    }
+  }
+}
+
+// The same for int8: codes as fp16 values in the activations' own place.  The rows'
+// scales first (into `rows` in shared memory, several rows' maxima in flight), then
+// the tile's values as one run of 16-byte pieces, five in flight a thread: the tile
+// is otherwise a chain of L2 latencies, two for each of its rows.
+template <int BN>
+__device__ __forceinline__ void quantize_chunk_int8(const GemmParams &p, const Tile &tl, int tid, float2 *rows) {
+  const int ld = tl.shared ? p.Is : p.I, nb = ld >> 5, rbase = tid >> 3, c8 = tid & 7;
+  const bool split = quant_blocks<BN>(p, ld) > 1;  // this tile covers 256 columns of each row
+  const int col0 = split ? tl.rb * 256 : 0, cols = split ? min(256, ld - col0) : ld, npc = cols >> 3;
+  const float *am = (tl.shared ? p.amax_s : p.amax) + (size_t)tl.row0 * nb;
+  float *scales = (tl.shared ? p.asc_s : p.asc) + tl.row0;
+  uint4 *act = reinterpret_cast<uint4 *>((tl.shared ? p.act_s : p.act) + (size_t)tl.row0 * ld + col0);
+  constexpr int kRows = 4;  // in flight
+#pragma unroll 1
+  for (int j = 0; j < tl.ntok; j += 16 * kRows) {
+    float m[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int row = j + 16 * u + rbase;
+      m[u] = row < tl.ntok ? strided_max(am + (size_t)row * nb, c8, 8, nb) : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int row = j + 16 * u + rbase;
+      float v = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], 1));
+      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+      if (c8 == 0 && row < tl.ntok) {
+        const Int8Row q = int8_row(v);
+        rows[row] = make_float2(q.pre, q.mul);
+        if (col0 == 0) scales[row] = q.scale;
+      }
+    }
+  }
+  named_bar_sync(3, kTokThreads);
+  constexpr int kPieces = 5;  // in flight
+  const int n = tl.ntok * npc;
+#pragma unroll 1
+  for (int i = tid; i < n; i += kTokThreads * kPieces) {
+    uint4 v[kPieces];
+    int row[kPieces];
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int k = i + u * kTokThreads;
+      row[u] = k / npc;
+      if (k < n) v[u] = __ldcg(act + (size_t)row[u] * (ld >> 3) + (k - row[u] * npc));
+    }
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int k = i + u * kTokThreads;
+      if (k >= n) break;
+      Int8Row q;
+      const float2 f = rows[row[u]];
+      q.pre = f.x;
+      q.mul = f.y;
+      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        o[e] = int8_f16x2(int8_round(__uint_as_float(w[e] << 16), q), int8_round(__uint_as_float(w[e] & 0xFFFF0000u), q));
+      act[(size_t)row[u] * (ld >> 3) + (k - row[u] * npc)] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -887,7 +937,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
           // quantisation tile: every loader thread reads activations and
           // their row maxima itself, after thread 0's acquire of the count
           named_bar_sync(3, kTokThreads);
-          quantize_chunk_rows<BN, MODE>(p, tl, rbase, c8);
+          if constexpr (I8) quantize_chunk_int8<BN>(p, tl, tid, reinterpret_cast<float2 *>(smem + L::kRowsOff));
+          else quantize_chunk_rows<BN>(p, tl, rbase, c8);
           __threadfence();  // the codes and scales, before the count (release)
           named_bar_sync(3, kTokThreads);
           if (tid == 0) atomicAdd(done2 + tl.seg, 1u);
@@ -1355,7 +1406,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
     // step (j - 2) needed MMA j - 5 done, which orders the slot's earlier phase
     // (MMA j - 6) before its wait; with an even number of code slots, step
     // j - KQ belonged to the same group.
-    static_assert(!(Q8 || I8) || (KQ % 2 == 0 && KW == 3), "two converter groups need an even code ring and three weight slots");
+    // With two weight slots each group has a slot of its own.
+    static_assert(!(Q8 || I8) || (KQ % 2 == 0 && (KW == 3 || KW == 2)), "two converter groups need an even code ring");
     const int cw = warp - (kEpiWarp0 + EW);
     const int grp = cw >> 2, wg = cw & 3;
     const int box = wg >> 1, c = lane & 3;
