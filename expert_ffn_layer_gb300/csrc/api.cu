@@ -125,19 +125,21 @@ bool map_bf16_2d(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, 
   const uint32_t box[2] = {64, box_rows};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
-// E4M3 codes [rows][cols] (uint8), box {64 codes, box_rows}, no swizzle
-bool map_u8_2d(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, uint32_t box_rows) {
+// E4M3 codes [rows][cols] (uint8), box {64 codes, box_rows}, no swizzle unless given
+bool map_u8_2d(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, uint32_t box_rows,
+               CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_NONE) {
   const uint64_t dims[2] = {cols, rows};
   const uint64_t str[1] = {cols};
   const uint32_t box[2] = {64, box_rows};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, ptr, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, ptr, dims, str, box, swz);
 }
-// stacked E4M3 codes [n][rows][cols], box {64, box_rows, 1}, no swizzle
-bool map_u8_3d(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, uint64_t n, uint32_t box_rows) {
+// stacked E4M3 codes [n][rows][cols], box {64, box_rows, 1}, no swizzle unless given
+bool map_u8_3d(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, uint64_t n, uint32_t box_rows,
+               CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_NONE) {
   const uint64_t dims[3] = {cols, rows, n};
   const uint64_t str[2] = {cols, cols * rows};
   const uint32_t box[3] = {64, box_rows, 1};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, ptr, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, ptr, dims, str, box, swz);
 }
 // E4M3 codes for the W8A8 kernel: boxes of 128 codes x box_rows, 128-byte
 // swizzle (one 128-byte K-step row per matrix row, as the bf16 maps)
@@ -529,6 +531,7 @@ moe_status do_expert_phases(const moe_dims &d, int phases, const moe_bf16 *hidde
   }
   if (i8 != nullptr) {  // int8: maps of the codes, and the row scales; the token codes in the place of hidden
     g.mode = 4;
+    g.late_tokens = !g.early;  // behind launch_quantize_int8
     g.hidden = sc.hx;
     g.sc_g = i8->gate_scale;
     g.sc_u = i8->up_scale;
@@ -541,11 +544,13 @@ moe_status do_expert_phases(const moe_dims &d, int phases, const moe_bf16 *hidde
     g.amax_s = sc.amax_s;
     g.asc = sc.asc;
     g.asc_s = sc.asc_s;
-    ok = map_u8_3d(&g.map_wg, i8->gate, d.H, d.I, d.E, 128) && map_u8_3d(&g.map_wu, i8->up, d.H, d.I, d.E, 128) &&
-         map_u8_3d(&g.map_wd, i8->down, d.I, d.H, d.E, 128);
+    // tiles whose converters read a row a lane
+    const CUtensorMapSwizzle swz = int8_in_tmem(bn) ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE;
+    ok = map_u8_3d(&g.map_wg, i8->gate, d.H, d.I, d.E, 128, swz) && map_u8_3d(&g.map_wu, i8->up, d.H, d.I, d.E, 128, swz) &&
+         map_u8_3d(&g.map_wd, i8->down, d.I, d.H, d.E, 128, swz);
     if (d.has_shared)
-      ok = ok && map_u8_2d(&g.map_sg, i8->s_gate, d.H, g.Is, 128) && map_u8_2d(&g.map_su, i8->s_up, d.H, g.Is, 128) &&
-           map_u8_2d(&g.map_sd, i8->s_down, g.Is, d.H, 128);
+      ok = ok && map_u8_2d(&g.map_sg, i8->s_gate, d.H, g.Is, 128, swz) &&
+           map_u8_2d(&g.map_su, i8->s_up, d.H, g.Is, 128, swz) && map_u8_2d(&g.map_sd, i8->s_down, g.Is, d.H, 128, swz);
     for (int b = 0; b < 4; ++b) ok = ok && map_bf16_2d(&g.map_act[b], g.act, d.I, g.S, 16u << b);
     if (d.has_shared)
       for (int b = 0; b < 4; ++b) ok = ok && map_bf16_2d(&g.map_acts[b], g.act_s, g.Is, d.T, 16u << b);

@@ -118,11 +118,16 @@ __host__ __device__ constexpr bool requantizes(int mode) { return mode == kModeF
 template <int BN, int MODE>
 struct Rings {
   static constexpr bool CV = converts(MODE);
+  // int8, tiles of at most 64 tokens: the converters' fp16 weights go to TMEM, which
+  // has room beside two accumulators, and the MMAs take them from there.  Through
+  // shared memory a K step's 16 KB of codes move 96 KB, of which its 128 bytes a
+  // cycle leave less than HBM's rate; this way 32 KB.
+  static constexpr bool kTA = MODE == kModeI8 && int8_in_tmem(BN);
   // int8 at 240 tokens: with two code slots (and three weight slots) the SM waits for
   // HBM most of the time
   static constexpr bool kI8Wide = MODE == kModeI8 && BN >= 240;
-  static constexpr int kW = kI8Wide ? 2 : CV ? 3 : BN >= 256 ? 3 : BN >= 240 ? 4 : BN >= 128 ? 5 : 6;
-  static constexpr int kQ = kI8Wide ? 4 : CV ? (BN >= 240 ? 2 : BN >= 128 ? 4 : 6) : 0;  // MXFP4: two K steps each
+  static constexpr int kW = kTA ? (BN <= 32 ? 6 : 4) : kI8Wide ? 2 : CV ? 3 : BN >= 256 ? 3 : BN >= 240 ? 4 : BN >= 128 ? 5 : 6;
+  static constexpr int kQ = kTA ? 10 : kI8Wide ? 4 : CV ? (BN >= 240 ? 2 : BN >= 128 ? 4 : 6) : 0;  // MXFP4: two K steps each
   static constexpr int kT = BN >= 64 ? 3 : 4;
 };
 
@@ -134,7 +139,8 @@ struct Layout {
   static constexpr int kT = Rings<BN, MODE>::kT;
   static constexpr int kEpiW = CV ? kEpiWarps - kCvtWarps : kEpiWarps;  // epilogue warps
   static constexpr int kTokBytes = BN * 128;
-  static constexpr int kQOff = kW * kABytes;
+  static constexpr bool kTA = Rings<BN, MODE>::kTA;
+  static constexpr int kQOff = kTA ? 0 : kW * kABytes;
   static constexpr int kTOff = kQOff + kQ * kQBytes;
   // wide tiles stage each epilogue warp's 32-row x 16-token block in shared
   // memory and store whole 16-byte pieces of token rows (1 KB per warp)
@@ -152,12 +158,12 @@ struct Layout {
   static constexpr int kCstOff = kSegOffOff + 4 * kMaxSeg;    // routed chunk prefix [E + 1]
   static constexpr int kRunStartOff = kCstOff + 4 * kMaxSeg;  // first tile of each run [runs + 1]
   static constexpr int kRunDescOff = kRunStartOff + 4 * (kMaxRuns + 1);
-  static constexpr int kRowsOff = (kRunDescOff + 4 * kMaxRuns + 15) & ~15;  // int8: a quantisation tile's row factors
-  static constexpr int kBytes = kRowsOff + (MODE == kModeI8 ? 8 * BN : 0);
+  static constexpr int kBytes = kRunDescOff + 4 * kMaxRuns;
   static constexpr size_t kSmem = 1024 + kBytes;
   // accumulator pairs of 2 x BN columns: two while they fit in 512 columns, else one
   static constexpr int kAccBufs = 4 * BN <= 512 ? 2 : 1;
-  static constexpr uint32_t kTmemUsed = kAccBufs * 2 * BN;
+  static constexpr uint32_t kTmemA = kAccBufs * 2 * BN;  // first column of the weight slots, 64 columns each
+  static constexpr uint32_t kTmemUsed = kTmemA + (kTA ? kW * 64 : 0);
   // TMEM is allocated in powers of two columns
   static constexpr uint32_t kTmemCols = kTmemUsed <= 32 ? 32 : kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128
                                         : kTmemUsed <= 256 ? 256 : 512;
@@ -606,69 +612,81 @@ __device__ __forceinline__ void quantize_chunk_rows(const GemmParams &p, const T
   }
 }
 
-// The same for int8: codes as fp16 values in the activations' own place.  The rows'
-// scales first (into `rows` in shared memory, several rows' maxima in flight), then
-// the tile's values as one run of 16-byte pieces, five in flight a thread: the tile
-// is otherwise a chain of L2 latencies, two for each of its rows.
+// The same for int8: codes as fp16 values in the activations' own place.  The loader
+// and the converter warps (which have nothing else to do in such a tile) take four
+// rows at a time, eight lanes a row, each warp on its own: with the loaders alone
+// these tiles, chains of L2 latencies, took 190 of 1565 us at Hy3 T = 4096.
+// Not inlined: its registers beside the other roles' would spill in their loops
+// (gate/up at T = 512 625 -> 746 us).
+constexpr int kQuantWarps = 4 + kCvtWarps;
+__device__ __noinline__ void quantize_rows_int8(__nv_bfloat16 *act, const float *am, float *scales, int ld, int pc0,
+                                                int pc1, int ntok, int w) {
+  const int lane = threadIdx.x & 31, c8 = lane & 7, nb = ld >> 5;
+  constexpr int kPieces = 6;  // in flight
+#pragma unroll 1
+  for (int r0 = 4 * w; r0 < ntok; r0 += 4 * kQuantWarps) {
+    const int row = r0 + (lane >> 3);
+    const bool on = row < ntok;
+    float m = on ? strided_max(am + (size_t)row * nb, c8, 8, nb) : 0.0f;
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+    if (!on) continue;
+    const Int8Row q = int8_row(m);
+    if (c8 == 0 && pc0 == 0) scales[row] = q.scale;
+    uint4 *at = reinterpret_cast<uint4 *>(act + (size_t)row * ld);
+#pragma unroll 1
+    for (int pc = pc0 + c8; pc < pc1; pc += 8 * kPieces) {
+      uint4 v[kPieces];
+#pragma unroll
+      for (int u = 0; u < kPieces; ++u)
+        if (pc + 8 * u < pc1) v[u] = __ldcg(at + pc + 8 * u);
+#pragma unroll
+      for (int u = 0; u < kPieces; ++u)
+        if (pc + 8 * u < pc1) {
+          const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            o[e] = int8_f16x2(int8_round(__uint_as_float(x[e] << 16), q), int8_round(__uint_as_float(x[e] & 0xFFFF0000u), q));
+          at[pc + 8 * u] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+  }
+}
+
+// A warp's share of an int8 quantisation tile: after every gate/up tile of the
+// segment (a bounded wait), and counted when it is written.  False: given up.
 template <int BN>
-__device__ __forceinline__ void quantize_chunk_int8(const GemmParams &p, const Tile &tl, int tid, float2 *rows) {
-  const int ld = tl.shared ? p.Is : p.I, nb = ld >> 5, rbase = tid >> 3, c8 = tid & 7;
-  const bool split = quant_blocks<BN>(p, ld) > 1;  // this tile covers 256 columns of each row
-  const int col0 = split ? tl.rb * 256 : 0, cols = split ? min(256, ld - col0) : ld, npc = cols >> 3;
-  const float *am = (tl.shared ? p.amax_s : p.amax) + (size_t)tl.row0 * nb;
-  float *scales = (tl.shared ? p.asc_s : p.asc) + tl.row0;
-  uint4 *act = reinterpret_cast<uint4 *>((tl.shared ? p.act_s : p.act) + (size_t)tl.row0 * ld + col0);
-  constexpr int kRows = 4;  // in flight
-#pragma unroll 1
-  for (int j = 0; j < tl.ntok; j += 16 * kRows) {
-    float m[kRows];
-#pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int row = j + 16 * u + rbase;
-      m[u] = row < tl.ntok ? strided_max(am + (size_t)row * nb, c8, 8, nb) : 0.0f;
-    }
-#pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int row = j + 16 * u + rbase;
-      float v = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], 1));
-      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-      if (c8 == 0 && row < tl.ntok) {
-        const Int8Row q = int8_row(v);
-        rows[row] = make_float2(q.pre, q.mul);
-        if (col0 == 0) scales[row] = q.scale;
+__device__ __forceinline__ bool quant_tile_int8(const GemmParams &p, const Tile &tl, const unsigned *done, unsigned need,
+                                                unsigned *count, int w, int lane, unsigned *err, volatile int *abort_flag) {
+  bool ok = true;
+  if (lane == 0) {
+    const unsigned long long t0 = globaltimer();
+    while (ld_acquire_gpu(done) < need) {
+      if (*abort_flag || globaltimer() - t0 > kWaitLimitNs) {
+        if (!*abort_flag && err != nullptr) atomicOr(err, MOE_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+        ok = false;
+        break;
       }
+      __nanosleep(64);
     }
   }
-  named_bar_sync(3, kTokThreads);
-  constexpr int kPieces = 5;  // in flight
-  const int n = tl.ntok * npc;
-#pragma unroll 1
-  for (int i = tid; i < n; i += kTokThreads * kPieces) {
-    uint4 v[kPieces];
-    int row[kPieces];
-#pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      const int k = i + u * kTokThreads;
-      row[u] = k / npc;
-      if (k < n) v[u] = __ldcg(act + (size_t)row[u] * (ld >> 3) + (k - row[u] * npc));
-    }
-#pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      const int k = i + u * kTokThreads;
-      if (k >= n) break;
-      Int8Row q;
-      const float2 f = rows[row[u]];
-      q.pre = f.x;
-      q.mul = f.y;
-      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-      uint32_t o[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        o[e] = int8_f16x2(int8_round(__uint_as_float(w[e] << 16), q), int8_round(__uint_as_float(w[e] & 0xFFFF0000u), q));
-      act[(size_t)row[u] * (ld >> 3) + (k - row[u] * npc)] = make_uint4(o[0], o[1], o[2], o[3]);
-    }
+  ok = __shfl_sync(0xffffffffu, ok, 0) != 0;
+  if (!ok) return false;
+  {
+    const int ld = tl.shared ? p.Is : p.I;
+    const bool split = quant_blocks<BN>(p, ld) > 1;  // the tile covers 256 columns of each row
+    const int pc0 = split ? tl.rb * 32 : 0, pc1 = split ? min(pc0 + 32, ld >> 3) : ld >> 3;
+    quantize_rows_int8((tl.shared ? p.act_s : p.act) + (size_t)tl.row0 * ld,
+                       (tl.shared ? p.amax_s : p.amax) + (size_t)tl.row0 * (ld >> 5),
+                       (tl.shared ? p.asc_s : p.asc) + tl.row0, ld, pc0, pc1, tl.ntok, w);
   }
+  __threadfence();  // the codes and scales, before the count (release)
+  __syncwarp();
+  if (lane == 0) atomicAdd(count, 1u);
+  return true;
 }
 
 }  // namespace
@@ -678,6 +696,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
   using L = Layout<BN, MODE>;
   constexpr bool Q8 = MODE == kModeQ8, F8 = MODE == kModeF8, Q4 = MODE == kModeQ4, I8 = MODE == kModeI8;
   constexpr bool CV = converts(MODE), RQ = requantizes(MODE);
+  constexpr bool TA = L::kTA;
   constexpr int KE = F8 ? 128 : 64;  // K elements per step: one 128-byte row of a weight or token box
   constexpr int KSH = F8 ? 7 : 6;
   constexpr int KW = L::kW, KT = L::kT, KQ = L::kQ, EW = L::kEpiW;
@@ -713,12 +732,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < KW; ++s) {
-      mbar_init(wfull_bar(s), CV ? kCvtWarps / 2 : 1);  // the weight loader's expect_tx arrival, or one converter group
+      // the weight loader's expect_tx arrival, or one converter group, or all converters
+      mbar_init(wfull_bar(s), TA ? kCvtWarps : CV ? kCvtWarps / 2 : 1);
       mbar_init(wempty_bar(s), 2);                  // both MMA issuers' commits
     }
     for (int s = 0; s < KQ; ++s) {
       mbar_init(qfull_bar(s), 1);           // the loader's expect_tx arrival
-      mbar_init(qempty_bar(s), Q4 ? kCvtWarps : kCvtWarps / 2);  // its converter groups done reading
+      mbar_init(qempty_bar(s), Q4 || TA ? kCvtWarps : kCvtWarps / 2);  // its converter groups done reading
     }
     for (int s = 0; s < KT; ++s) {
       mbar_init(tfull_bar(s), kTokThreads);  // one arrival per loader thread (cp.async, or the TMA expect_tx)
@@ -763,7 +783,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
   // hidden, the shared weights, the header's counters -- was complete before the
   // chain's second kernel could launch: its first one, the router's split or the
   // permutation with wait_first, waits before it triggers.)
-  if (!p.early) pdl_wait();
+  if (!p.early && !p.late_tokens) pdl_wait();
   const Sched q = make_sched<BN>(p);
   if (p.early && q.Rs > 0 && warp == kWWarp && lane == 0) {
     // The shared expert's weights into L2 while the routing still runs: none
@@ -897,6 +917,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
     uint32_t tph = 0;
     uint32_t issued = 0, issued_par = 0;  // per token slot: an activation TMA issued (thread 0)
     bool waited = !p.early;
+    if (p.late_tokens) pdl_wait();  // the token codes; all else was complete before the quantiser let this kernel start
     for (int i = 0; ok; ++i) {
       const int r = i % kRing;
       ok = __all_sync(0xffffffffu, mbar_wait(id_full(r), (uint32_t)(i / kRing) & 1u, err, abort_flag));
@@ -913,11 +934,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
 
       // ---- a down tile needs every gate/up tile of its segment -- with W8A8,
       // every quantisation tile of its segment, each of which needed those
+      if constexpr (I8) {
+        if (tl.phase == 2) {
+          const int nch = tl.shared ? q.nch_s : cst[tl.seg + 1] - cst[tl.seg];
+          ok = quant_tile_int8<BN>(p, tl, done1 + tl.seg, (unsigned)(nch * (tl.shared ? q.Rs : q.Rr)), done2 + tl.seg,
+                                   warp - kTokWarp0, lane, err, abort_flag);
+          continue;
+        }
+      }
       if (tl.phase >= 1 && (p.phases & 1) && tid == 0) {
         const int nch = tl.shared ? q.nch_s : cst[tl.seg + 1] - cst[tl.seg];
         const bool on_quant = RQ && tl.phase == 1;
         const unsigned *cnt = (on_quant ? done2 : done1) + tl.seg;
-        const int nq = quant_blocks<BN>(p, tl.shared ? p.Is : p.I);  // quantisation tiles per chunk
+        const int nq = quant_blocks<BN>(p, tl.shared ? p.Is : p.I) * (I8 ? kQuantWarps : 1);  // quantisation counts per chunk
         const unsigned need = (unsigned)(on_quant ? nch * nq : nch * (tl.shared ? q.Rs : q.Rr));
         if (ld_acquire_gpu(cnt) < need) {
           const unsigned long long t0 = globaltimer();
@@ -932,13 +961,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
         }
         fence_proxy_async_global();  // the activations were written by other CTAs' generic stores
       }
-      if constexpr (RQ) {
+      if constexpr (F8) {
         if (tl.phase == 2) {
           // quantisation tile: every loader thread reads activations and
           // their row maxima itself, after thread 0's acquire of the count
           named_bar_sync(3, kTokThreads);
-          if constexpr (I8) quantize_chunk_int8<BN>(p, tl, tid, reinterpret_cast<float2 *>(smem + L::kRowsOff));
-          else quantize_chunk_rows<BN>(p, tl, rbase, c8);
+          quantize_chunk_rows<BN>(p, tl, rbase, c8);
           __threadfence();  // the codes and scales, before the count (release)
           named_bar_sync(3, kTokThreads);
           if (tid == 0) atomicAdd(done2 + tl.seg, 1u);
@@ -949,7 +977,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
       // ---- token rows of this thread for a gate/up tile: rows rbase + 16 j, as
       // 16-byte pieces of 128-byte K-step rows (64 bf16 values, or with W8A8 the
       // 128 E4M3 codes of the token's quantised row)
-      const uint8_t *src[BN / 16];
+      // (int8 keeps the tokens' numbers, half the registers of their addresses)
+      const uint8_t *src[I8 ? 1 : BN / 16];
+      int token[I8 ? BN / 16 : 1];
       if (tl.phase == 0) {
         bool bad = false;
 #pragma unroll
@@ -969,7 +999,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
               }
             }
           }
-          src[j] = F8 ? p.hq + (size_t)tok * p.H + c8 * 16
+          if constexpr (I8) token[j] = tok;
+          else src[j] = F8 ? p.hq + (size_t)tok * p.H + c8 * 16
                       : reinterpret_cast<const uint8_t *>(p.hidden) + (size_t)tok * p.H * 2 + c8 * 16;
         }
         if (bad && err != nullptr) atomicOr(err, MOE_DEVERR_INDEX);
@@ -986,7 +1017,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
 #pragma unroll
           for (int j = 0; j < BN / 16; ++j) {
             const int row = rbase + 16 * j;
-            if (row < tl.N) cp_async_16(bs + row * 128 + ((c8 ^ (row & 7)) << 4), src[j] + kb * 128);
+            if (row < tl.N) {
+              const uint8_t *at;
+              if constexpr (I8)
+                at = reinterpret_cast<const uint8_t *>(p.hidden) + (size_t)token[j] * p.H * 2 + c8 * 16 + kb * 128;
+              else at = src[j] + kb * 128;
+              cp_async_16(bs + row * 128 + ((c8 ^ (row & 7)) << 4), at);
+            }
           }
           cp_async_arrive_noinc(tfull_bar(ts));
         } else if (tid == 0) {
@@ -1065,7 +1102,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const uint32_t accum = (kb > 0 || kk > 0) ? 1u : 0u;
-            if constexpr (F8) umma_f8(dh, ah + 2 * kk, bd + 2 * kk, idesc, accum);  // 32 codes of K per MMA
+            if constexpr (TA)
+              umma_f16_ta(dh, tmem + L::kTmemA + (uint32_t)(ws * 64 + half * 32 + kk * 8), bd + 2 * kk, idesc, accum);
+            else if constexpr (F8) umma_f8(dh, ah + 2 * kk, bd + 2 * kk, idesc, accum);  // 32 codes of K per MMA
             else umma_bf16(dh, ah + 2 * kk, bd + 2 * kk, idesc, accum);
           }
           any = true;
@@ -1100,6 +1139,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
     const int c_first = kEpiCols * ((warp - kEpiWarp0) >> 2);
     __nv_bfloat16 *stage = reinterpret_cast<__nv_bfloat16 *>(smem + L::kEpiOff + (warp - kEpiWarp0) * kEpiCols * 64);
     const int r = 32 * q + lane;  // weight row within the 128-row half
+    if (p.late_tokens) pdl_wait();  // the token scales
     int na = 0;  // tiles that used an accumulator (quantisation tiles do not)
     for (int i = 0; ok; ++i) {
       const int rs = i % kRing;
@@ -1248,7 +1288,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
                     m[j] = fabsf(__bfloat162float(b));
                   }
                 }
-                const int col = col_max16(m, lane);  // lane's column of the warp-wide maxima (in m[0])
+                int col;  // lane's column of the warp-wide maxima (in m[0])
+                if constexpr (I8) {
+                  uint32_t mine = 0;
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) {  // magnitudes order as their bits
+                    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m[j]));
+                    if (lane >> 1 == j) mine = top;
+                  }
+                  m[0] = __uint_as_float(mine);
+                  col = lane >> 1;
+                } else {
+                  col = col_max16(m, lane);
+                }
                 if ((lane & 1) == 0 && c16 + col < tl.ntok && tl.rb * 4 + q < (ld >> 5))
                   (tl.shared ? p.amax_s : p.amax)[(size_t)(tl.row0 + c16 + col) * (ld >> 5) + tl.rb * 4 + q] = m[0];
               } else if (ii < ld) {
@@ -1394,6 +1446,70 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
         }
       }
     }
+  } else if constexpr (TA) {
+    // ================= int8 weights to TMEM (warps 14..21): the first four take the
+    // first 128-row box, the others the second, each its lane quarter, a lane a row.
+    // A lane reads the 64 codes of its row (their 16-byte pieces swizzled by TMA so
+    // that eight lanes cover all banks), frees the code slot and writes 32 columns.
+    const int cw = warp - (kEpiWarp0 + EW), box = cw >> 2, row = 32 * (warp & 3) + lane;
+    const uint32_t lane_at = tmem + L::kTmemA + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(32 * box);
+    const uint8_t *code_at = smem + L::kQOff + box * (kQBytes / 2) + row * 64;
+    const int swz = (row >> 1) & 3;
+    int ws = 0, qs = 0;
+    uint32_t wph = 0, qph = 0;
+    for (int i = 0; ok; ++i) {
+      const int rs = i % kRing;
+      ok = __all_sync(0xffffffffu, mbar_wait(id_full(rs), (uint32_t)(i / kRing) & 1u, err, abort_flag));
+      if (!ok) break;
+      const int t = ring[rs];
+      const Tile tl = tiles[rs];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(id_empty(rs));
+      if (t < 0) break;
+      if (tl.phase == 2) {
+        const int nch = tl.shared ? q.nch_s : cst[tl.seg + 1] - cst[tl.seg];
+        ok = quant_tile_int8<BN>(p, tl, done1 + tl.seg, (unsigned)(nch * (tl.shared ? q.Rs : q.Rr)), done2 + tl.seg, 4 + cw,
+                                 lane, err, abort_flag);
+        continue;
+      }
+      for (int kb = 0; kb < tl.nk; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait(qfull_bar(qs), qph, err, abort_flag));
+        if (!ok) break;
+        uint4 v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          v[c] = *reinterpret_cast<const uint4 *>(code_at + qs * kQBytes + ((c ^ swz) << 4));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qempty_bar(qs));
+        ok = __all_sync(0xffffffffu, mbar_wait(wempty_bar(ws), wph ^ 1u, err, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+          uint32_t o[16];
+          const uint32_t x[8] = {v[c].x, v[c].y, v[c].z, v[c].w, v[c + 1].x, v[c + 1].y, v[c + 1].z, v[c + 1].w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint2 h = int8x4_to_f16(x[e]);
+            o[2 * e] = h.x;
+            o[2 * e + 1] = h.y;
+          }
+          tmem_st16(lane_at + (uint32_t)(ws * 64 + 8 * c), o);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(wfull_bar(ws));
+        if (++ws == KW) {
+          ws = 0;
+          wph ^= 1u;
+        }
+        if (++qs == KQ) {
+          qs = 0;
+          qph ^= 1u;
+        }
+      }
+    }
   } else if constexpr (Q8 || I8) {
     // ================= FP8 (int8) weights (warps 14..21): codes -> bf16 (fp16) weight
     // slots (the values of the codes; the epilogue applies each row's scale).
@@ -1431,6 +1547,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
       __syncwarp();
       if (lane == 0) mbar_arrive(id_empty(rs));
       if (t < 0) break;
+      if constexpr (I8) {
+        if (tl.phase == 2) {
+          const int nch = tl.shared ? q.nch_s : cst[tl.seg + 1] - cst[tl.seg];
+          ok = quant_tile_int8<BN>(p, tl, done1 + tl.seg, (unsigned)(nch * (tl.shared ? q.Rs : q.Rr)), done2 + tl.seg,
+                                   4 + cw, lane, err, abort_flag);
+          continue;
+        }
+      }
       for (int kb = 0; kb < tl.nk; ++kb, ++kstep) {
         if ((int)(kstep & 1u) == grp) {
           ok = __all_sync(0xffffffffu, mbar_wait(qfull_bar(qs), qph, err, abort_flag) &&

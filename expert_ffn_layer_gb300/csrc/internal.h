@@ -105,6 +105,10 @@ struct GemmParams {
   // kernel's results (perm, offsets) are awaited -- only when that kernel is
   // this library's permutation, in the layer chain
   int early;
+  // 1 (int8, not early): the kernel before is this library's quantiser of the hidden
+  // state, which waits for the work before it and then lets this one start: only the
+  // token rows and their scales are waited for
+  int late_tokens;
   int gu_order;  // gate/up claim order: 1 level-major (row block outermost), 0 segment-major
 };
 // word offsets into the workspace header (4 KiB, zero when the workspace is fresh;
@@ -115,6 +119,7 @@ constexpr int kSyncClaim = 64, kSyncExit = 65, kSyncPermute = 66,
               kSyncDone = 128,   // kSyncDone .. + 257: gate/up tiles finished, per segment
               kSyncQuant = 512;  // kSyncQuant .. + 257: W8A8 quantisation tiles finished, per segment
 constexpr int kWsHeaderBytes = 4096;
+constexpr bool int8_in_tmem(int bn) { return bn <= 64; }  // int8: tiles whose weights are multiplied from TMEM
 int gemm_tile_n(int T, int top_k, int E);  // widest token tile (multiple of 16, <= 256) for a batch
 cudaError_t launch_expert_ffn(const GemmParams &p, int bn, int num_ctas, cudaStream_t stream, bool pdl);
 
