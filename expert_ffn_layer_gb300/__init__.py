@@ -279,13 +279,14 @@ def moe_combine_backward(d: MoeDims, grad_out, y_sorted, inv_perm, topk_w, grad_
                          stream=None) -> None:
     """Gradients of moe_combine with respect to its weights (needs y_sorted) and to the
     experts' outputs (needs topk_w)."""
-    S = d.T * d.top_k
-    _check(grad_out, torch.bfloat16, (d.T, d.H), "grad_out")
-    _check(y_sorted, torch.bfloat16, (S, d.H), "y_sorted")
+    T, H, k = d.T, d.H, d.top_k
+    S = T * k
+    _check(grad_out, torch.bfloat16, (T, H), "grad_out")
+    _check(y_sorted, torch.bfloat16, (S, H), "y_sorted")
     _check(inv_perm, torch.int32, (S,), "inv_perm")
-    _check(topk_w, torch.float32, (d.T, d.top_k), "topk_w")
-    _check(grad_topk_w, torch.float32, (d.T, d.top_k), "grad_topk_w")
-    _check(grad_y_sorted, torch.bfloat16, (S, d.H), "grad_y_sorted")
+    _check(topk_w, torch.float32, (T, k), "topk_w")
+    _check(grad_topk_w, torch.float32, (T, k), "grad_topk_w")
+    _check(grad_y_sorted, torch.bfloat16, (S, H), "grad_y_sorted")
     _call("moe_combine_backward", ctypes.byref(d), _ptr(grad_out), _ptr(y_sorted), _ptr(inv_perm), _ptr(topk_w),
           _ptr(grad_topk_w), _ptr(grad_y_sorted), _stream(stream))
 
@@ -294,13 +295,13 @@ def moe_balance_loss(d: MoeDims, logits, topk_idx, counts, tokens, losses, ws, s
     """counts [n_seq, E] and tokens [n_seq] int32 of each sequence, losses [2] fp32 (the
     balance and the z loss; None: the counts alone).  seq_id [T] int32: each token's
     sequence, negative for padding; None: one sequence."""
-    n_seq = tokens.numel()
-    _check(logits, torch.float32, (d.T, d.E), "logits")
-    _check(topk_idx, torch.int32, (d.T, d.top_k), "topk_idx")
-    _check(counts, torch.int32, (n_seq, d.E), "counts")
+    n_seq, T, E = tokens.numel(), d.T, d.E
+    _check(logits, torch.float32, (T, E), "logits")
+    _check(topk_idx, torch.int32, (T, d.top_k), "topk_idx")
+    _check(counts, torch.int32, (n_seq, E), "counts")
     _check(tokens, torch.int32, (n_seq,), "tokens")
     _check(losses, torch.float32, (2,), "losses")
-    _check(seq_id, torch.int32, (d.T,), "seq_id")
+    _check(seq_id, torch.int32, (T,), "seq_id")
     _call("moe_balance_loss", ctypes.byref(d), _ptr(logits), _ptr(topk_idx), _ptr(seq_id), n_seq, _ptr(counts),
           _ptr(tokens), _ptr(losses), _ptr(ws), ws.numel(), _stream(stream))
 
@@ -319,18 +320,18 @@ def moe_route_backward(d: MoeDims, logits, topk_idx, ws, grad_w=None, grad_losse
         if seq_id is not None:
             raise ValueError("seq_id without tokens: n_seq is needed")
         n_seq = 1
-    _check(logits, torch.float32, (d.T, d.E), "logits")
-    _check(topk_idx, torch.int32, (d.T, d.top_k), "topk_idx")
-    _check(grad_w, torch.float32, (d.T, d.top_k), "grad_w")
-    _check(grad_losses, torch.float32, (2,), "grad_losses")
-    _check(counts, torch.int32, (n_seq, d.E), "counts")
-    _check(tokens, torch.int32, (n_seq,), "tokens")
-    _check(seq_id, torch.int32, (d.T,), "seq_id")
-    _check(hidden, torch.bfloat16, (d.T, d.H), "hidden")
-    _check(router_w, torch.float32, (d.E, d.H), "router_w")
-    _check(grad_logits, torch.float32, (d.T, d.E), "grad_logits")
-    _check(grad_hidden, torch.bfloat16, (d.T, d.H), "grad_hidden")
-    _check(grad_router_w, torch.float32, (d.E, d.H), "grad_router_w")
+    T, H, E, k = d.T, d.H, d.E, d.top_k
+    for t, dtype, shape, name in ((logits, torch.float32, (T, E), "logits"), (topk_idx, torch.int32, (T, k), "topk_idx"),
+                                  (grad_w, torch.float32, (T, k), "grad_w"),
+                                  (grad_losses, torch.float32, (2,), "grad_losses"),
+                                  (counts, torch.int32, (n_seq, E), "counts"), (tokens, torch.int32, (n_seq,), "tokens"),
+                                  (seq_id, torch.int32, (T,), "seq_id"), (hidden, torch.bfloat16, (T, H), "hidden"),
+                                  (router_w, torch.float32, (E, H), "router_w"),
+                                  (grad_logits, torch.float32, (T, E), "grad_logits"),
+                                  (grad_hidden, torch.bfloat16, (T, H), "grad_hidden"),
+                                  (grad_router_w, torch.float32, (E, H), "grad_router_w")):
+        if t is not None:
+            _check(t, dtype, shape, name)
     _call("moe_route_backward", ctypes.byref(d), _ptr(hidden), _ptr(router_w), _ptr(logits), _ptr(topk_idx),
           _ptr(grad_w), _ptr(seq_id), n_seq, _ptr(counts), _ptr(tokens), _ptr(grad_losses), _ptr(grad_logits),
           _ptr(grad_hidden), _ptr(grad_router_w), _ptr(ws), ws.numel(), _stream(stream))
