@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineParams p
 // fixed order.  HBM-bound: K slots' loads in flight together (8 for top-8 and fewer:
 // Hy3 T = 4096, 571 MB, 121 -> 94 us, one slot at a time against eight), then their stores.
 template <int K>
-__global__ void __launch_bounds__(kThreads) combine_grad_kernel(const CombineGradParams p) {
+__global__ void __launch_bounds__(kThreads, K <= 8 ? 3 : 1) combine_grad_kernel(const CombineGradParams p) {
   __shared__ float sums[kThreads / 32][K];
   pdl_wait();
   pdl_launch_dependents();

@@ -12,13 +12,15 @@ namespace moe {
 namespace {
 constexpr int kThreads = 256;  // eight rows (one per warp) per CTA step
 
-// Largest magnitude of eight bf16 values as integer bits, which order as the
-// values do with NaN above infinity.
+// Largest magnitudes of the even and of the odd of eight bf16 values, as 16-bit
+// integers, which order as the values do with NaN above infinity.
 __device__ __forceinline__ uint32_t top_bits(const uint4 &v, uint32_t m) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) m = max(m, max(u[j] << 16 & 0x7FFFFFFFu, u[j] & 0x7FFF0000u));
-  return m;
+  m = __vimax3_u16x2(m, v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu);
+  return __vimax3_u16x2(m, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu);
+}
+// The largest of a warp's, as an fp32 value.
+__device__ __forceinline__ float warp_top(uint32_t m) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16)) << 16);
 }
 }  // namespace
 
@@ -67,8 +69,7 @@ __global__ void __launch_bounds__(kThreads) int8_rows_kernel(const __nv_bfloat16
     } else {
       for (int i = lane; i < n8; i += 32) m = top_bits(row[i], m);
     }
-    m = __reduce_max_sync(0xffffffffu, m);
-    const Int8Row q = int8_row(__uint_as_float(m));
+    const Int8Row q = int8_row(warp_top(m));
     if (lane == 0) scales[r] = q.scale;
     if constexpr (V > 0) {
 #pragma unroll
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) int8_row_cta_kernel(const __nv_bfloa
 #pragma unroll
   for (int i = 0; i < V; ++i)
     if ((int)threadIdx.x + kThreads * i < n8) m = top_bits(v[i], m);
-  m = __reduce_max_sync(0xffffffffu, m);
+  m = __float_as_uint(warp_top(m));
   if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = m;
   __syncthreads();
 #pragma unroll
@@ -150,10 +151,12 @@ __global__ void __launch_bounds__(kThreads) int8_values_kernel(const int8_t *__r
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const uint32_t pair = w[2 * h + j / 2] >> (16 * (j & 1));
-              const __nv_bfloat162 b =
-                  __floats2bfloat162_rn((float)(int8_t)(pair & 0xFF) * s, (float)(int8_t)(pair >> 8 & 0xFF) * s);
-              o[j] = *reinterpret_cast<const uint32_t *>(&b);
+              // code + 128 as the low byte of 2^23 + code + 128
+              const uint32_t x = w[2 * h + j / 2] ^ 0x80808080u;
+              const float a = __uint_as_float(__byte_perm(x, 0x4B000000u, j & 1 ? 0x7442 : 0x7440)) - 8388736.0f;
+              const float b = __uint_as_float(__byte_perm(x, 0x4B000000u, j & 1 ? 0x7443 : 0x7441)) - 8388736.0f;
+              const __nv_bfloat162 p = __floats2bfloat162_rn(a * s, b * s);
+              o[j] = *reinterpret_cast<const uint32_t *>(&p);
             }
             __stcs(out + (size_t)(i0 + 32 * u + lane) * (W / 2) + h, make_uint4(o[0], o[1], o[2], o[3]));
           }

@@ -30,9 +30,10 @@ __device__ __forceinline__ Int8Row int8_row(float m) {
 // least v / (127 * 255) away from that, v being its magnitude: more than 2^-16 for
 // v >= 1/2.  The fused product (off by at most 127 * 2^-24 < 2^-17) is rounded to a
 // multiple of 2^-15 (by adding 384, where fp32's spacing is that), which restores
-// the half-way values and crosses none, and then to an integer.
+// the half-way values and crosses none, and then to an integer (384 comes off in the
+// same addition).
 __device__ __forceinline__ float int8_round(float x, const Int8Row &r) {
-  return __fadd_rn(__fadd_rn(__fmaf_rn(x * r.pre, r.mul, 384.0f), -384.0f), 12582912.0f);
+  return __fadd_rn(__fmaf_rn(x * r.pre, r.mul, 384.0f), 12582528.0f);
 }
 // Four codes from four int8_round() results, the first in the low byte.
 __device__ __forceinline__ uint32_t int8_pack4(float a, float b, float c, float d) {
