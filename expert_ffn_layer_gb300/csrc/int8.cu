@@ -1,8 +1,6 @@
 // 8-bit integer experts: the row quantiser that makes their weights, the way back
 // to bf16, and the quantiser of the hidden state that the expert kernel reads.
 // The rule is in int8.cuh.
-#include <type_traits>
-
 #include "int8.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -24,13 +22,27 @@ __device__ __forceinline__ float warp_top(uint32_t m) {
 }
 }  // namespace
 
-// One warp per row, 8 values (16 bytes) per lane and piece.  V > 0: rows of at most
-// 256 V values, read once and kept in registers (the row maximum is wanted first);
-// V = 0: longer rows, read twice, the second time from L1 or L2.  Bound by HBM: 64
-// stacked matrices of 1536 x 4096 (805 MB in, 403 out) take 196 us, 0.91 of the copy
-// bandwidth; reading each row twice, 250.
-// F16: the codes as fp16 values, the form in which the expert kernel multiplies them,
-// else bytes.
+// Codes of eight values, at piece `at`.  F16: as fp16 values, the form in which the
+// expert kernel multiplies them, else bytes.
+template <bool F16>
+__device__ __forceinline__ void put8(void *codes, long long at, const uint4 &v, const Int8Row &q) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = int8_round(__uint_as_float(u[j] << 16), q);
+    f[2 * j + 1] = int8_round(__uint_as_float(u[j] & 0xFFFF0000u), q);
+  }
+  if (F16)
+    reinterpret_cast<uint4 *>(codes)[at] = make_uint4(int8_f16x2(f[0], f[1]), int8_f16x2(f[2], f[3]),
+                                                      int8_f16x2(f[4], f[5]), int8_f16x2(f[6], f[7]));
+  else
+    reinterpret_cast<uint2 *>(codes)[at] =
+        make_uint2(int8_pack4(f[0], f[1], f[2], f[3]), int8_pack4(f[4], f[5], f[6], f[7]));
+}
+
+// A warp per row of at most 2048 values, which are read once and kept in registers
+// (the row's maximum is wanted first), or of any width, read twice (V = 0).
 template <bool F16, int V>
 __global__ void __launch_bounds__(kThreads) int8_rows_kernel(const __nv_bfloat16 *__restrict__ src,
                                                              void *__restrict__ codes, float *__restrict__ scales,
@@ -39,21 +51,6 @@ __global__ void __launch_bounds__(kThreads) int8_rows_kernel(const __nv_bfloat16
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int n8 = cols >> 3;
-  auto put = [&](long long at, const uint4 &v, const Int8Row &q) {
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-    float f[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[2 * j] = int8_round(__uint_as_float(u[j] << 16), q);
-      f[2 * j + 1] = int8_round(__uint_as_float(u[j] & 0xFFFF0000u), q);
-    }
-    if (F16)
-      reinterpret_cast<uint4 *>(codes)[at] = make_uint4(int8_f16x2(f[0], f[1]), int8_f16x2(f[2], f[3]),
-                                                        int8_f16x2(f[4], f[5]), int8_f16x2(f[6], f[7]));
-    else
-      reinterpret_cast<uint2 *>(codes)[at] =
-          make_uint2(int8_pack4(f[0], f[1], f[2], f[3]), int8_pack4(f[4], f[5], f[6], f[7]));
-  };
   for (long long r = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); r < rows;
        r += (long long)gridDim.x * (kThreads / 32)) {
     const uint4 *row = reinterpret_cast<const uint4 *>(src + r * cols);
@@ -61,11 +58,9 @@ __global__ void __launch_bounds__(kThreads) int8_rows_kernel(const __nv_bfloat16
     uint4 v[V > 0 ? V : 1];
     if constexpr (V > 0) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (lane + 32 * i < n8) v[i] = __ldcs(row + lane + 32 * i);
+      for (int i = 0; i < V; ++i) v[i] = lane + 32 * i < n8 ? __ldcs(row + lane + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (lane + 32 * i < n8) m = top_bits(v[i], m);
+      for (int i = 0; i < V; ++i) m = top_bits(v[i], m);
     } else {
       for (int i = lane; i < n8; i += 32) m = top_bits(row[i], m);
     }
@@ -74,92 +69,85 @@ __global__ void __launch_bounds__(kThreads) int8_rows_kernel(const __nv_bfloat16
     if constexpr (V > 0) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (lane + 32 * i < n8) put(r * n8 + lane + 32 * i, v[i], q);
+        if (lane + 32 * i < n8) put8<F16>(codes, r * n8 + lane + 32 * i, v[i], q);
     } else {
-      for (int i = lane; i < n8; i += 32) put(r * n8 + i, row[i], q);
+      for (int i = lane; i < n8; i += 32) put8<F16>(codes, r * n8 + i, row[i], q);
     }
   }
 }
 
-// A CTA per row of the hidden state, for batches that leave most of the device idle
-// with a warp a row.
-__global__ void __launch_bounds__(kThreads) int8_row_cta_kernel(const __nv_bfloat16 *__restrict__ src,
-                                                                uint4 *__restrict__ codes, float *__restrict__ scales,
-                                                                int cols) {
-  constexpr int V = 16384 / 8 / kThreads;  // pieces of a thread, the widest row
-  __shared__ uint32_t top[kThreads / 32];
+// Wider rows, up to 1024 V values: a CTA of four warps per row, again read once.
+constexpr int kWideThreads = 128;
+template <bool F16, int V>
+__global__ void __launch_bounds__(kWideThreads) int8_wide_rows_kernel(const __nv_bfloat16 *__restrict__ src,
+                                                                      void *__restrict__ codes,
+                                                                      float *__restrict__ scales, long long rows,
+                                                                      int cols) {
+  __shared__ float top[2][kWideThreads / 32];
   pdl_wait();
   pdl_launch_dependents();
-  const int n8 = cols >> 3;
-  const size_t r = blockIdx.x;
-  const uint4 *row = reinterpret_cast<const uint4 *>(src + r * cols);
-  uint4 v[V];
-  uint32_t m = 0;
+  const int n8 = cols >> 3, tid = threadIdx.x;
+  int par = 0;
+  for (long long r = blockIdx.x; r < rows; r += gridDim.x, par ^= 1) {
+    const uint4 *row = reinterpret_cast<const uint4 *>(src + r * cols);
+    uint4 v[V];
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if ((int)threadIdx.x + kThreads * i < n8) v[i] = row[threadIdx.x + kThreads * i];
+    for (int i = 0; i < V; ++i)
+      v[i] = tid + kWideThreads * i < n8 ? __ldcs(row + tid + kWideThreads * i) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if ((int)threadIdx.x + kThreads * i < n8) m = top_bits(v[i], m);
-  m = __float_as_uint(warp_top(m));
-  if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = m;
-  __syncthreads();
+    for (int i = 0; i < V; ++i) m = top_bits(v[i], m);
+    const float mine = warp_top(m);
+    if ((tid & 31) == 0) top[par][tid >> 5] = mine;
+    __syncthreads();  // one a row: the next row's maxima go to the other place
+    uint32_t t = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) m = max(m, top[w]);
-  const Int8Row q = int8_row(__uint_as_float(m));
-  if (threadIdx.x == 0) scales[r] = q.scale;
+    for (int w = 0; w < kWideThreads / 32; ++w) t = max(t, __float_as_uint(top[par][w]));  // NaN above all
+    const Int8Row q = int8_row(__uint_as_float(t));
+    if (tid == 0) scales[r] = q.scale;
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if ((int)threadIdx.x + kThreads * i < n8) {
-      const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      uint32_t o[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        o[j] = int8_f16x2(int8_round(__uint_as_float(u[j] << 16), q), int8_round(__uint_as_float(u[j] & 0xFFFF0000u), q));
-      codes[r * n8 + threadIdx.x + kThreads * i] = make_uint4(o[0], o[1], o[2], o[3]);
-    }
+    for (int i = 0; i < V; ++i)
+      if (tid + kWideThreads * i < n8) put8<F16>(codes, r * n8 + tid + kWideThreads * i, v[i], q);
+  }
 }
 
-// A warp per row: code * scale in fp32, rounded once to bf16.  16 codes (W = 4 words)
-// per lane step where the rows' width allows, else 8; four steps' loads in flight.
-template <int W>
+// A warp per row: code * scale in fp32, rounded to bf16.  Eight codes a lane and step,
+// so that a lane's values are one whole 16-byte store (sixteen, stored as two halves
+// of every other sector: 264 against 190 us for 403 M values); eight steps' loads in
+// flight.
 __global__ void __launch_bounds__(kThreads) int8_values_kernel(const int8_t *__restrict__ codes,
                                                                const float *__restrict__ scales,
                                                                __nv_bfloat16 *__restrict__ dst, long long rows,
                                                                int cols) {
   pdl_wait();
   pdl_launch_dependents();
+  constexpr int kSteps = 8;
   const int lane = threadIdx.x & 31;
-  const int n = cols / (4 * W);
-  using Vec = typename std::conditional<W == 4, uint4, uint2>::type;
+  const int n8 = cols >> 3;
   for (long long r = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); r < rows;
        r += (long long)gridDim.x * (kThreads / 32)) {
     const float s = __ldg(scales + r);
-    const Vec *row = reinterpret_cast<const Vec *>(codes) + r * n;
-    uint4 *out = reinterpret_cast<uint4 *>(dst) + r * n * (W / 2);
-    for (int i0 = 0; i0 < n; i0 += 128) {
-      Vec v[4];
+    const uint2 *row = reinterpret_cast<const uint2 *>(codes) + r * n8;
+    uint4 *out = reinterpret_cast<uint4 *>(dst) + r * n8;
+    for (int i0 = lane; i0 < n8; i0 += 32 * kSteps) {
+      uint2 v[kSteps];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i0 + 32 * u + lane < n) v[u] = __ldcs(row + i0 + 32 * u + lane);
+      for (int u = 0; u < kSteps; ++u)
+        if (i0 + 32 * u < n8) v[u] = __ldcs(row + i0 + 32 * u);
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i0 + 32 * u + lane < n) {
-          const uint32_t *w = reinterpret_cast<const uint32_t *>(&v[u]);
+      for (int u = 0; u < kSteps; ++u)
+        if (i0 + 32 * u < n8) {
+          uint32_t o[4];
 #pragma unroll
-          for (int h = 0; h < W / 2; ++h) {
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              // code + 128 as the low byte of 2^23 + code + 128
-              const uint32_t x = w[2 * h + j / 2] ^ 0x80808080u;
-              const float a = __uint_as_float(__byte_perm(x, 0x4B000000u, j & 1 ? 0x7442 : 0x7440)) - 8388736.0f;
-              const float b = __uint_as_float(__byte_perm(x, 0x4B000000u, j & 1 ? 0x7443 : 0x7441)) - 8388736.0f;
-              const __nv_bfloat162 p = __floats2bfloat162_rn(a * s, b * s);
-              o[j] = *reinterpret_cast<const uint32_t *>(&p);
-            }
-            __stcs(out + (size_t)(i0 + 32 * u + lane) * (W / 2) + h, make_uint4(o[0], o[1], o[2], o[3]));
+          for (int j = 0; j < 4; ++j) {
+            // code + 128 as the low byte of 2^23 + code + 128
+            const uint32_t x = (j < 2 ? v[u].x : v[u].y) ^ 0x80808080u;
+            const float a = __uint_as_float(__byte_perm(x, 0x4B000000u, j & 1 ? 0x7442 : 0x7440)) - 8388736.0f;
+            const float b = __uint_as_float(__byte_perm(x, 0x4B000000u, j & 1 ? 0x7443 : 0x7441)) - 8388736.0f;
+            const __nv_bfloat162 p = __floats2bfloat162_rn(a * s, b * s);
+            o[j] = *reinterpret_cast<const uint32_t *>(&p);
           }
+          __stcs(out + i0 + 32 * u, make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
   }
@@ -181,31 +169,30 @@ unsigned row_blocks(long long rows) {
   return (unsigned)(blocks < cap ? blocks : cap);
 }
 template <bool F16>
-const void *rows_kernel(int cols) {
-  if (cols <= 512) return (const void *)int8_rows_kernel<F16, 2>;
-  if (cols <= 1536) return (const void *)int8_rows_kernel<F16, 6>;
-  if (cols <= 4096) return (const void *)int8_rows_kernel<F16, 16>;
-  return (const void *)int8_rows_kernel<F16, 0>;
+cudaError_t launch_rows(const __nv_bfloat16 *src, void *codes, float *scales, long long rows, int cols, cudaStream_t stream) {
+  void *args[] = {(void *)&src, (void *)&codes, (void *)&scales, (void *)&rows, (void *)&cols};
+  if (cols > 2048 && cols <= 16384) {
+    const long long cap = 16LL * sms();
+    return launch_ex(cols <= 4096 ? (const void *)int8_wide_rows_kernel<F16, 4> : (const void *)int8_wide_rows_kernel<F16, 16>,
+                     dim3((unsigned)(rows < cap ? rows : cap)), dim3(kWideThreads), 0, stream, true, 1, args);
+  }
+  return launch_ex(cols <= 1024   ? (const void *)int8_rows_kernel<F16, 4>
+                   : cols <= 2048 ? (const void *)int8_rows_kernel<F16, 8>
+                                  : (const void *)int8_rows_kernel<F16, 0>,
+                   dim3(row_blocks(rows)), dim3(kThreads), 0, stream, true, 1, args);
 }
 }  // namespace
 
 cudaError_t launch_quantize_int8(const __nv_bfloat16 *src, void *codes, bool f16, float *scales, long long rows,
                                  int cols, cudaStream_t stream) {
-  if (f16 && cols <= 16384 && rows <= 2 * sms()) {
-    uint4 *out = static_cast<uint4 *>(codes);
-    void *args[] = {(void *)&src, (void *)&out, (void *)&scales, (void *)&cols};
-    return launch_ex((const void *)int8_row_cta_kernel, dim3((unsigned)rows), dim3(kThreads), 0, stream, true, 1, args);
-  }
-  void *args[] = {(void *)&src, (void *)&codes, (void *)&scales, (void *)&rows, (void *)&cols};
-  return launch_ex(f16 ? rows_kernel<true>(cols) : rows_kernel<false>(cols), dim3(row_blocks(rows)), dim3(kThreads), 0,
-                   stream, true, 1, args);
+  return f16 ? launch_rows<true>(src, codes, scales, rows, cols, stream)
+             : launch_rows<false>(src, codes, scales, rows, cols, stream);
 }
 
 cudaError_t launch_dequantize_int8(const int8_t *codes, const float *scales, __nv_bfloat16 *dst, long long rows,
                                    int cols, cudaStream_t stream) {
   void *args[] = {(void *)&codes, (void *)&scales, (void *)&dst, (void *)&rows, (void *)&cols};
-  return launch_ex(cols % 16 ? (const void *)int8_values_kernel<2> : (const void *)int8_values_kernel<4>,
-                   dim3(row_blocks(rows)), dim3(kThreads), 0, stream, true, 1, args);
+  return launch_ex((const void *)int8_values_kernel, dim3(row_blocks(rows)), dim3(kThreads), 0, stream, true, 1, args);
 }
 
 }  // namespace moe
