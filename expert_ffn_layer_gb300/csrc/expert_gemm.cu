@@ -138,6 +138,11 @@ struct Layout {
   static constexpr int kQ = Rings<BN, MODE>::kQ;
   static constexpr int kT = Rings<BN, MODE>::kT;
   static constexpr int kEpiW = CV ? kEpiWarps - kCvtWarps : kEpiWarps;  // epilogue warps
+  // int8 at 240 tokens: the accumulators fill TMEM, so nothing is multiplied while they
+  // are drained, and the converters, which then have nothing to do, drain with the others
+  static constexpr bool kBothDrain = MODE == kModeI8 && 4 * BN > 512;
+  static constexpr int kDrainW = kEpiW + (kBothDrain ? kCvtWarps : 0);
+  static constexpr int kQuantW = 4 + kCvtWarps + (kBothDrain ? kEpiW : 0);  // warps of an int8 quantisation tile
   static constexpr int kTokBytes = BN * 128;
   static constexpr bool kTA = Rings<BN, MODE>::kTA;
   static constexpr int kQOff = kTA ? 0 : kW * kABytes;
@@ -618,13 +623,12 @@ __device__ __forceinline__ void quantize_chunk_rows(const GemmParams &p, const T
 // these tiles, chains of L2 latencies, took 190 of 1565 us at Hy3 T = 4096.
 // Not inlined: its registers beside the other roles' would spill in their loops
 // (gate/up at T = 512 625 -> 746 us).
-constexpr int kQuantWarps = 4 + kCvtWarps;
 __device__ __noinline__ void quantize_rows_int8(__nv_bfloat16 *act, const float *am, float *scales, int ld, int pc0,
-                                                int pc1, int ntok, int w) {
+                                                int pc1, int ntok, int w, int warps) {
   const int lane = threadIdx.x & 31, c8 = lane & 7, nb = ld >> 5;
   constexpr int kPieces = 6;  // in flight
 #pragma unroll 1
-  for (int r0 = 4 * w; r0 < ntok; r0 += 4 * kQuantWarps) {
+  for (int r0 = 4 * w; r0 < ntok; r0 += 4 * warps) {
     const int row = r0 + (lane >> 3);
     const bool on = row < ntok;
     float m = on ? strided_max(am + (size_t)row * nb, c8, 8, nb) : 0.0f;
@@ -657,7 +661,7 @@ __device__ __noinline__ void quantize_rows_int8(__nv_bfloat16 *act, const float 
 
 // A warp's share of an int8 quantisation tile: after every gate/up tile of the
 // segment (a bounded wait), and counted when it is written.  False: given up.
-template <int BN>
+template <int BN, int WARPS>
 __device__ __forceinline__ bool quant_tile_int8(const GemmParams &p, const Tile &tl, const unsigned *done, unsigned need,
                                                 unsigned *count, int w, int lane, unsigned *err, volatile int *abort_flag) {
   bool ok = true;
@@ -681,7 +685,7 @@ __device__ __forceinline__ bool quant_tile_int8(const GemmParams &p, const Tile 
     const int pc0 = split ? tl.rb * 32 : 0, pc1 = split ? min(pc0 + 32, ld >> 3) : ld >> 3;
     quantize_rows_int8((tl.shared ? p.act_s : p.act) + (size_t)tl.row0 * ld,
                        (tl.shared ? p.amax_s : p.amax) + (size_t)tl.row0 * (ld >> 5),
-                       (tl.shared ? p.asc_s : p.asc) + tl.row0, ld, pc0, pc1, tl.ntok, w);
+                       (tl.shared ? p.asc_s : p.asc) + tl.row0, ld, pc0, pc1, tl.ntok, w, WARPS);
   }
   __threadfence();  // the codes and scales, before the count (release)
   __syncwarp();
@@ -696,7 +700,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
   using L = Layout<BN, MODE>;
   constexpr bool Q8 = MODE == kModeQ8, F8 = MODE == kModeF8, Q4 = MODE == kModeQ4, I8 = MODE == kModeI8;
   constexpr bool CV = converts(MODE), RQ = requantizes(MODE);
-  constexpr bool TA = L::kTA;
+  constexpr bool TA = L::kTA, BD = L::kBothDrain;
+  constexpr int kGuCounts = BD ? L::kDrainW : 1;  // a gate/up tile is counted once, or by each warp that drains it
   constexpr int KE = F8 ? 128 : 64;  // K elements per step: one 128-byte row of a weight or token box
   constexpr int KSH = F8 ? 7 : 6;
   constexpr int KW = L::kW, KT = L::kT, KQ = L::kQ, EW = L::kEpiW;
@@ -746,7 +751,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(afull_bar(a), 2);
-      mbar_init(aempty_bar(a), EW);
+      mbar_init(aempty_bar(a), L::kDrainW);
     }
     mbar_init(drain_bar, 1);
     mbar_init(drain_bar2, 1);
@@ -785,6 +790,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
   // permutation with wait_first, waits before it triggers.)
   if (!p.early && !p.late_tokens) pdl_wait();
   const Sched q = make_sched<BN>(p);
+  const Sched &sched = q;  // where a role's own q hides it
   if (p.early && q.Rs > 0 && warp == kWWarp && lane == 0) {
     // The shared expert's weights into L2 while the routing still runs: none
     // of its tiles depends on the routing, and the early block alone would
@@ -809,6 +815,72 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
   unsigned *done2 = p.sync + kSyncQuant;  // W8A8: quantisation tiles finished, per segment
   bool ok = true;
   auto decode = [&](int t) { return decode_tile<BN, KSH>(p, t, q, *misc, seg_off, cst, rstart, rdesc); };
+
+  // FP8 (int8) weights (warps 14..21): the codes of a tile -> bf16 (fp16) weight
+  // slots (the values of the codes; the epilogue applies each row's scale).
+  // Two groups of four converter warps take alternate K steps (the per-step
+  // handoff -- waits, proxy fence, arrivals -- then overlaps across groups).
+  // Warp wg of a group converts rows 64 (wg & 1) .. + 63 of box wg >> 1; per
+  // pass, lane l converts 16 codes (chunk l & 3) of row 8 it + (l >> 2), so a
+  // warp reads 512 contiguous bytes and writes whole 128-byte swizzled rows.
+  // Parity waits stay unambiguous: with three weight slots a group's previous
+  // step (j - 2) needed MMA j - 5 done, which orders the slot's earlier phase
+  // (MMA j - 6) before its wait; with an even number of code slots, step
+  // j - KQ belonged to the same group.
+  // With two weight slots each group has a slot of its own.
+  static_assert(!(Q8 || (I8 && !TA)) || (KQ % 2 == 0 && (KW == 3 || KW == 2)), "two converter groups need an even code ring");
+  struct {
+    int ws = 0, qs = 0;
+    uint32_t wph = 0, qph = 0;
+    unsigned kstep = 0;
+  } cv;
+  auto convert_tile = [&](const Tile &tl) -> bool {
+    const int cw = warp - (kEpiWarp0 + EW);
+    const int grp = cw >> 2, wg = cw & 3;
+    const int box = wg >> 1, c = lane & 3;
+    auto wide = [](uint32_t a, uint32_t b) {  // eight codes to 16-bit values
+      if constexpr (I8) {
+        const uint2 x = int8x4_to_f16(a), y = int8x4_to_f16(b);
+        return make_uint4(x.x, x.y, y.x, y.y);
+      } else {
+        return e4m3x8_to_bf16(a, b);
+      }
+    };
+    for (int kb = 0; kb < tl.nk; ++kb, ++cv.kstep) {
+      if ((int)(cv.kstep & 1u) == grp) {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(qfull_bar(cv.qs), cv.qph, err, abort_flag) &&
+                                         mbar_wait(wempty_bar(cv.ws), cv.wph ^ 1u, err, abort_flag));
+        if (!ok) return false;
+        const uint8_t *src = smem + L::kQOff + cv.qs * kQBytes + box * (kQBytes / 2);
+        uint8_t *dst = smem + cv.ws * kABytes + box * (kABytes / 2);
+        uint4 v[8];  // every read first: the stores cannot then hold back the next loads
+#pragma unroll
+        for (int it = 0; it < 8; ++it)
+          v[it] = *reinterpret_cast<const uint4 *>(src + (64 * (wg & 1) + 8 * it + (lane >> 2)) * 64 + c * 16);
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+          const int rr = 64 * (wg & 1) + 8 * it + (lane >> 2);
+          *reinterpret_cast<uint4 *>(dst + rr * 128 + (((2 * c) ^ (rr & 7)) << 4)) = wide(v[it].x, v[it].y);
+          *reinterpret_cast<uint4 *>(dst + rr * 128 + (((2 * c + 1) ^ (rr & 7)) << 4)) = wide(v[it].z, v[it].w);
+        }
+        fence_proxy_async_smem();  // generic-proxy writes read by the tensor core
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(wfull_bar(cv.ws));
+          mbar_arrive(qempty_bar(cv.qs));
+        }
+      }
+      if (++cv.ws == KW) {
+        cv.ws = 0;
+        cv.wph ^= 1u;
+      }
+      if (++cv.qs == KQ) {
+        cv.qs = 0;
+        cv.qph ^= 1u;
+      }
+    }
+    return true;
+  };
 
   if (warp == kWWarp) {
     // ================= tile claims and weight loads.  Lane 0 claims tiles and
@@ -937,7 +1009,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
       if constexpr (I8) {
         if (tl.phase == 2) {
           const int nch = tl.shared ? q.nch_s : cst[tl.seg + 1] - cst[tl.seg];
-          ok = quant_tile_int8<BN>(p, tl, done1 + tl.seg, (unsigned)(nch * (tl.shared ? q.Rs : q.Rr)), done2 + tl.seg,
+          ok = quant_tile_int8<BN, L::kQuantW>(p, tl, done1 + tl.seg, (unsigned)(nch * (tl.shared ? q.Rs : q.Rr) * kGuCounts), done2 + tl.seg,
                                    warp - kTokWarp0, lane, err, abort_flag);
           continue;
         }
@@ -946,8 +1018,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
         const int nch = tl.shared ? q.nch_s : cst[tl.seg + 1] - cst[tl.seg];
         const bool on_quant = RQ && tl.phase == 1;
         const unsigned *cnt = (on_quant ? done2 : done1) + tl.seg;
-        const int nq = quant_blocks<BN>(p, tl.shared ? p.Is : p.I) * (I8 ? kQuantWarps : 1);  // quantisation counts per chunk
-        const unsigned need = (unsigned)(on_quant ? nch * nq : nch * (tl.shared ? q.Rs : q.Rr));
+        const int nq = quant_blocks<BN>(p, tl.shared ? p.Is : p.I) * (I8 ? L::kQuantW : 1);  // quantisation counts per chunk
+        const unsigned need = (unsigned)(on_quant ? nch * nq : nch * (tl.shared ? q.Rs : q.Rr) * kGuCounts);
         if (ld_acquire_gpu(cnt) < need) {
           const unsigned long long t0 = globaltimer();
           while (ld_acquire_gpu(cnt) < need) {
@@ -1128,15 +1200,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
         mbar_wait_drain(db, 0);
       }
     }
-  } else if (warp < kEpiWarp0 + EW) {
+  } else if (warp < kEpiWarp0 + L::kDrainW) {
     // ================= epilogue (warps 6..21 -> TMEM lane quarters 2,3,0,1, four times;
     // with FP8 weights warps 6..13, twice)
     const int q = warp & 3;
     // column groups of kEpiCols (16: one TMEM wait per 16 columns);
     // the warps of a lane quarter take its groups in turn
     constexpr int kEpiCols = BN >= 64 ? kWideEpiCols : 16;
-    constexpr int kEpiStep = kEpiCols * (EW / 4);  // the lane quarter's warps take groups in turn
+    constexpr int kEpiStep = kEpiCols * (L::kDrainW / 4);  // the lane quarter's warps take groups in turn
     const int c_first = kEpiCols * ((warp - kEpiWarp0) >> 2);
+    const int cw = warp - (kEpiWarp0 + EW);  // BD: a converter warp where not negative
     __nv_bfloat16 *stage = reinterpret_cast<__nv_bfloat16 *>(smem + L::kEpiOff + (warp - kEpiWarp0) * kEpiCols * 64);
     const int r = 32 * q + lane;  // weight row within the 128-row half
     if (p.late_tokens) pdl_wait();  // the token scales
@@ -1150,6 +1223,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
       __syncwarp();
       if (lane == 0) mbar_arrive(id_empty(rs));
       if (t < 0) break;
+      if constexpr (BD) {
+        if (tl.phase == 2) {
+          const int nch = tl.shared ? sched.nch_s : cst[tl.seg + 1] - cst[tl.seg];
+          ok = quant_tile_int8<BN, L::kQuantW>(p, tl, done1 + tl.seg,
+                                               (unsigned)(nch * (tl.shared ? sched.Rs : sched.Rr) * kGuCounts),
+                                               done2 + tl.seg, 4 + warp - kEpiWarp0, lane, err, abort_flag);
+          continue;
+        }
+        if (cw >= 0) {
+          ok = convert_tile(tl);
+          if (!ok) break;
+        }
+      }
       if (tl.phase == 2) continue;
       const int acc = na % L::kAccBufs;
       const uint32_t aph = (uint32_t)(na / L::kAccBufs) & 1u;
@@ -1361,8 +1447,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
       if (tl.phase == 0 && (p.phases & 2)) {
         // publish: this gate/up tile's activations are written (release to the down tiles)
         __threadfence();
-        named_bar_sync(2, 32 * EW);
-        if (warp == kEpiWarp0 && lane == 0) atomicAdd(done1 + tl.seg, 1u);
+        if constexpr (BD) {
+          __syncwarp();
+          if (lane == 0) atomicAdd(done1 + tl.seg, 1u);
+        } else {
+          named_bar_sync(2, 32 * EW);
+          if (warp == kEpiWarp0 && lane == 0) atomicAdd(done1 + tl.seg, 1u);
+        }
       }
     }
   } else if constexpr (Q4) {
@@ -1468,7 +1559,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
       if (t < 0) break;
       if (tl.phase == 2) {
         const int nch = tl.shared ? q.nch_s : cst[tl.seg + 1] - cst[tl.seg];
-        ok = quant_tile_int8<BN>(p, tl, done1 + tl.seg, (unsigned)(nch * (tl.shared ? q.Rs : q.Rr)), done2 + tl.seg, 4 + cw,
+        ok = quant_tile_int8<BN, L::kQuantW>(p, tl, done1 + tl.seg, (unsigned)(nch * (tl.shared ? q.Rs : q.Rr) * kGuCounts), done2 + tl.seg, 4 + cw,
                                  lane, err, abort_flag);
         continue;
       }
@@ -1510,34 +1601,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
         }
       }
     }
-  } else if constexpr (Q8 || I8) {
-    // ================= FP8 (int8) weights (warps 14..21): codes -> bf16 (fp16) weight
-    // slots (the values of the codes; the epilogue applies each row's scale).
-    // Two groups of four converter warps take alternate K steps (the per-step
-    // handoff -- waits, proxy fence, arrivals -- then overlaps across groups).
-    // Warp wg of a group converts rows 64 (wg & 1) .. + 63 of box wg >> 1; per
-    // pass, lane l converts 16 codes (chunk l & 3) of row 8 it + (l >> 2), so a
-    // warp reads 512 contiguous bytes and writes whole 128-byte swizzled rows.
-    // Parity waits stay unambiguous: with three weight slots a group's previous
-    // step (j - 2) needed MMA j - 5 done, which orders the slot's earlier phase
-    // (MMA j - 6) before its wait; with an even number of code slots, step
-    // j - KQ belonged to the same group.
-    // With two weight slots each group has a slot of its own.
-    static_assert(!(Q8 || I8) || (KQ % 2 == 0 && (KW == 3 || KW == 2)), "two converter groups need an even code ring");
+  } else if constexpr ((Q8 || I8) && !BD) {
+    // ================= FP8 (int8) weights (warps 14..21)
     const int cw = warp - (kEpiWarp0 + EW);
-    const int grp = cw >> 2, wg = cw & 3;
-    const int box = wg >> 1, c = lane & 3;
-    auto wide = [](uint32_t a, uint32_t b) {  // eight codes to 16-bit values
-      if constexpr (I8) {
-        const uint2 x = int8x4_to_f16(a), y = int8x4_to_f16(b);
-        return make_uint4(x.x, x.y, y.x, y.y);
-      } else {
-        return e4m3x8_to_bf16(a, b);
-      }
-    };
-    int ws = 0, qs = 0;
-    uint32_t wph = 0, qph = 0;
-    unsigned kstep = 0;
     for (int i = 0; ok; ++i) {
       const int rs = i % kRing;
       ok = __all_sync(0xffffffffu, mbar_wait(id_full(rs), (uint32_t)(i / kRing) & 1u, err, abort_flag));
@@ -1550,44 +1616,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
       if constexpr (I8) {
         if (tl.phase == 2) {
           const int nch = tl.shared ? q.nch_s : cst[tl.seg + 1] - cst[tl.seg];
-          ok = quant_tile_int8<BN>(p, tl, done1 + tl.seg, (unsigned)(nch * (tl.shared ? q.Rs : q.Rr)), done2 + tl.seg,
+          ok = quant_tile_int8<BN, L::kQuantW>(p, tl, done1 + tl.seg, (unsigned)(nch * (tl.shared ? q.Rs : q.Rr) * kGuCounts), done2 + tl.seg,
                                    4 + cw, lane, err, abort_flag);
           continue;
         }
       }
-      for (int kb = 0; kb < tl.nk; ++kb, ++kstep) {
-        if ((int)(kstep & 1u) == grp) {
-          ok = __all_sync(0xffffffffu, mbar_wait(qfull_bar(qs), qph, err, abort_flag) &&
-                                           mbar_wait(wempty_bar(ws), wph ^ 1u, err, abort_flag));
-          if (!ok) break;
-          const uint8_t *src = smem + L::kQOff + qs * kQBytes + box * (kQBytes / 2);
-          uint8_t *dst = smem + ws * kABytes + box * (kABytes / 2);
-          uint4 v[8];  // every read first: the stores cannot then hold back the next loads
-#pragma unroll
-          for (int it = 0; it < 8; ++it)
-            v[it] = *reinterpret_cast<const uint4 *>(src + (64 * (wg & 1) + 8 * it + (lane >> 2)) * 64 + c * 16);
-#pragma unroll
-          for (int it = 0; it < 8; ++it) {
-            const int rr = 64 * (wg & 1) + 8 * it + (lane >> 2);
-            *reinterpret_cast<uint4 *>(dst + rr * 128 + (((2 * c) ^ (rr & 7)) << 4)) = wide(v[it].x, v[it].y);
-            *reinterpret_cast<uint4 *>(dst + rr * 128 + (((2 * c + 1) ^ (rr & 7)) << 4)) = wide(v[it].z, v[it].w);
-          }
-          fence_proxy_async_smem();  // generic-proxy writes read by the tensor core
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(wfull_bar(ws));
-            mbar_arrive(qempty_bar(qs));
-          }
-        }
-        if (++ws == KW) {
-          ws = 0;
-          wph ^= 1u;
-        }
-        if (++qs == KQ) {
-          qs = 0;
-          qph ^= 1u;
-        }
-      }
+      ok = convert_tile(tl);
     }
   }
 
