@@ -474,7 +474,7 @@ moe_status do_expert_phases(const moe_dims &d, int phases, const moe_bf16 *hidde
                             (d.has_shared ? (d.T / 16 + 1) * ((Is + 127) / 128 + rd) : 0);
     if (worst >= (1LL << 30)) return MOE_ERR_UNSUPPORTED;
   }
-  const int bn = gemm_tile_n(d.T, d.top_k, d.E);
+  const int bn = i8 != nullptr ? int8_tile_n(d.T, d.top_k, d.E) : gemm_tile_n(d.T, d.top_k, d.E);
   GemmParams g;
   std::memset(&g, 0, sizeof(g));
   g.T = d.T;

@@ -853,15 +853,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_ffn_kernel(const __gri
         if (!ok) return false;
         const uint8_t *src = smem + L::kQOff + cv.qs * kQBytes + box * (kQBytes / 2);
         uint8_t *dst = smem + cv.ws * kABytes + box * (kABytes / 2);
-        uint4 v[8];  // every read first: the stores cannot then hold back the next loads
+        constexpr int kPass = BD ? 4 : 8;  // reads before their stores, which could otherwise hold back the next loads
 #pragma unroll
-        for (int it = 0; it < 8; ++it)
-          v[it] = *reinterpret_cast<const uint4 *>(src + (64 * (wg & 1) + 8 * it + (lane >> 2)) * 64 + c * 16);
+        for (int i0 = 0; i0 < 8; i0 += kPass) {
+          uint4 v[kPass];
 #pragma unroll
-        for (int it = 0; it < 8; ++it) {
-          const int rr = 64 * (wg & 1) + 8 * it + (lane >> 2);
-          *reinterpret_cast<uint4 *>(dst + rr * 128 + (((2 * c) ^ (rr & 7)) << 4)) = wide(v[it].x, v[it].y);
-          *reinterpret_cast<uint4 *>(dst + rr * 128 + (((2 * c + 1) ^ (rr & 7)) << 4)) = wide(v[it].z, v[it].w);
+          for (int it = 0; it < kPass; ++it)
+            v[it] = *reinterpret_cast<const uint4 *>(src + (64 * (wg & 1) + 8 * (i0 + it) + (lane >> 2)) * 64 + c * 16);
+#pragma unroll
+          for (int it = 0; it < kPass; ++it) {
+            const int rr = 64 * (wg & 1) + 8 * (i0 + it) + (lane >> 2);
+            *reinterpret_cast<uint4 *>(dst + rr * 128 + (((2 * c) ^ (rr & 7)) << 4)) = wide(v[it].x, v[it].y);
+            *reinterpret_cast<uint4 *>(dst + rr * 128 + (((2 * c + 1) ^ (rr & 7)) << 4)) = wide(v[it].z, v[it].w);
+          }
         }
         fence_proxy_async_smem();  // generic-proxy writes read by the tensor core
         __syncwarp();
@@ -1659,6 +1663,17 @@ int gemm_tile_n(int T, int top_k, int E) {
   return (long long)T * top_k > 256LL * E ? 256 : 240;
 }
 
+// int8: 64-token tiles, the widest with two accumulator pairs beside weights in TMEM,
+// while experts average at most 48 tokens (experts of more are several chunks), then
+// 128 and 240.  Hy3 shape, tiles of 64, 128 and 240 tokens: T = 128 (5 tokens an
+// expert) 753, 910 and 909 us, T = 1024 (43) 848, 991 and 1121, T = 2048 (85) 1651,
+// 1082 and 1211, T = 4096 (171) 2613, 2115 and 1463.
+int int8_tile_n(int T, int top_k, int E) {
+  if (T <= 64) return gemm_tile_n(T, top_k, E);
+  const long long S = (long long)T * top_k;
+  return S <= 48LL * E ? 64 : S <= 96LL * E ? 128 : 240;
+}
+
 namespace {
 template <int BN, int MODE>
 cudaError_t launch_one(const GemmParams &p, int num_ctas, cudaStream_t stream, bool pdl) {
@@ -1690,8 +1705,8 @@ cudaError_t launch_expert_ffn(const GemmParams &p, int bn, int num_ctas, cudaStr
       default: return cudaErrorInvalidValue;  // 32 tokens and fewer run the one-kernel form
     }
   }
-  if (p.mode == kModeI8) {  // as W8A8
-    switch (bn < 240 ? bn : 240) {
+  if (p.mode == kModeI8) {
+    switch (bn) {
       case 16: return launch_one<16, kModeI8>(p, num_ctas, stream, pdl);
       case 32: return launch_one<32, kModeI8>(p, num_ctas, stream, pdl);
       case 64: return launch_one<64, kModeI8>(p, num_ctas, stream, pdl);

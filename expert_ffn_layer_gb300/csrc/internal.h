@@ -121,6 +121,7 @@ constexpr int kSyncClaim = 64, kSyncExit = 65, kSyncPermute = 66,
 constexpr int kWsHeaderBytes = 4096;
 constexpr bool int8_in_tmem(int bn) { return bn <= 64; }  // int8: tiles whose weights are multiplied from TMEM
 int gemm_tile_n(int T, int top_k, int E);  // widest token tile (multiple of 16, <= 256) for a batch
+int int8_tile_n(int T, int top_k, int E);  // the same for int8 weights (<= 240)
 cudaError_t launch_expert_ffn(const GemmParams &p, int bn, int num_ctas, cudaStream_t stream, bool pdl);
 
 // --------------------------------------------------------------- combine

@@ -138,8 +138,12 @@ def ffn(dl, w, perm, offsets):
 # widths that are odd multiples of 64 (a ragged row block, a last group of 32-column maxima past the row) on
 # every token tile, a shared expert of another width, one expert, one token
 ODD_I = W.Workload("odd_i", 300, 320, 8, 2, 192, 448, "sigmoid", 2.826, 0.0, True, "normal", 0.1, 12)
+# tiles of 128 and of 240 tokens with I past 256 columns (ragged column blocks in the quantisation tiles), and
+# 64-token tiles with several chunks an expert
+MANY = W.Workload("many", 600, 192, 8, 1, 576, 320, "sigmoid", 2.826, 0.0, True, "normal", 0.1, 15)
 LONG_I = W.Workload("long_i", 260, 128, 3, 1, 1600, 64, "sigmoid", 2.826, 0.0, True, "normal", 0.1, 13)
 SHAPES = [W.WORKLOADS["tiny"], MID, MID_SOFTMAX, WIDE, ODD_H, NOSHARED, ODD_I, LONG_I,
+          MANY, MANY.with_(name="many_800", T=800), MANY.with_(name="many_360", T=360, E=16),
           *(ODD_I.with_(name=f"odd_i_{T}", T=T) for T in (1, 17, 33, 65, 129)), W.WORKLOADS["decode"]]
 
 
