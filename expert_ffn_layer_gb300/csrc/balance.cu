@@ -146,18 +146,30 @@ __global__ void __launch_bounds__(kThreads) balance_loss_kernel(const BalancePar
   }
   __syncthreads();
   if (!last) return;
-  const int2 nt = sequence_totals(p.tokens, p.n_seq, nb);
-  if (warp > 1) return;
   __threadfence();
-  // warp 0 the balance loss, warp 1 the z loss: lane l adds CTAs l, l + 32, ..
-  double v = 0.0;
-  for (int i = lane; i < (int)gridDim.x; i += 32) v += __ldcg(p.part + 2 * i + warp);
+  // every CTA's pair at once, then added in a fixed order
+  double a = 0.0, b = 0.0;
+  for (int i = threadIdx.x; i < (int)gridDim.x; i += kThreads) {
+    a += __ldcg(p.part + 2 * i);
+    b += __ldcg(p.part + 2 * i + 1);
+  }
+  const int2 nt = sequence_totals(p.tokens, p.n_seq, nb);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
   if (lane == 0) {
-    const double scale = warp == 0 ? (double)p.E / p.top_k / max(nt.x, 1) : 1.0 / max(nt.y, 1);
-    p.losses[warp] = (float)(v * scale);
-    if (warp == 0) *p.done = 0;
+    sums[0][warp] = a;
+    sums[1][warp] = b;
+  }
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    double v = 0.0;
+    for (int w = 0; w < kThreads / 32; ++w) v += sums[threadIdx.x][w];
+    const double scale = threadIdx.x == 0 ? (double)p.E / p.top_k / max(nt.x, 1) : 1.0 / max(nt.y, 1);
+    p.losses[threadIdx.x] = (float)(v * scale);
+    if (threadIdx.x == 0) *p.done = 0;
   }
 }
 
@@ -194,6 +206,7 @@ cudaError_t launch_balance(const BalanceParams &p, int num_sms, cudaStream_t str
   }
   if (p.losses == nullptr) return cudaSuccess;
   int blocks = (p.T + kThreads / 32 - 1) / (kThreads / 32);
+  if (blocks > 4 * num_sms) blocks = 4 * num_sms;
   if (blocks > kBalanceMaxCtas) blocks = kBalanceMaxCtas;
   void *args[] = {(void *)&p};
   return launch_ex(p.sigmoid ? (const void *)balance_loss_kernel<true> : (const void *)balance_loss_kernel<false>,
