@@ -20,7 +20,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kClusterCtas = 8, kClusterThreads = 1024;
 constexpr int kClusterCounters = 11000;   // 44 KB of shared memory
-constexpr int kClusterSlots = 32 * kClusterCtas * kClusterThreads;  // 32 choices a thread
+constexpr int kClusterSlots = 8 * kClusterCtas * kClusterThreads;  // 8 choices a thread
 }
 
 __global__ void __launch_bounds__(kThreads) balance_zero_kernel(int32_t *counts, int32_t *tokens, long long nc, int n_seq) {
@@ -109,40 +109,64 @@ __global__ void __launch_bounds__(kThreads) balance_loss_kernel(const BalancePar
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_launch_dependents();
   pdl_wait();
-  double balance = 0.0, z = 0.0;
-  for (unsigned t = blockIdx.x * (kThreads / 32) + warp; t < (unsigned)p.T; t += gridDim.x * (kThreads / 32)) {
-    const int b = token_seq(p.seq_id, p.n_seq, t, p.err);
-    if (b < 0) continue;
-    float v[kPerLane];
-    int c[kPerLane];
+  // a warp's few tokens are added in fp32 with the rounding carried along (Kahan)
+  float balance = 0.0f, z = 0.0f, balance_c = 0.0f, z_c = 0.0f;
+  auto add = [](float &sum, float &c, float x) {
+    const float y = __fsub_rn(x, c), t = __fadd_rn(sum, y);
+    c = __fsub_rn(__fsub_rn(t, sum), y);
+    sum = t;
+  };
+  const unsigned step = gridDim.x * (kThreads / 32);
+  unsigned t = blockIdx.x * (kThreads / 32) + warp;
+  float v[kPerLane];
+  int seq = -1;
+  if (t < (unsigned)p.T) {
+    seq = token_seq(p.seq_id, p.n_seq, t, p.err);
     load_logits(p.logits + (size_t)t * p.E, p.E, lane, v);
-    const int32_t *of = p.counts + (size_t)b * p.E;
+  }
+  while (t < (unsigned)p.T) {
+    const int here = seq;
+    int c[kPerLane];
+    float n = 1.0f, now[kPerLane];
+    if (here >= 0) {
+      // through L1: every token reads the same few lines, which L2 would serve one by one
+      // (the logits' pass 29 against 17 us at 16384 tokens)
+      const int32_t *of = p.counts + (size_t)here * p.E;
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) c[j] = expert_of(lane, j) < p.E ? __ldcg(of + expert_of(lane, j)) : 0;
-    const float n = (float)__ldcg(p.tokens + b);
-    const TokenScores r = token_scores<SIGMOID>(v, p.E, lane);
+      for (int j = 0; j < kPerLane; ++j) c[j] = expert_of(lane, j) < p.E ? __ldg(of + expert_of(lane, j)) : 0;
+      n = (float)__ldg(p.tokens + here);
+    }
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) now[j] = v[j];
+    t += step;
+    if (t < (unsigned)p.T) {  // the next token's, while this one is worked on
+      seq = token_seq(p.seq_id, p.n_seq, t, p.err);
+      load_logits(p.logits + (size_t)t * p.E, p.E, lane, v);
+    }
+    if (here < 0) continue;
+    const TokenScores r = token_scores<SIGMOID>(now, p.E, lane);
     float dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) dot = fmaf((float)c[j], SIGMOID ? r.s[j] : r.p[j], dot);
     dot = warp_sum(dot);
-    balance += (double)(dot / ((SIGMOID ? r.total : 1.0f) * n) / n);
-    z += (double)(r.lse * r.lse);
+    add(balance, balance_c, dot / ((SIGMOID ? r.total : 1.0f) * n) / n);
+    add(z, z_c, r.lse * r.lse);
   }
   if (lane == 0) {
-    sums[0][warp] = balance;
-    sums[1][warp] = z;
+    sums[0][warp] = (double)balance - balance_c;
+    sums[1][warp] = (double)z - z_c;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double a = 0.0, b = 0.0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      a += sums[0][w];
-      b += sums[1][w];
+  if (warp == 0) {
+    double v = 0.0;
+    if (lane < 2) {
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) v += sums[lane][w];
+      p.part[2 * blockIdx.x + lane] = v;
+      __threadfence();
     }
-    p.part[2 * blockIdx.x] = a;
-    p.part[2 * blockIdx.x + 1] = b;
-    __threadfence();
-    last = atomicAdd(p.done, 1u) == gridDim.x - 1;
+    __syncwarp();
+    if (lane == 0) last = atomicAdd(p.done, 1u) == gridDim.x - 1;
   }
   __syncthreads();
   if (!last) return;
@@ -166,9 +190,10 @@ __global__ void __launch_bounds__(kThreads) balance_loss_kernel(const BalancePar
   __syncthreads();
   if (threadIdx.x < 2) {
     double v = 0.0;
+#pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) v += sums[threadIdx.x][w];
-    const double scale = threadIdx.x == 0 ? (double)p.E / p.top_k / max(nt.x, 1) : 1.0 / max(nt.y, 1);
-    p.losses[threadIdx.x] = (float)(v * scale);
+    p.losses[threadIdx.x] = threadIdx.x == 0 ? (float)v * ((float)p.E / (float)p.top_k) / (float)max(nt.x, 1)
+                                             : (float)v / (float)max(nt.y, 1);
     if (threadIdx.x == 0) *p.done = 0;
   }
 }
@@ -206,7 +231,8 @@ cudaError_t launch_balance(const BalanceParams &p, int num_sms, cudaStream_t str
   }
   if (p.losses == nullptr) return cudaSuccess;
   int blocks = (p.T + kThreads / 32 - 1) / (kThreads / 32);
-  if (blocks > 4 * num_sms) blocks = 4 * num_sms;
+  // a few tokens a warp and one wave: each CTA's end costs about as much as two tokens
+  if (blocks > 3 * num_sms) blocks = 3 * num_sms;
   if (blocks > kBalanceMaxCtas) blocks = kBalanceMaxCtas;
   void *args[] = {(void *)&p};
   return launch_ex(p.sigmoid ? (const void *)balance_loss_kernel<true> : (const void *)balance_loss_kernel<false>,

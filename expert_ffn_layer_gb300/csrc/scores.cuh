@@ -102,9 +102,12 @@ __device__ __forceinline__ TokenScores token_scores(const float (&v)[kPerLane], 
   if (SIGMOID) {
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) {
-      const bool on = expert_of(lane, j) < E;
-      r.s[j] = on ? 1.0f / (1.0f + expf(-v[j])) : 0.0f;
-      r.miss[j] = on ? 1.0f / (1.0f + expf(v[j])) : 0.0f;
+      // both ends from one exponential, which cannot overflow, and one reciprocal of a
+      // value in [1, 2]; past the last expert v = -infinity, so s = 0
+      const float t = expf(-fabsf(v[j])), big = __fdividef(1.0f, 1.0f + t), small = t * big;
+      r.s[j] = v[j] >= 0.0f ? big : small;
+      r.miss[j] = v[j] >= 0.0f ? small : big;
+      if (v[j] != v[j]) r.s[j] = r.miss[j] = v[j];
       r.total += r.s[j];
     }
     r.total = warp_sum(r.total);
