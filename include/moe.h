@@ -226,7 +226,7 @@ moe_status moe_combine(const moe_dims *d, const moe_bf16 *y_sorted, const moe_bf
  * number marks padding, which counts nowhere, gets a zero gradient and is not read
  * (its logits and hidden state may hold anything).  A number of n_seq or more sets
  * MOE_DEVERR_INDEX and is taken for padding.  seq_id NULL: one sequence (n_seq = 1).
- * 1 <= n_seq <= 65536.
+ * 1 <= n_seq <= 65536.  Outputs overlap no input.
  *
  * moe_balance_loss: per-expert counts and the router's two auxiliary losses.
  *   logits   [T, E] fp32, as moe_route writes them (may be NULL when losses is)
@@ -240,8 +240,8 @@ moe_status moe_combine(const moe_dims *d, const moe_bf16 *y_sorted, const moe_bf
  *         mode (the bias and route_scale take no part): 1 when choices or scores
  *         are even
  *     [1] z: mean over all counted tokens of (log sum_e exp logits_te)^2
- *   Both are 0 when no token counts.  Sums over tokens are held in 64 bits and
- *   added in a fixed order. */
+ *   Both are 0 when no token counts.  Sums over tokens are held in more than 32
+ *   bits and added in a fixed order. */
 moe_status moe_balance_loss(const moe_dims *d, const float *logits, const int32_t *topk_idx, const int32_t *seq_id,
                             int n_seq, int32_t *counts, int32_t *tokens, float *losses, void *ws, size_t ws_bytes,
                             void *stream);
@@ -369,14 +369,15 @@ moe_status moe_layer_forward_w8a8(const moe_dims *d, const moe_bf16 *hidden, con
  * deployments that [case] names without a format.  A row's scale is m / 127 in
  * fp32, m its largest magnitude (1 for a row of zeros); a code is 127 w / m to
  * the nearest integer, ties to even (nothing is rounded before that); it stands for
- * code * scale.  A row with an infinity or NaN has a NaN scale: every output that
- * reads it is NaN, and its codes are unspecified.  Weights have a scale for each
- * output row (channel).  Activations are quantised by the same rule at run time:
- * the hidden state per token before the gate/up product, and the bf16 SiLU(gate) *
- * up activation per routed slot (per token for the shared expert) before the down
- * product.  Each output element is (sum of code products) * row scale * column
- * scale; products are exact, and so is their sum while it stays under 2^24 (past
- * that it is rounded as fp32 is).  The router stays fp32. */
+ * code * scale.  Codes made elsewhere may use -128 too.  A row with an infinity or
+ * NaN has a NaN scale: every output that reads it is NaN, and its codes are
+ * unspecified.  Weights have a scale for each output row (channel).  Activations
+ * are quantised by the same rule at run time: the hidden state per token before the
+ * gate/up product, and the bf16 SiLU(gate) * up activation per routed slot (per
+ * token for the shared expert) before the down product.  Each output element is
+ * (sum of code products) * row scale * column scale; products are exact, and so is
+ * their sum while it stays under 2^24 (past that it is rounded as fp32 is).  The
+ * router stays fp32. */
 typedef struct {
   const int8_t *gate, *up;                  /* [E, I, H] codes */
   const int8_t *down;                       /* [E, H, I] */

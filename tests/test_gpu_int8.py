@@ -112,6 +112,30 @@ def test_quantizer_special_rows():
     assert torch.isnan(values(codes.cuda(), scales.cuda())[4:7]).all()
 
 
+def test_every_code_back():
+    """Codes of a checkpoint may use all of -128 .. 127."""
+    codes = torch.arange(-128, 128, dtype=torch.int8, device="cuda").repeat(3, 1)
+    scales = torch.tensor([1.0, 0.3, 2.0 ** -120], device="cuda")
+    want = (codes.double() * scales.double()[:, None]).float().bfloat16()
+    assert torch.equal(values(codes, scales), want)
+
+
+def test_codes_of_minus_128_in_the_products():
+    """Weights whose codes are all -128 or 127, as other quantisers make them."""
+    w = W.Workload("codes", 20, 128, 2, 1, 64, 64, "sigmoid", 2.826, 0.0, False, "normal", 0.1, 16)
+    inp = W.layer_inputs(w)
+    rng = np.random.default_rng(3)
+    pair = lambda *s: (np.where(rng.random(s) < 0.5, -128, 127).astype(np.int8), np.full(s[:-1], 2e-4, np.float32))  # noqa: E731
+    q = {"w_gate": pair(2, 64, 128), "w_up": pair(2, 64, 128), "w_down": pair(2, 128, 64)}
+    r = ref8.layer(w, inp, {n: [(c[e], s[e].astype(np.float64)) for e in range(2)] for n, (c, s) in q.items()})
+    dl = DeviceLayer(w, inp)
+    ex = moe.Int8Experts(**{n[2:]: (torch.from_numpy(c).cuda(), torch.from_numpy(s).cuda()) for n, (c, s) in q.items()})
+    y = torch.empty((w.S, w.H), dtype=torch.bfloat16, device="cuda")
+    moe.moe_expert_ffn_int8(dl.d, dl.hidden, i32_dev(r["perm"]), i32_dev(r["offsets"]), ex, y, None, dl.ws)
+    torch.cuda.synchronize()
+    assert_layer_close(host_f64(y), r["y_sorted"], "y_sorted")
+
+
 def dev_experts(dl):
     return moe.quantize_int8_experts(dl.w_gate, dl.w_up, dl.w_down, dl.ws_gate, dl.ws_up, dl.ws_down)
 

@@ -99,8 +99,12 @@ CASES = [dict(T=1, E=1, k=1), dict(T=1, E=192, k=8), dict(T=2, E=33, k=16), dict
 IDS = lambda c: "-".join(f"{k}{v}" for k, v in c.items())  # noqa: E731
 
 
+# more choices, and more counters, than one cluster counts
+MANY = [dict(T=9000, E=16, k=8, n_seq=3, pad=0.1), dict(T=300, E=200, k=8, n_seq=60), dict(T=8500, E=8, k=8, sort=False, n_seq=5)]
+
+
 @pytest.mark.parametrize("mode", ["sigmoid", "softmax"])
-@pytest.mark.parametrize("c", CASES, ids=IDS)
+@pytest.mark.parametrize("c", CASES + MANY, ids=IDS)
 def test_balance_loss(c, mode):
     a = Case(mode=mode, **c)
     counts, tokens, out = a.balance()
@@ -268,6 +272,27 @@ def test_grad_hidden_and_router_w(c):
     assert torch.equal(one["grad_router_w"], got["grad_router_w"])
     two = a.backward(router_w=router_w)
     assert torch.equal(two["grad_hidden"], got["grad_hidden"])
+
+
+def test_more_tokens_than_one_pass():
+    """grad_router_w over several rounds of both accumulators and grad_hidden over several token tiles a CTA: sums and
+    rows far from the first, with padding in between."""
+    c = dict(T=5000, E=72, k=4, H=8192, n_seq=4, pad=0.05)
+    a = Case(mode="softmax", **c)
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    hidden = torch.randn((5000, 8192), device="cuda", generator=gen).bfloat16()
+    router_w = torch.randn((72, 8192), device="cuda", generator=gen) * 0.02
+    got = a.backward(hidden=hidden, router_w=router_w)
+    dl = got["grad_logits"].double()
+    at = torch.cat([torch.arange(0, 40), torch.arange(2040, 2060), torch.arange(4970, 5000)]).cuda()
+    want, mag = dl[at] @ router_w.double(), dl[at].abs() @ router_w.double().abs()
+    assert ((got["grad_hidden"][at].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -14 * mag + 1e-37).all()
+    cols = torch.cat([torch.arange(0, 64), torch.arange(8100, 8192)]).cuda()
+    x = hidden[:, cols].double()
+    want, mag = dl.T @ x, dl.T.abs() @ x.abs()
+    # at most 128 tokens, 3 * 8 steps, in an accumulator, then 40 sums in registers and 8 of the cluster
+    assert ((got["grad_router_w"][:, cols].double() - want).abs() <= (24 * 2.0 ** -23 + 48 * U) * mag + 1e-37).all()
+    assert (got["grad_router_w"][:, cols].double() - want).norm() <= 1e-6 * want.norm()
 
 
 def test_wide_ranges_of_gradients():
