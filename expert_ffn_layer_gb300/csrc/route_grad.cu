@@ -452,7 +452,6 @@ __global__ void __launch_bounds__(kProdThreads, 1) grad_router_w_kernel(const __
   const int split = gridDim.x, rank = blockIdx.x, h0 = blockIdx.y * 128;
   const int blocks = (p.T + kStep - 1) / kStep;
   const int k0 = (int)((long long)blocks * rank / split), k1 = (int)((long long)blocks * (rank + 1) / split);
-  const bool masked = p.seq_id != nullptr;
   volatile int *abort_flag = &sh->abort;
   unsigned *err = p.err;
   uint32_t tmem_cols = 32;
@@ -482,6 +481,14 @@ __global__ void __launch_bounds__(kProdThreads, 1) grad_router_w_kernel(const __
   // waited for the pieces, they are there already; its own end is waited for below.
   if (!waited) pdl_wait();
   pdl_launch_dependents();
+  // whether any of this part's tokens is padding
+  bool masked = false;
+  if (p.seq_id != nullptr) {
+    int any = 0;
+    for (int t = kStep * k0 + threadIdx.x; t < min(p.T, kStep * k1); t += kProdThreads)
+      any |= token_seq(p.seq_id, p.n_seq, t, err) < 0;
+    masked = __syncthreads_or(any);
+  }
   bool ok = true;
   if (warp == 0) {
     if (lane == 0) {
@@ -608,6 +615,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) grad_router_w_kernel(const __
     cluster_sync();
     // rank r adds up experts r, r + split, ..: a warp a row of 128 columns
     const int col = 4 * lane;
+#pragma unroll 2
     for (int e = rank + split * warp; e < p.E; e += split * (kProdThreads / 32)) {
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
       float4 v[kMaxSplit];
