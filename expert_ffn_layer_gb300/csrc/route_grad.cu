@@ -679,8 +679,10 @@ cudaError_t launch_route_grad(RouteGradParams p, int num_sms, cudaStream_t strea
     const cudaError_t e0 = set_smem_attr_once((const void *)grad_router_w_kernel, kSmemMax, attr_w);
     if (e0 != cudaSuccess) return e0;
     const int steps = (p.T + kStep - 1) / kStep, stage = (2 + 3 * eb) * kWBox;
-    int split = 1;  // parts of the tokens: a cluster
-    while (2 * split <= kMaxSplit && 2 * split <= steps && hb * 2 * split <= num_sms) split *= 2;
+    // parts of the tokens, a cluster, of at least four steps each (512 tokens at H = 4096:
+    // two parts 24 us in all, four 29)
+    int split = 1;
+    while (2 * split <= kMaxSplit && 8 * split <= steps && hb * 2 * split <= num_sms) split *= 2;
     p.w_stages = (kSmemMax - tail) / stage;
     if (p.w_stages > 8) p.w_stages = 8;
     p.w_smem = p.w_stages * stage;

@@ -241,7 +241,8 @@ def test_bad_indices_are_clamped_and_flagged():
 PRODUCTS = [dict(T=1, E=1, k=1, H=64), dict(T=1, E=192, k=8, H=4096), dict(T=8, E=192, k=8, H=1024),
             dict(T=127, E=40, k=5, H=1088, n_seq=3, pad=0.3), dict(T=129, E=64, k=8, H=128),
             dict(T=300, E=256, k=16, H=320, n_seq=2), dict(T=513, E=17, k=2, H=192, pad=0.5, n_seq=40),
-            dict(T=640, E=255, k=3, H=704), dict(T=1300, E=130, k=4, H=256, pad=0.1), dict(T=40, E=2, k=1, H=16384)]
+            dict(T=640, E=255, k=3, H=704), dict(T=1300, E=130, k=4, H=256, pad=0.1), dict(T=40, E=2, k=1, H=16384),
+            dict(T=2100, E=33, k=3, H=128, n_seq=3, pad=0.05)]
 
 
 @pytest.mark.parametrize("c", PRODUCTS, ids=IDS)
