@@ -120,11 +120,12 @@ struct Rings {
   static constexpr bool CV = converts(MODE);
   // int8, tiles of at most 64 tokens: the converters' fp16 weights go to TMEM, which
   // has room beside two accumulators, and the MMAs take them from there.  Through
-  // shared memory a K step's 16 KB of codes move 96 KB, of which its 128 bytes a
-  // cycle leave less than HBM's rate; this way 32 KB.
+  // shared memory a K step's 16 KB of codes move 96 KB there, at 128 bytes a cycle as
+  // long as HBM takes to bring them; this way 32 KB (Hy3 T = 8 250 -> 241 us, T = 32
+  // 573 -> 557).
   static constexpr bool kTA = MODE == kModeI8 && int8_in_tmem(BN);
   // int8 at 240 tokens: with two code slots (and three weight slots) the SM waits for
-  // HBM most of the time
+  // HBM most of the time (Hy3 T = 4096 1846 us, this way 1569)
   static constexpr bool kI8Wide = MODE == kModeI8 && BN >= 240;
   static constexpr int kW = kTA ? (BN <= 32 ? 6 : 4) : kI8Wide ? 2 : CV ? 3 : BN >= 256 ? 3 : BN >= 240 ? 4 : BN >= 128 ? 5 : 6;
   static constexpr int kQ = kTA ? 10 : kI8Wide ? 4 : CV ? (BN >= 240 ? 2 : BN >= 128 ? 4 : 6) : 0;  // MXFP4: two K steps each
@@ -139,7 +140,8 @@ struct Layout {
   static constexpr int kT = Rings<BN, MODE>::kT;
   static constexpr int kEpiW = CV ? kEpiWarps - kCvtWarps : kEpiWarps;  // epilogue warps
   // int8 at 240 tokens: the accumulators fill TMEM, so nothing is multiplied while they
-  // are drained, and the converters, which then have nothing to do, drain with the others
+  // are drained, and the converters, which then have nothing to do, drain with the
+  // others (Hy3 T = 4096 1523 -> 1480 us)
   static constexpr bool kBothDrain = MODE == kModeI8 && 4 * BN > 512;
   static constexpr int kDrainW = kEpiW + (kBothDrain ? kCvtWarps : 0);
   static constexpr int kQuantW = 4 + kCvtWarps + (kBothDrain ? kEpiW : 0);  // warps of an int8 quantisation tile

@@ -77,6 +77,8 @@ __global__ void __launch_bounds__(kThreads) int8_rows_kernel(const __nv_bfloat16
 }
 
 // Wider rows, up to 1024 V values: a CTA of four warps per row, again read once.
+// Bound by HBM: 98304 rows of 4096 values (805 MB in, 403 out) take 187 us, 6.5 TB/s,
+// against 250 with a warp a row that reads it twice.
 constexpr int kWideThreads = 128;
 template <bool F16, int V>
 __global__ void __launch_bounds__(kWideThreads) int8_wide_rows_kernel(const __nv_bfloat16 *__restrict__ src,
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kWideThreads) int8_wide_rows_kernel(const __nv
 
 // A warp per row: code * scale in fp32, rounded to bf16.  Eight codes a lane and step,
 // so that a lane's values are one whole 16-byte store (sixteen, stored as two halves
-// of every other sector: 264 against 190 us for 403 M values); eight steps' loads in
+// of every other sector: 264 against 197 us for 403 M values); eight steps' loads in
 // flight.
 __global__ void __launch_bounds__(kThreads) int8_values_kernel(const int8_t *__restrict__ codes,
                                                                const float *__restrict__ scales,

@@ -151,6 +151,7 @@ def test_masked_experts_and_saturated_logits(mode):
     a = Case(T=40, E=48, k=4, mode=mode, spread=1.0)
     a.logits[:, 5] = -np.inf
     a.logits[:, 9] = -1e30
+    a.logits[:, 11] = np.finfo(np.float32).min
     a.logits[3:6] += 60.0
     a.logits[7, :4] = 80.0
     a.logits[8, 10] = -60.0
@@ -242,7 +243,8 @@ PRODUCTS = [dict(T=1, E=1, k=1, H=64), dict(T=1, E=192, k=8, H=4096), dict(T=8, 
             dict(T=127, E=40, k=5, H=1088, n_seq=3, pad=0.3), dict(T=129, E=64, k=8, H=128),
             dict(T=300, E=256, k=16, H=320, n_seq=2), dict(T=513, E=17, k=2, H=192, pad=0.5, n_seq=40),
             dict(T=640, E=255, k=3, H=704), dict(T=1300, E=130, k=4, H=256, pad=0.1), dict(T=40, E=2, k=1, H=16384),
-            dict(T=2100, E=33, k=3, H=128, n_seq=3, pad=0.05)]
+            dict(T=2100, E=33, k=3, H=128, n_seq=3, pad=0.05), dict(T=100, E=20, k=2, H=64, n_seq=2, pad=0.2),
+            dict(T=17, E=192, k=8, H=192), dict(T=16, E=256, k=16, H=64, n_seq=3, pad=0.3)]
 
 
 @pytest.mark.parametrize("c", PRODUCTS, ids=IDS)
