@@ -98,19 +98,20 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineParams p
   }
 }
 
-// Gradients of the combine.  A CTA per token: its row of grad_out against the rows of
-// its slots, 8 values a thread step; the sums over H are added across the CTA in a
-// fixed order.  HBM-bound: K slots' loads in flight together (8 for top-8 and fewer:
+// Gradients of the combine.  A CTA per token, or (WARP: rows of at most 1024 values,
+// which would leave most of a CTA idle) a warp: its row of grad_out against the rows of
+// its slots, 8 values a thread step; the sums over H are added in a fixed order.  HBM-bound: K slots' loads in flight together (8 for top-8 and fewer:
 // Hy3 T = 4096, 571 MB, 98 us, 5.8 TB/s, against 121 one slot at a time), then their
 // stores.
-template <int K>
+template <int K, bool WARP>
 __global__ void __launch_bounds__(kThreads, K <= 8 ? 3 : 1) combine_grad_kernel(const CombineGradParams p) {
   __shared__ float sums[kThreads / 32][K];
   pdl_wait();
   pdl_launch_dependents();
   const int hv = p.H >> 3, k = p.top_k;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+  constexpr int kTokens = WARP ? kThreads / 32 : 1, kPerToken = WARP ? 32 : kThreads;
+  for (unsigned t = blockIdx.x * kTokens + (WARP ? warp : 0); t < (unsigned)p.T; t += gridDim.x * kTokens) {
     int pos[K];
     float wt[K], acc[K];
 #pragma unroll
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, K <= 8 ? 3 : 1) combine_grad_kernel(
         if (p.grad_y != nullptr) wt[j] = __ldg(p.topk_w + (size_t)t * k + j);
       }
     }
-    for (int c = threadIdx.x; c < hv; c += kThreads) {
+    for (int c = WARP ? lane : (int)threadIdx.x; c < hv; c += kPerToken) {
       float g[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       const uint4 go = __ldg(reinterpret_cast<const uint4 *>(p.grad_out + (size_t)t * p.H) + c);
       if (p.grad_w != nullptr) {
@@ -166,8 +167,12 @@ __global__ void __launch_bounds__(kThreads, K <= 8 ? 3 : 1) combine_grad_kernel(
       if (j >= k) break;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
-      if (lane == 0) sums[warp][j] = acc[j];
+      if (lane == 0) {
+        if (WARP) p.grad_w[(size_t)t * k + j] = acc[j];
+        else sums[warp][j] = acc[j];
+      }
     }
+    if (WARP) continue;
     __syncthreads();
     if (threadIdx.x < (unsigned)k) {
       float s = 0.0f;
@@ -188,10 +193,13 @@ cudaError_t launch_combine_grad(const CombineGradParams &p, cudaStream_t stream)
   }
   const int cap = (nsm > 0 ? nsm : 1) * 8;
   void *args[] = {(void *)&p};
-  const void *fn = p.top_k <= 2   ? (const void *)combine_grad_kernel<2>
-                   : p.top_k <= 8 ? (const void *)combine_grad_kernel<8>
-                                  : (const void *)combine_grad_kernel<kMaxK>;
-  return launch_ex(fn, dim3(p.T < cap ? p.T : cap), dim3(kThreads), 0, stream, true, 1, args);
+  const bool warp = p.H <= 1024 && p.T > cap;  // fewer tokens: a CTA each, all at once
+  const void *fn = p.top_k <= 2   ? warp ? (const void *)combine_grad_kernel<2, true> : (const void *)combine_grad_kernel<2, false>
+                   : p.top_k <= 8 ? warp ? (const void *)combine_grad_kernel<8, true> : (const void *)combine_grad_kernel<8, false>
+                   : warp         ? (const void *)combine_grad_kernel<kMaxK, true>
+                                  : (const void *)combine_grad_kernel<kMaxK, false>;
+  const int blocks = warp ? (p.T + kThreads / 32 - 1) / (kThreads / 32) : p.T;
+  return launch_ex(fn, dim3(blocks < cap ? blocks : cap), dim3(kThreads), 0, stream, true, 1, args);
 }
 
 cudaError_t launch_combine(const CombineParams &p, cudaStream_t stream, bool pdl) {
