@@ -98,8 +98,8 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineParams p
   }
 }
 
-// Gradients of the combine.  A CTA per token, or (WARP: rows of at most 1024 values,
-// which would leave most of a CTA idle) a warp: its row of grad_out against the rows of
+// Gradients of the combine.  A CTA per token, or (WARP: rows of at most 2048 values,
+// which leave much of a CTA idle) a warp: its row of grad_out against the rows of
 // its slots, 8 values a thread step; the sums over H are added in a fixed order.  HBM-bound: K slots' loads in flight together (8 for top-8 and fewer:
 // Hy3 T = 4096, 571 MB, 98 us, 5.8 TB/s, against 121 one slot at a time), then their
 // stores.
@@ -193,7 +193,9 @@ cudaError_t launch_combine_grad(const CombineGradParams &p, cudaStream_t stream)
   }
   const int cap = (nsm > 0 ? nsm : 1) * 8;
   void *args[] = {(void *)&p};
-  const bool warp = p.H <= 1024 && p.T > cap;  // fewer tokens: a CTA each, all at once
+  // H = 2048: 16384 tokens, top-8, 183 us with a warp a token, 213 with a CTA; H = 4096,
+  // 4096 tokens, top-8, 114 and 98.  Fewer tokens than CTAs: a CTA each, all at once.
+  const bool warp = p.H <= 2048 && p.T > cap;
   const void *fn = p.top_k <= 2   ? warp ? (const void *)combine_grad_kernel<2, true> : (const void *)combine_grad_kernel<2, false>
                    : p.top_k <= 8 ? warp ? (const void *)combine_grad_kernel<8, true> : (const void *)combine_grad_kernel<8, false>
                    : warp         ? (const void *)combine_grad_kernel<kMaxK, true>

@@ -314,7 +314,7 @@ def test_wide_ranges_of_gradients():
 
 
 COMBINE = [dict(T=1, H=64, k=1), dict(T=13, H=1088, k=6), dict(T=3, H=16384, k=16), dict(T=700, H=192, k=2),
-           dict(T=2500, H=128, k=8), dict(T=5, H=4096, k=8), dict(T=9, H=2112, k=7), dict(T=1300, H=1024, k=16), dict(T=9001, H=64, k=1), dict(T=1250, H=1088, k=3)]
+           dict(T=2500, H=128, k=8), dict(T=5, H=4096, k=8), dict(T=9, H=2112, k=7), dict(T=1300, H=1024, k=16), dict(T=9001, H=64, k=1), dict(T=1250, H=1088, k=3), dict(T=1301, H=2048, k=2)]
 
 
 @pytest.mark.parametrize("c", COMBINE, ids=IDS)
@@ -330,9 +330,9 @@ def test_combine_backward(c):
     moe.moe_combine_backward(d, g, y, inv, w, gw, gy)
     rows = y.double()[inv.long()].view(T, k, H)
     want, mag = (rows * g.double()[:, None]).sum(-1), (rows * g.double()[:, None]).abs().sum(-1)
-    # a thread adds 8 ceil(H / 2048) products at most, or where a warp has a row of at most 1024 values 32, then 13
-    # sums follow
-    steps = max(8 * ((H + 2047) // 2048), 32 if H <= 1024 else 0) + 16
+    # a thread adds 8 ceil(H / 2048) products at most, or where a warp has a row of at most 2048 values 8 ceil(H / 256),
+    # then 13 sums follow
+    steps = 8 * ((H + 255) // 256 if H <= 2048 else (H + 2047) // 2048) + 16
     assert ((gw.double() - want).abs() <= steps * U * mag).all()
     expect = torch.empty_like(y)
     expect[inv.long()] = (w[..., None] * g.float()[:, None]).bfloat16().view(T * k, H)
