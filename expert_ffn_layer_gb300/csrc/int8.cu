@@ -180,7 +180,7 @@ cudaError_t launch_rows(const __nv_bfloat16 *src, void *codes, float *scales, lo
   }
   return launch_ex(cols <= 1024   ? (const void *)int8_rows_kernel<F16, 4>
                    : cols <= 2048 ? (const void *)int8_rows_kernel<F16, 8>
-                                  : (const void *)int8_rows_kernel<F16, 0>,
+                                  : (const void *)int8_rows_kernel<false, 0>,  // no hidden state is this wide
                    dim3(row_blocks(rows)), dim3(kThreads), 0, stream, true, 1, args);
 }
 }  // namespace

@@ -84,7 +84,8 @@ def test_quantizer_every_ratio(shift):
     assert np.array_equal(scales.cpu().numpy(), top / np.float32(127))
 
 
-@pytest.mark.parametrize("shape", [(1, 8), (3, 24), (37, 520), (5, 16384), (2, 3, 64)], ids=str)
+@pytest.mark.parametrize("shape", [(1, 8), (3, 24), (37, 520), (7, 2048), (3, 2056), (1300, 4096), (5, 16384), (3, 20008), (2, 3, 64)],
+                         ids=str)
 def test_quantizer_shapes_and_values(shape):
     src = bf16_dev(W.normal_bf16(2, 51, shape, 0.02))
     codes, scales = quantized(src)
