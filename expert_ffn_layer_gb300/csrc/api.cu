@@ -1015,10 +1015,11 @@ MOE_API moe_status moe_route_backward(const moe_dims *d, const moe_bf16 *hidden,
   if (grad_hidden != nullptr || grad_router_w != nullptr) {
     p.pieces = at<uint16_t>(ws, L.pieces);
     p.w_pieces = at<uint16_t>(ws, L.w_pieces);
-    bool ok = map_bf16_3d(&p.map_dl_k, p.pieces, p.Epad, d->T, 3, 128) &&
-              map_bf16_3d(&p.map_dl_mn, p.pieces, p.Epad, d->T, 3, 64);
-    if (grad_hidden != nullptr) ok = ok && map_bf16_3d(&p.map_w, p.w_pieces, d->H, d->E, 2, 64);
-    if (grad_router_w != nullptr) ok = ok && map_bf16_2d(&p.map_x, hidden, d->H, d->T, 64);
+    bool ok = true;
+    if (grad_hidden != nullptr && d->T > kFewTokens)
+      ok = map_bf16_3d(&p.map_dl_k, p.pieces, p.Epad, d->T, 3, 128) && map_bf16_3d(&p.map_w, p.w_pieces, d->H, d->E, 2, 64);
+    if (grad_router_w != nullptr && d->T > kFewTokens)
+      ok = ok && map_bf16_3d(&p.map_dl_mn, p.pieces, p.Epad, d->T, 3, 64) && map_bf16_2d(&p.map_x, hidden, d->H, d->T, 64);
     if (!ok) return MOE_ERR_CUDA;
   }
   p.hidden = reinterpret_cast<const __nv_bfloat16 *>(hidden);

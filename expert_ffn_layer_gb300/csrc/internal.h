@@ -187,6 +187,7 @@ struct RouteGradParams {
   int T, H, E, top_k, n_seq, sigmoid;
   float route_scale, renorm_eps;
 };
+constexpr int kFewTokens = 16;  // with a product wanted: one kernel, which uses no map
 cudaError_t launch_route_grad(RouteGradParams p, int num_sms, cudaStream_t stream);
 
 // ------------------------------------------------------------------- FP8

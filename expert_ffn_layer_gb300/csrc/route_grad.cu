@@ -194,7 +194,6 @@ __global__ void __launch_bounds__(kThreads) grad_logits_kernel(const __grid_cons
 // fp32.  The products are a read and a write of the router weight's size (Hy3's
 // router, T = 8: 6.4 MB, 12 us as against 22 in three kernels, most of it the launch
 // and the chain of loads).
-constexpr int kFewTokens = 16;
 template <bool SIGMOID>
 __global__ void __launch_bounds__(kThreads) grad_few_kernel(const __grid_constant__ RouteGradParams p) {
   __shared__ int sh[2];
